@@ -473,6 +473,111 @@ pdq_status pdq_linear_int8_outlier_noalloc(const void* x, pdq_dtype dt, int64_t 
                                            int32_t* outlier_idx, int32_t* n_outlier, int64_t max_outliers,
                                            int32_t* acc_out, void* stream);
 
+/*
+ * The INT8 key/value cache: what stands between the projection that makes a
+ * decoder block's queries, keys and values and the projection that takes the
+ * attention's output.  The codes are the layer's absmax codes (S = C / 127, q =
+ * clamp(rne(x / S), -127, 127)) with one scale for each page of tokens and head.
+ *
+ * pdq_kv_cache: a pool of pages (host struct of device pointers, read during the
+ * call only).
+ *   k        int8 [pages, heads, page, dim]
+ *   v        int8 [pages, heads, page / 4, dim, 4]: four consecutive tokens of a
+ *            channel lie together, as the attention's value product takes them
+ *   k_scale, v_scale   float [pages, heads]
+ *   pages    0 .. 2^31 - 1; heads 1 .. 256 key/value heads; page 16, 32, 64, 128
+ *            or 256 tokens; dim 64, 128 or 256 channels of a head
+ * pdq_kv_batch: the sequences of a call (host struct of device pointers).
+ *   page_table  int32 [batch, max_pages], row pitch ldt: the pages of a sequence
+ *               in the order of its tokens (those beyond its length are not read)
+ *   seq_len     int32 [batch]: the sequence's tokens, the call's new ones included
+ *   cu_q        int32 [batch + 1], ascending: rows cu_q[s] .. cu_q[s + 1] - 1
+ *               are the new tokens of sequence s, its last ones; NULL: one row for
+ *               each sequence (tokens == batch)
+ *   batch       0 .. 65536; max_pages * page at most 2^30
+ * The position of row t of sequence s is seq_len[s] - (cu_q[s + 1] - t).
+ *
+ * What the device arrays hold cannot be refused.  A page number outside the pool
+ * is never followed: its tokens are not written and no row sees them.  Tokens at
+ * negative positions or beyond max_pages * page are not written.  Rows before
+ * cu_q[0] and from cu_q[batch] on belong to no sequence: their outputs stay as
+ * they were.
+ */
+typedef struct pdq_kv_cache {
+    int8_t* k;
+    int8_t* v;
+    float* k_scale;
+    float* v_scale;
+    int64_t pages;
+    int32_t heads, page, dim;
+} pdq_kv_cache;
+
+typedef struct pdq_kv_batch {
+    const int32_t* page_table;
+    int64_t ldt;
+    const int32_t* seq_len;
+    const int32_t* cu_q;
+    int32_t batch, max_pages;
+} pdq_kv_batch;
+
+/*
+ * Appends the new tokens' keys and values, after rotating the keys (and the
+ * queries, for pdq_kv_attention) by their positions.
+ *
+ *   k, v     [tokens, heads, dim] of dt (BF16 or F16), row pitches ldk, ldv, the
+ *            heads of a row side by side (e.g. columns of the projection's output)
+ *   q        [tokens, hq, dim] of dt, row pitch ldq, or NULL; q_out likewise, row
+ *            pitch ldqo: q rotated, rounded to dt (must not overlap q)
+ *   cos, sin float [positions, rot / 2] or both NULL (no rotation; rot is ignored,
+ *            q must be NULL): the first rot channels of a head are rotated,
+ *            (a, b) -> (a cos - b sin, b cos + a sin) with a, b the channels
+ *            (j, j + rot / 2), or (2 j, 2 j + 1) with interleaved != 0; every
+ *            operation rounded to binary32.  rot: a multiple of 16, 16 .. dim.
+ *            At a position outside the tables the rotated channels are NaN.
+ *   A page with new tokens x (rotated keys; values) takes, for each head,
+ *            S_new = max(S_old, C / 127, 2^-64), C the largest |x| among them,
+ *            S_old = 0 if the page held no earlier token of the sequence;
+ *            q = clamp(rne(x / S_new), -127, 127); where S_new > S_old the codes of
+ *            its earlier tokens become rne(code * fl(S_old / S_new)), so that one
+ *            scale holds for the page.  If some x (or S_old) is not finite, S_new
+ *            is NaN and the new codes are 0: every row that sees the page is NaN.
+ *   A page that a call writes must be named by one sequence only, at one place.
+ */
+pdq_status pdq_kv_append(const void* k, const void* v, const void* q, pdq_dtype dt, int64_t tokens,
+                         int64_t hq, int64_t ldk, int64_t ldv, int64_t ldq, const float* cos, const float* sin,
+                         int64_t positions, int64_t rot, int interleaved, const pdq_kv_cache* cache,
+                         const pdq_kv_batch* batch, void* q_out, int64_t ldqo, void* stream);
+
+/*
+ * Attention of the new rows over the cache (which already holds them).
+ *
+ *   q        [tokens, hq, dim] of dt (BF16 or F16), row pitch ldq; hq a multiple of
+ *            the cache's heads (query head h reads key/value head h / (hq / heads))
+ *   scores   z = scale * S_k[page] * (q . codes), then z = softcap * tanh(z /
+ *            softcap) if softcap > 0, then z += slopes[h] * (key - row) positions
+ *            if slopes (float [hq]) is not NULL
+ *   mask     a row at position p sees the keys
+ *            max(0, p - window + 1) (0 if window == 0) .. min(max(p, prefix[s] - 1),
+ *            seq_len[s] - 1); prefix (int32 [batch], or NULL: causal) makes the
+ *            first prefix[s] tokens visible to every row (INT32_MAX: all tokens)
+ *   y        [tokens, hq, dim] of dt out, row pitch ldy: softmax(z) V.  A row that
+ *            sees nothing gets 0.
+ *   lse      float [tokens, hq] out or NULL: ln sum exp z (-INF for such a row)
+ *   workspace  device scratch of at least pdq_kv_attention_workspace(tokens, batch,
+ *            hq, heads, dim) bytes, 256-byte aligned; its contents on entry do not
+ *            matter and nothing in it carries over; calls that overlap in time
+ *            (other streams, other graphs) need one each
+ * Scores, the softmax's maximum and sum and both products are held in binary32; a
+ * weight of the softmax is rounded to binary16 (11 bits) for the product with the
+ * value codes.  Scales must be at least 2^-64 in magnitude (pdq_kv_append's are).
+ */
+size_t pdq_kv_attention_workspace(int64_t tokens, int64_t batch, int64_t hq, int64_t heads, int64_t dim);
+
+pdq_status pdq_kv_attention(const void* q, pdq_dtype dt, int64_t tokens, int64_t hq, int64_t ldq,
+                            const pdq_kv_cache* cache, const pdq_kv_batch* batch, float scale, float softcap,
+                            int64_t window, const float* slopes, const int32_t* prefix, void* y, int64_t ldy,
+                            float* lse, void* workspace, size_t workspace_bytes, void* stream);
+
 #ifdef __cplusplus
 }
 #endif

@@ -1,0 +1,77 @@
+// What the kernels of the INT8 key/value cache share: the cache's layout, where
+// a sequence's new tokens lie, which rows a work item is.
+#pragma once
+
+#include "pdq_device.h"
+#include "pdq_kernels.h"
+
+namespace pdq {
+
+// One sequence of the batch as the kernels see it.  What the device arrays hold
+// cannot be checked on the host: new rows are clamped to [0, tokens), so that
+// no value of cu_q reaches outside q, k, v.
+struct KvSeq {
+    int q0, n;  // first new row, new rows
+    int len;    // tokens after the call, as given
+    int p0;     // position of the first new row: len - n (may be negative)
+};
+
+__device__ __forceinline__ KvSeq kv_seq(const KvBatch& b, int s) {
+    KvSeq r;
+    if (b.cu_q) {
+        r.q0 = min(max(b.cu_q[s], 0), b.tokens);
+        r.n = min(max(b.cu_q[s + 1], r.q0), b.tokens) - r.q0;
+    } else {
+        r.q0 = s;
+        r.n = 1;
+    }
+    // lengths outside [0, 2^30] count as the nearer of the two: positions and their differences stay in int32
+    r.len = min(max(b.seq_len[s], 0), 1 << 30);
+    r.p0 = r.len - r.n;
+    return r;
+}
+
+// Work items of a sequence are numbered without a prefix sum: those of sequence
+// s begin at floor(cu_q[s] * mul / per) + extra * s.  floor(a + b) >= floor(a) +
+// floor(b), so a sequence of n rows has room for floor(n * mul / per) + extra
+// items.  item_seq finds the sequence of item w (the last one that begins at or
+// before it): 64 candidates a step, one step for up to 64 sequences.  The whole
+// wavefront calls it with the same w.
+__device__ __forceinline__ int64_t item_start(const KvBatch& b, int s, int mul, int per, int extra) {
+    const int q0 = b.cu_q ? min(max(b.cu_q[s], 0), b.tokens) : s;
+    return (int64_t)q0 * mul / per + (int64_t)extra * s;
+}
+
+__device__ __forceinline__ int item_seq(const KvBatch& b, int64_t w, int mul, int per, int extra) {
+    const int lane = threadIdx.x & 63;
+    int lo = 0, n = b.batch;
+    while (n > 1) {
+        const int step = (n + 63) / 64;
+        const int i = lo + lane * step;
+        const bool in = lane * step < n && item_start(b, i, mul, per, extra) <= w;
+        const int k = max(__popcll(__ballot(in)), 1) - 1;
+        lo += k * step;
+        n = min(step, n - k * step);
+    }
+    return __builtin_amdgcn_readfirstlane(lo);
+}
+
+// The sequence of row t, by one thread.
+__device__ __forceinline__ int row_seq(const KvBatch& b, int t) {
+    if (!b.cu_q) return t;
+    int lo = 0, hi = b.batch;  // the last s with cu_q[s] <= t
+    while (hi - lo > 1) {
+        const int mid = (lo + hi) >> 1;
+        if (b.cu_q[mid] <= t) lo = mid;
+        else hi = mid;
+    }
+    return lo;
+}
+
+// A page's number, or -1 where the table names none of the pool.
+__device__ __forceinline__ int kv_page(const KvCache& c, const KvBatch& b, int s, int j) {
+    const int id = b.page_table[(int64_t)s * b.ldt + j];
+    return (uint32_t)id < (uint32_t)c.pages ? id : -1;
+}
+
+}  // namespace pdq

@@ -756,3 +756,126 @@ pdq_status pdq_linear_int8_outlier_noalloc(const void* x, pdq_dtype dt, int64_t 
 }
 
 }  // extern "C"
+
+namespace {
+
+constexpr int64_t kMaxBatch = 65536, kMaxHeads = 256, kMaxSeq = int64_t(1) << 30;
+constexpr int64_t kMaxThreads = int64_t(1) << 31;  // of one launch
+
+// The checks that the two cache calls share; fills the kernels' views.
+pdq_status check_kv(const pdq_kv_cache* cache, const pdq_kv_batch* batch, int64_t tokens, KvCache* c, KvBatch* b) {
+    if (!cache || !batch) return PDQ_ERR_NULL;
+    if (cache->pages < 0 || cache->pages > INT32_MAX || cache->heads < 1 || cache->heads > kMaxHeads) return PDQ_ERR_SHAPE;
+    if (cache->page != 16 && cache->page != 32 && cache->page != 64 && cache->page != 128 && cache->page != 256)
+        return PDQ_ERR_SHAPE;
+    if (cache->dim != 64 && cache->dim != 128 && cache->dim != 256) return PDQ_ERR_SHAPE;
+    if (tokens < 0 || tokens > kMaxRows || batch->batch < 0 || batch->batch > kMaxBatch) return PDQ_ERR_SHAPE;
+    if (batch->max_pages < 0 || (int64_t)batch->max_pages * cache->page > kMaxSeq || batch->ldt < batch->max_pages)
+        return PDQ_ERR_SHAPE;
+    if (!batch->cu_q && tokens != batch->batch) return PDQ_ERR_SHAPE;
+    if (cache->pages > 0 && (!cache->k || !cache->v || !cache->k_scale || !cache->v_scale)) return PDQ_ERR_NULL;
+    if (batch->batch > 0 && (!batch->seq_len || (batch->max_pages > 0 && !batch->page_table))) return PDQ_ERR_NULL;
+    if (!aligned(cache->k, 16) || !aligned(cache->v, 16) || !aligned(cache->k_scale, 4) ||
+        !aligned(cache->v_scale, 4) || !aligned(batch->page_table, 4) || !aligned(batch->seq_len, 4) ||
+        !aligned(batch->cu_q, 4))
+        return PDQ_ERR_ALIGN;
+    *c = KvCache{cache->k, cache->v, cache->k_scale, cache->v_scale, (int)cache->pages, cache->heads, cache->page,
+                 cache->dim};
+    *b = KvBatch{batch->page_table, batch->ldt, batch->seq_len, batch->cu_q, batch->batch, batch->max_pages,
+                 (int)tokens};
+    return PDQ_OK;
+}
+
+// A [rows, heads, dim] operand of 16-bit values.
+pdq_status check_rows(const void* p, int64_t rows, int64_t heads, int64_t dim, int64_t ld) {
+    if (rows * heads > kMaxValues / dim || ld < heads * dim || ld > kMaxValues) return PDQ_ERR_SHAPE;
+    if (rows > 0 && !p) return PDQ_ERR_NULL;
+    if (!aligned(p, 16) || ld % 8 != 0) return PDQ_ERR_ALIGN;
+    return PDQ_OK;
+}
+
+}  // namespace
+
+extern "C" {
+
+pdq_status pdq_kv_append(const void* k, const void* v, const void* q, pdq_dtype dt, int64_t tokens,
+                         int64_t hq, int64_t ldk, int64_t ldv, int64_t ldq, const float* cos, const float* sin,
+                         int64_t positions, int64_t rot, int interleaved, const pdq_kv_cache* cache,
+                         const pdq_kv_batch* batch, void* q_out, int64_t ldqo, void* stream) {
+    if (dt != PDQ_BF16 && dt != PDQ_F16) return PDQ_ERR_DTYPE;
+    KvAppendArgs a{};
+    PDQ_TRY(check_kv(cache, batch, tokens, &a.c, &a.b));
+    PDQ_TRY(check_rows(k, tokens, a.c.heads, a.c.dim, ldk));
+    PDQ_TRY(check_rows(v, tokens, a.c.heads, a.c.dim, ldv));
+    if (!cos != !sin || (q && !cos) || (q && tokens > 0 && !q_out)) return PDQ_ERR_NULL;
+    if (q) {
+        if (hq < 1 || hq > kMaxHeads * 64) return PDQ_ERR_SHAPE;
+        PDQ_TRY(check_rows(q, tokens, hq, a.c.dim, ldq));
+        PDQ_TRY(check_rows(q_out, tokens, hq, a.c.dim, ldqo));
+    }
+    if (cos) {
+        if (positions < 1 || positions > kMaxSeq || rot < 16 || rot > a.c.dim || rot % 16 != 0) return PDQ_ERR_SHAPE;
+        if (!aligned(cos, 16) || !aligned(sin, 16)) return PDQ_ERR_ALIGN;
+    }
+    a.k = k;
+    a.v = v;
+    a.q = q;
+    a.q_out = q_out;
+    a.ldk = ldk;
+    a.ldv = ldv;
+    a.ldq = ldq;
+    a.ldqo = ldqo;
+    a.cos = cos;
+    a.sin = sin;
+    a.positions = (int)positions;
+    a.rot = (int)rot;
+    a.interleaved = interleaved != 0;
+    a.hq = q ? (int)hq : 1;
+    if (kv_append_threads(a) > kMaxThreads) return PDQ_ERR_SHAPE;
+    if (tokens == 0 || a.b.batch == 0) return PDQ_OK;
+    launch_kv_append(a, dt, static_cast<hipStream_t>(stream));
+    return launched();
+}
+
+size_t pdq_kv_attention_workspace(int64_t tokens, int64_t batch, int64_t hq, int64_t heads, int64_t dim) {
+    if (tokens < 1 || batch < 1 || heads < 1 || heads > kMaxHeads || hq < heads || hq > kMaxHeads * 64 ||
+        hq % heads != 0 || dim < 1 || tokens > kMaxRows || batch > kMaxBatch)
+        return 0;
+    return align256(attention_workspace(tokens, batch, (int)hq, (int)heads, (int)dim));
+}
+
+pdq_status pdq_kv_attention(const void* q, pdq_dtype dt, int64_t tokens, int64_t hq, int64_t ldq,
+                            const pdq_kv_cache* cache, const pdq_kv_batch* batch, float scale, float softcap,
+                            int64_t window, const float* slopes, const int32_t* prefix, void* y, int64_t ldy,
+                            float* lse, void* workspace, size_t workspace_bytes, void* stream) {
+    if (dt != PDQ_BF16 && dt != PDQ_F16) return PDQ_ERR_DTYPE;
+    AttentionArgs a{};
+    PDQ_TRY(check_kv(cache, batch, tokens, &a.c, &a.b));
+    if (hq < a.c.heads || hq > kMaxHeads * 64 || hq % a.c.heads != 0 || window < 0 || window > INT32_MAX)
+        return PDQ_ERR_SHAPE;
+    PDQ_TRY(check_rows(q, tokens, hq, a.c.dim, ldq));
+    PDQ_TRY(check_rows(y, tokens, hq, a.c.dim, ldy));
+    if (!isfinite(scale) || !isfinite(softcap) || softcap < 0.0f) return PDQ_ERR_UNSUPPORTED;
+    if (!aligned(slopes, 4) || !aligned(prefix, 4) || !aligned(lse, 4)) return PDQ_ERR_ALIGN;
+    const size_t need = pdq_kv_attention_workspace(tokens, a.b.batch, hq, a.c.heads, a.c.dim);
+    if (need > 0 && (!workspace || workspace_bytes < need)) return PDQ_ERR_WORKSPACE;
+    if (!aligned(workspace, 256)) return PDQ_ERR_ALIGN;
+    a.q = q;
+    a.y = y;
+    a.lse = lse;
+    a.ldq = ldq;
+    a.ldy = ldy;
+    a.hq = (int)hq;
+    a.scale = scale;
+    a.softcap = softcap;
+    a.window = (int)window;
+    a.slopes = slopes;
+    a.prefix = prefix;
+    a.ws = static_cast<float*>(workspace);
+    if (attention_threads(a) > kMaxThreads) return PDQ_ERR_SHAPE;
+    if (tokens == 0 || a.b.batch == 0) return PDQ_OK;
+    launch_attention(a, dt, static_cast<hipStream_t>(stream));
+    return launched();
+}
+
+}  // extern "C"

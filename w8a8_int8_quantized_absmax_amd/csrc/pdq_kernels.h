@@ -144,4 +144,56 @@ void launch_outlier_partial(const void* x, int dt, int64_t M, int64_t K, int64_t
 void launch_outlier_index(const uint8_t* partial, int64_t M, int64_t K, uint8_t* mask, int32_t* idx,
                           int32_t* count, int64_t max_out, hipStream_t st);
 
+// kv_append.hip, attention.hip -------------------------------------------
+// The paged INT8 key/value cache: k [pages, heads, page, dim], v [pages, heads,
+// page / 4, dim, 4] (four consecutive tokens of one channel lie together, as a
+// lane of the attention's value product takes them), one scale for each page
+// and head.
+struct KvCache {
+    int8_t* k;
+    int8_t* v;
+    float* k_scale;  // [pages, heads]
+    float* v_scale;
+    int pages, heads, page, dim;
+};
+struct KvBatch {
+    const int32_t* page_table;  // [batch, max_pages], row pitch ldt
+    int64_t ldt;
+    const int32_t* seq_len;  // [batch]
+    const int32_t* cu_q;     // [batch + 1], or null: one new row a sequence
+    int batch, max_pages, tokens;
+};
+struct KvAppendArgs {
+    KvCache c;
+    KvBatch b;
+    const void* k;
+    const void* v;
+    const void* q;  // null: no queries
+    void* q_out;
+    int64_t ldk, ldv, ldq, ldqo;
+    const float* cos;  // [positions, rot / 2], null: no rotation
+    const float* sin;
+    int positions, rot, interleaved, hq;
+};
+int64_t kv_append_threads(const KvAppendArgs& a);  // of its launch
+void launch_kv_append(const KvAppendArgs& a, int dt, hipStream_t st);
+
+struct AttentionArgs {
+    KvCache c;
+    KvBatch b;
+    const void* q;
+    void* y;
+    float* lse;  // [tokens, hq] or null
+    int64_t ldq, ldy;
+    int hq;
+    float scale, softcap;  // softcap 0: none
+    int window;            // 0: none
+    const float* slopes;   // [hq] or null
+    const int32_t* prefix; // [batch] or null
+    float* ws;
+};
+size_t attention_workspace(int64_t tokens, int64_t batch, int hq, int hkv, int dim);
+int64_t attention_threads(const AttentionArgs& a);  // of its largest launch
+void launch_attention(const AttentionArgs& a, int dt, hipStream_t st);
+
 }  // namespace pdq

@@ -8,6 +8,7 @@ is raised.
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import os
 import re
@@ -70,6 +71,11 @@ SIGNATURES = {
     "pdq_linear_int8_outlier_noalloc": (ctypes.c_int, [_vp, ctypes.c_int, _i64, _i64, _i64, _f32, _vp, _vp,
                                                        _vp, _i64, _vp, _i64, _vp, _i64, _vp, _vp, _vp, _vp,
                                                        _i64, _vp, _vp]),
+    "pdq_kv_append": (ctypes.c_int, [_vp, _vp, _vp, ctypes.c_int, _i64, _i64, _i64, _i64, _i64, _vp, _vp, _i64, _i64,
+                                     ctypes.c_int, _vp, _vp, _vp, _i64, _vp]),
+    "pdq_kv_attention_workspace": (_sz, [_i64, _i64, _i64, _i64, _i64]),
+    "pdq_kv_attention": (ctypes.c_int, [_vp, ctypes.c_int, _i64, _i64, _i64, _vp, _vp, _f32, _f32, _i64, _vp, _vp,
+                                        _vp, _i64, _vp, _vp, _sz, _vp]),
 }
 
 _lib = None
@@ -569,3 +575,200 @@ def gemm_static(xq, a_scale: float, a_zp: int, wq, w_scale, colsum, bias=None, w
     _call("pdq_gemm_static", _p(xq), m, k, float(a_scale), int(a_zp), _p(wq), _p(w_scale), _p(colsum),
           _p(bias), n, _p(y), _ld(y), _p(acc), _stream(dev))
     return dict(y=y, acc=acc)
+
+
+# ---- the INT8 key/value cache ---------------------------------------------
+
+class _KVCacheC(ctypes.Structure):
+    _fields_ = [("k", _vp), ("v", _vp), ("k_scale", _vp), ("v_scale", _vp), ("pages", _i64), ("heads", _i32),
+                ("page", _i32), ("dim", _i32)]
+
+
+class _KVBatchC(ctypes.Structure):
+    _fields_ = [("page_table", _vp), ("ldt", _i64), ("seq_len", _vp), ("cu_q", _vp), ("batch", _i32),
+                ("max_pages", _i32)]
+
+
+def _check_dense(t, name, dtype, shape=None):
+    if not t.is_cuda or t.dtype != dtype or not t.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous {dtype} device tensor")
+    if shape is not None and tuple(t.shape) != tuple(shape):
+        raise ValueError(f"{name} has shape {tuple(t.shape)}, {tuple(shape)} needed")
+
+
+class KVCache:
+    """A pool of pages of the INT8 key/value cache (include/pdq.h, pdq_kv_cache).
+
+    k [pages, heads, page, dim] and v [pages, heads, page / 4, dim, 4] int8,
+    k_scale and v_scale [pages, heads] float32, all contiguous on one device.
+    """
+
+    __slots__ = ("k", "v", "k_scale", "v_scale", "pages", "heads", "page", "dim", "device", "_c", "_ref")
+
+    def __init__(self, k: torch.Tensor, v: torch.Tensor, k_scale: torch.Tensor, v_scale: torch.Tensor):
+        if k.dim() != 4:
+            raise ValueError("k must be [pages, heads, page, dim]")
+        pages, heads, page, dim = k.shape
+        _check_dense(k, "k", torch.int8)
+        _check_dense(v, "v", torch.int8, (pages, heads, page // 4, dim, 4))
+        _check_dense(k_scale, "k_scale", torch.float32, (pages, heads))
+        _check_dense(v_scale, "v_scale", torch.float32, (pages, heads))
+        if not k.device == v.device == k_scale.device == v_scale.device:
+            raise ValueError("the cache's tensors must be on one device")
+        self.k, self.v, self.k_scale, self.v_scale = k, v, k_scale, v_scale
+        self.pages, self.heads, self.page, self.dim, self.device = pages, heads, page, dim, k.device
+        self._c = _KVCacheC(k.data_ptr(), v.data_ptr(), k_scale.data_ptr(), v_scale.data_ptr(), pages, heads, page, dim)
+        self._ref = ctypes.byref(self._c)
+
+    @classmethod
+    def empty(cls, pages: int, heads: int, dim: int, page: int = 64, device="cuda") -> "KVCache":
+        return cls(torch.empty((pages, heads, page, dim), dtype=torch.int8, device=device),
+                   torch.empty((pages, heads, page // 4, dim, 4), dtype=torch.int8, device=device),
+                   torch.empty((pages, heads), dtype=torch.float32, device=device),
+                   torch.empty((pages, heads), dtype=torch.float32, device=device))
+
+
+class KVBatch:
+    """The sequences of a call (include/pdq.h, pdq_kv_batch): page_table int32
+    [batch, max_pages], seq_len int32 [batch] (the new tokens included), cu_q int32
+    [batch + 1] row offsets of the new tokens, or None: one row a sequence.  The
+    tensors are read when the calls run on the device, so that a program may
+    update them in place between calls (or between replays of a graph)."""
+
+    __slots__ = ("page_table", "seq_len", "cu_q", "batch", "device", "_c", "_ref")
+
+    def __init__(self, page_table: torch.Tensor, seq_len: torch.Tensor, cu_q: torch.Tensor | None = None):
+        _check_mat(page_table, "page_table", (torch.int32,))
+        batch, max_pages = page_table.shape
+        _check_dense(seq_len, "seq_len", torch.int32, (batch,))
+        if cu_q is not None:
+            _check_dense(cu_q, "cu_q", torch.int32, (batch + 1,))
+        if page_table.device != seq_len.device or (cu_q is not None and cu_q.device != seq_len.device):
+            raise ValueError("the batch's tensors must be on one device")
+        self.page_table, self.seq_len, self.cu_q, self.batch = page_table, seq_len, cu_q, batch
+        self.device = seq_len.device
+        self._c = _KVBatchC(page_table.data_ptr(), _ld(page_table), seq_len.data_ptr(),
+                            cu_q.data_ptr() if cu_q is not None else None, batch, max_pages)
+        self._ref = ctypes.byref(self._c)
+
+
+def _check_kv_rows(t, name, cache, batch, heads=None, dtype=None):
+    """A [tokens, heads, dim] operand, the heads of a row side by side -> its row pitch."""
+    if t.device != cache.device or t.device != batch.device:
+        raise ValueError(f"{name}, the cache and the batch must be on one device")
+    if t.dtype not in _HALF or (dtype is not None and t.dtype != dtype):
+        raise ValueError(f"{name}: unsupported dtype {t.dtype}")
+    shape = t.shape
+    if len(shape) != 3 or shape[2] != cache.dim or (heads is not None and shape[1] != heads):
+        raise ValueError(f"{name} of shape {tuple(shape)} given, [tokens, "
+                         f"{heads if heads is not None else 'heads'}, {cache.dim}] needed")
+    rows, stride = shape[0], t.stride()
+    if rows and (stride[2] != 1 or (shape[1] > 1 and stride[1] != cache.dim)):
+        raise ValueError(f"{name}: the heads of a row must lie side by side")
+    return stride[0] if rows > 1 else shape[1] * shape[2]
+
+
+def _on(device):
+    """The device's current stream, with the device current (its kernels are launched there)."""
+    if device.index is not None and device.index != torch.cuda.current_device():
+        return torch.cuda.device(device)
+    return contextlib.nullcontext()
+
+
+def kv_append(k, v, cache: KVCache, batch: KVBatch, q=None, cos=None, sin=None, interleaved: bool = False,
+              q_out=None):
+    """Rotates k (and q) by position, codes k and v with one scale a page and head,
+    and writes them into the cache -> the rotated q (None without q).
+
+    k, v: [tokens, heads, dim] bf16 or f16; q: [tokens, hq, dim]; cos, sin: float32
+    [positions, rot / 2] (None: no rotation)."""
+    ldk = _check_kv_rows(k, "k", cache, batch, cache.heads)
+    tokens, dtype = k.shape[0], k.dtype
+    ldv = _check_kv_rows(v, "v", cache, batch, cache.heads, dtype)
+    if v.shape[0] != tokens:
+        raise ValueError("k and v must have the same rows")
+    if (cos is None) != (sin is None) or (q is not None and cos is None):
+        raise ValueError("a rotation needs both tables, and q is there to be rotated")
+    positions = rot = hq = ldq = ldqo = 0
+    if cos is not None:
+        _check_dense(cos, "cos", torch.float32)
+        _check_dense(sin, "sin", torch.float32, cos.shape)
+        if cos.dim() != 2 or cos.device != k.device or sin.device != k.device:
+            raise ValueError("cos and sin must be [positions, rot / 2] on k's device")
+        positions, rot = cos.shape[0], 2 * cos.shape[1]
+    if q is not None:
+        ldq = _check_kv_rows(q, "q", cache, batch, None, dtype)
+        if q.shape[0] != tokens:
+            raise ValueError("q and k must have the same rows")
+        hq = q.shape[1]
+        if q_out is None:
+            q_out = torch.empty((tokens, hq, cache.dim), dtype=dtype, device=k.device)
+            ldqo = hq * cache.dim
+        else:
+            ldqo = _check_kv_rows(q_out, "q_out", cache, batch, hq, dtype)
+            if q_out.shape[0] != tokens:
+                raise ValueError("q_out and q must have the same rows")
+    elif q_out is not None:
+        raise ValueError("q_out without q")
+    with _on(k.device):
+        _call("pdq_kv_append", k.data_ptr(), v.data_ptr(), q.data_ptr() if q is not None else None, _DT[dtype], tokens,
+              hq, ldk, ldv, ldq, cos.data_ptr() if cos is not None else None,
+              sin.data_ptr() if sin is not None else None, positions, rot, int(interleaved), cache._ref, batch._ref,
+              q_out.data_ptr() if q_out is not None else None, ldqo, torch.cuda.current_stream(k.device).cuda_stream)
+    return q_out
+
+
+def kv_attention_workspace_bytes(tokens: int, batch: int, hq: int, heads: int, dim: int) -> int:
+    return int(lib().pdq_kv_attention_workspace(tokens, batch, hq, heads, dim))
+
+
+def kv_attention(q, cache: KVCache, batch: KVBatch, scale: float | None = None, softcap: float = 0.0,
+                 window: int = 0, alibi_slopes=None, prefix_len=None, want_lse: bool = False, out=None, lse=None,
+                 workspace=None):
+    """Attention of the new rows q [tokens, hq, dim] over the cache -> dict(y of q's
+    shape and dtype, lse float32 [tokens, hq] or None).
+
+    scale: 1 / sqrt(dim) by default; softcap > 0: scores capped by softcap *
+    tanh(z / softcap); window > 0: the last window keys; alibi_slopes float32 [hq]:
+    a bias by distance; prefix_len int32 [batch]: tokens that every row sees."""
+    ldq = _check_kv_rows(q, "q", cache, batch)
+    tokens, hq, dim = q.shape
+    dev = q.device
+    if alibi_slopes is not None:
+        _check_dense(alibi_slopes, "alibi_slopes", torch.float32, (hq,))
+        if alibi_slopes.device != dev:
+            raise ValueError("alibi_slopes must be on q's device")
+    if prefix_len is not None:
+        _check_dense(prefix_len, "prefix_len", torch.int32, (batch.batch,))
+        if prefix_len.device != dev:
+            raise ValueError("prefix_len must be on q's device")
+    if out is None:
+        y = torch.empty((tokens, hq, dim), dtype=q.dtype, device=dev)
+        ldy = hq * dim
+    else:
+        y = out
+        ldy = _check_kv_rows(y, "out", cache, batch, hq, q.dtype)
+        if y.shape[0] != tokens:
+            raise ValueError("out and q must have the same rows")
+    if lse is not None:
+        _check_dense(lse, "lse", torch.float32, (tokens, hq))
+        if lse.device != dev:
+            raise ValueError("lse must be on q's device")
+    elif want_lse:
+        lse = torch.empty((tokens, hq), dtype=torch.float32, device=dev)
+    need = int(lib().pdq_kv_attention_workspace(tokens, batch.batch, hq, cache.heads, dim))
+    if workspace is None:
+        if need:
+            workspace = torch.empty(need, dtype=torch.uint8, device=dev)
+    else:
+        _check_dense(workspace, "workspace", torch.uint8)
+        if workspace.device != dev:
+            raise ValueError("workspace must be on q's device")
+    with _on(dev):
+        _call("pdq_kv_attention", q.data_ptr(), _DT[q.dtype], tokens, hq, ldq, cache._ref, batch._ref,
+              dim ** -0.5 if scale is None else float(scale), float(softcap), int(window),
+              alibi_slopes.data_ptr() if alibi_slopes is not None else None,
+              prefix_len.data_ptr() if prefix_len is not None else None, y.data_ptr(), ldy,
+              lse.data_ptr() if lse is not None else None, workspace.data_ptr() if workspace is not None else None,
+              workspace.numel() if workspace is not None else 0, torch.cuda.current_stream(dev).cuda_stream)
+    return dict(y=y, lse=lse)
