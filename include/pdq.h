@@ -476,8 +476,8 @@ pdq_status pdq_linear_int8_outlier_noalloc(const void* x, pdq_dtype dt, int64_t 
 /*
  * The INT8 key/value cache: what stands between the projection that makes a
  * decoder block's queries, keys and values and the projection that takes the
- * attention's output.  The codes are the layer's absmax codes (S = C / 127, q =
- * clamp(rne(x / S), -127, 127)) with one scale for each page of tokens and head.
+ * attention's output.  The codes are absmax codes, q = clamp(rne(x / S), -127, 127),
+ * with one scale S for each page of tokens and head.
  *
  * pdq_kv_cache: a pool of pages (host struct of device pointers, read during the
  * call only).
@@ -535,8 +535,9 @@ typedef struct pdq_kv_batch {
  *            operation rounded to binary32.  rot: a multiple of 16, 16 .. dim.
  *            At a position outside the tables the rotated channels are NaN.
  *   A page with new tokens x (rotated keys; values) takes, for each head,
- *            S_new = max(S_old, C / 127, 2^-64), C the largest |x| among them,
- *            S_old = 0 if the page held no earlier token of the sequence;
+ *            S_new = max(S_old, fl(C * fl(1 / 127)), 2^-64), C the largest |x| among
+ *            them (a binary32 product: within an ulp of C / 127), S_old = 0 if the
+ *            page held no earlier token of the sequence;
  *            q = clamp(rne(x / S_new), -127, 127); where S_new > S_old the codes of
  *            its earlier tokens become rne(code * fl(S_old / S_new)), so that one
  *            scale holds for the page.  If some x (or S_old) is not finite, S_new

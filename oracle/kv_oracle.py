@@ -72,7 +72,7 @@ def append(cache, table, seq_len, cu_q, k, v, q=None, cos=None, sin=None, interl
                         scale[p, h] = np.nan
                         codes[p, h, first:first + len(new)] = 0
                         continue
-                    now = max(held, max(np.abs(x).max() / F(127), MIN_SCALE))
+                    now = max(held, max(np.abs(x).max() * (F(1) / F(127)), MIN_SCALE))
                     if first > 0 and now > held:
                         codes[p, h, :first] = np.rint(codes[p, h, :first].astype(F) * (held / now))
                     codes[p, h, first:first + len(new)] = np.clip(np.rint(x / now), -127, 127)
