@@ -1,125 +1,551 @@
-// Attention over the paged INT8 key/value cache.  include/pdq.h
-// (pdq_kv_attention) states the arithmetic.
-#include "kv_device.h"
+// Attention over the paged INT8 key/value cache, few rows for each sequence
+// (decode; drafted tokens): bound by reading the cache.  include/pdq.h
+// (pdq_kv_attention) states the arithmetic, attention_device.h how it is taken.
+#include <algorithm>
+
+#include "attention_device.h"
 
 namespace pdq {
 
 namespace {
 
-constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
+constexpr int kStep = 128;  // tokens of a step: four waves of 32
 
-// One workgroup of four waves for each (row, query head): a wave takes groups of
-// 16 tokens in turn with its own running maximum and sum, and the four are
-// joined at the end.
-template <int DT, int D>
-__global__ __launch_bounds__(256) void k_attention_rows(AttentionArgs a) {
-    constexpr int DL = D / 4;   // channels of a lane in the score product
-    constexpr int DV = D / 64;  // channels of a lane in the value product
-    __shared__ float sm[4], sl[4], so[4][D];
-    const int t = blockIdx.x / a.hq, h = blockIdx.x % a.hq;
-    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, i = lane & 15, g = lane >> 4;
-    if (a.b.cu_q && (t < a.b.cu_q[0] || t >= a.b.cu_q[a.b.batch])) return;
-    const int s = row_seq(a.b, t);
-    const KvSeq q = kv_seq(a.b, s);
-    const int hk = h / (a.hq / a.c.heads);
-    const int pos = q.p0 + t - q.q0;
-    const int last = min(min(a.prefix ? max(pos, a.prefix[s] - 1) : pos, q.len - 1), a.b.max_pages * a.c.page - 1);
-    const int first = a.window ? max(pos - a.window + 1, 0) : 0;
-    float x[DL], o[DV] = {}, m = -INFINITY, l = 0.0f;
-    {
-        const uint16_t* row = reinterpret_cast<const uint16_t*>(a.q) + (int64_t)t * a.ldq + (int64_t)h * D + g * DL;
-#pragma unroll
-        for (int c = 0; c < DL / 8; ++c) {
-            float v[8];
-            widen8<DT>(load_raw8<DT>(row, c), v);
-#pragma unroll
-            for (int j = 0; j < 8; ++j) x[8 * c + j] = v[j];
-        }
-    }
-    for (int t0 = (first & ~15) + 16 * wave; t0 <= last; t0 += 64) {
-        const int id = kv_page(a.c, a.b, s, t0 / a.c.page);
-        if (id < 0) continue;
-        const int64_t at = (int64_t)id * a.c.heads + hk;
-        const int slot = t0 & (a.c.page - 1);
-        const int8_t* k = a.c.k + (at * a.c.page + slot + i) * D + g * DL;
-        float dot = 0.0f;
-#pragma unroll
-        for (int d = 0; d < DL; ++d) dot += x[d] * (float)k[d];
-        dot += __shfl_xor(dot, 16);
-        dot += __shfl_xor(dot, 32);
-        float z = dot * (a.scale * a.c.k_scale[at]);
-        if (a.softcap > 0.0f) z = a.softcap * tanhf(z / a.softcap);
-        const int key = t0 + i;
-        if (a.slopes) z += a.slopes[h] * (float)(key - pos);
-        if (key < first || key > last) z = -INFINITY;
-        float top = z;
-#pragma unroll
-        for (int w = 8; w >= 1; w >>= 1) top = fmaxf(top, __shfl_xor(top, w));
-        const float mn = fmaxf(m, top);
-        const float base = mn == -INFINITY ? 0.0f : mn;
-        const float keep = exp2f((m - base) * kLog2e);
-        const float p = exp2f((z - base) * kLog2e);
-        l *= keep;
-#pragma unroll
-        for (int d = 0; d < DV; ++d) o[d] *= keep;
-        m = mn;
-        const float sv = a.c.v_scale[at];
-        const int8_t* v = a.c.v + at * a.c.page * D + (int64_t)slot * D;
-#pragma unroll
-        for (int j = 0; j < 16; ++j) {
-            const float pj = __shfl(p, j);
-            l += pj;
-            if (pj != 0.0f) {
-#pragma unroll
-                for (int d = 0; d < DV; ++d)
-                    o[d] += pj * (sv * (float)v[((int64_t)(j >> 2) * D + lane * DV + d) * 4 + (j & 3)]);
-            }
-        }
-    }
-    if (lane == 0) {
-        sm[wave] = m;
-        sl[wave] = l;
-    }
-#pragma unroll
-    for (int d = 0; d < DV; ++d) so[wave][lane * DV + d] = o[d];
-    __syncthreads();
-    const float top = fmaxf(fmaxf(sm[0], sm[1]), fmaxf(sm[2], sm[3]));
-    const float base = top == -INFINITY ? 0.0f : top;
-    float f[4], total = 0.0f;
-#pragma unroll
-    for (int w = 0; w < 4; ++w) {
-        f[w] = exp2f((sm[w] - base) * kLog2e);
-        total += sl[w] * f[w];
-    }
-    for (int d = threadIdx.x; d < D; d += 256) {
-        float y = 0.0f;
-#pragma unroll
-        for (int w = 0; w < 4; ++w) y += so[w][d] * f[w];
-        y = total == 0.0f ? 0.0f : y / total;
-        reinterpret_cast<uint16_t*>(a.y)[(int64_t)t * a.ldy + (int64_t)h * D + d] =
-            DT == kBF16 ? f32_to_bf16(y) : f32_to_f16(y);
-    }
-    if (a.lse && threadIdx.x == 0)
-        a.lse[(int64_t)t * a.hq + h] = total == 0.0f ? -INFINITY : base + log2f(total) * kLn2;
+// The work: units of kStep keys, numbered over (sequence, key/value head, tile
+// of R rows, step), cut into equal ranges, one for each of 2^lw workgroups,
+// whatever the lengths are.  A (sequence, head, row tile) that lies in one range
+// is written out by its workgroup; one that is cut leaves a partial result (the
+// unnormalised output, M and l of each row) in each range's slot (2 w: the
+// range's first segment; 2 w + 1: its last), and the second kernel joins them.
+struct Units {
+    AttnSeq s;
+    int tiles, steps, k0;  // row tiles; steps of one (head, tile); first key, a multiple of 32
+    int64_t all;           // heads * tiles * steps
+};
+
+template <int R>
+__device__ __forceinline__ Units units_of(const AttentionArgs& a, int s) {
+    Units u;
+    u.s = attn_seq(a, s);
+    u.tiles = (u.s.q.n * (a.hq / a.c.heads) + R - 1) / R;
+    u.k0 = u.s.k0 & ~31;
+    u.steps = u.s.last < u.k0 ? 1 : (u.s.last - u.k0) / kStep + 1;
+    u.all = (int64_t)a.c.heads * u.tiles * u.steps;
+    return u;
 }
 
-template <int DT>
+// Range w of 2^lw: floor(w all / 2^lw), or one unit each while there are fewer
+// units than ranges.  range_of is the range that holds unit u.
+__device__ __forceinline__ int64_t range_start(int64_t all, int w, int lw) {
+    if (all >> lw == 0) return min((int64_t)w, all);
+    const int64_t r = all & (((int64_t)1 << lw) - 1);
+    return w * (all >> lw) + ((w * r) >> lw);
+}
+
+__device__ __forceinline__ int range_of(int64_t all, int64_t u, int lw) {
+    return all >> lw == 0 ? (int)u : (int)((((u + 1) << lw) - 1) / all);
+}
+
+__device__ __forceinline__ int64_t shfl64(int64_t v, int lane) {
+    const int lo = __shfl((int)v, lane), hi = __shfl((int)(v >> 32), lane);
+    return (int64_t)hi << 32 | (uint32_t)lo;
+}
+
+// Inclusive sums over the workgroup's 256 threads, and the total.
+__device__ __forceinline__ int64_t block_scan(int64_t v, int64_t* part, int64_t& total) {
+    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+#pragma unroll
+    for (int d = 1; d < 64; d <<= 1) {
+        const int64_t o = shfl64(v, max(lane - d, 0));
+        if (lane >= d) v += o;
+    }
+    __syncthreads();
+    if (lane == 63) part[wave] = v;
+    __syncthreads();
+    total = part[0] + part[1] + part[2] + part[3];
+    for (int w = 0; w < wave; ++w) v += part[w];
+    return v;
+}
+
+// Partial results of a slot: R rows of D values, then M and l of each row.
+template <int D, int R>
+__device__ __forceinline__ float* slot_of(const AttentionArgs& a, int64_t slot) {
+    return a.ws + slot * (R * (D + 2));
+}
+
+template <int DT, int D>
+__device__ __forceinline__ void write_row(const AttentionArgs& a, int64_t row, int head, int d, const float (&o)[8],
+                                          float M, float l) {
+    const float inv = l == 0.0f ? 0.0f : 1.0f / l;
+    uint4 w;
+    w.x = f32x2_to_16<DT>(o[0] * inv, o[1] * inv);
+    w.y = f32x2_to_16<DT>(o[2] * inv, o[3] * inv);
+    w.z = f32x2_to_16<DT>(o[4] * inv, o[5] * inv);
+    w.w = f32x2_to_16<DT>(o[6] * inv, o[7] * inv);
+    *reinterpret_cast<uint4*>(reinterpret_cast<uint16_t*>(a.y) + row * a.ldy + (int64_t)head * D + d) = w;
+    if (a.lse && d == 0)
+        a.lse[row * a.hq + head] = l == 0.0f ? -INFINITY : (M + __log2f(l)) * kLn2;
+}
+
+// One workgroup of four waves.  A wave takes every fourth tile of 32 tokens of
+// its segment straight from memory into the operands of 16x16x32 products: lane
+// (i = lane % 16, g = lane / 16) holds channels g D/4 .. of token i as K, and
+// channels i D/16 .. of tokens 4 g .. 4 g + 3 as V; scores come out with a row
+// of queries in lane i and tokens 4 g .. 4 g + 3 in its registers, which is the
+// weights' operand of the value product as it stands.  The next tile's codes are
+// loaded while one is computed.
+template <int DT, int D, int NQ>
+__global__ __launch_bounds__(256, D < 256 && (D / 64) * NQ <= 4 ? 2 : 1) void k_attention_few(AttentionArgs a, int lw) {
+    constexpr int R = 16 * NQ, DL = D / 4, NC = D / 32, NT = D / 16, W4 = D / 64;
+    constexpr int kPitch = D + 4;
+    __shared__ float so[4][16][kPitch];
+    __shared__ float sM[4][R], sl[4][R];
+    __shared__ int64_t part[4];
+    __shared__ int64_t found[2];
+    const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, i = lane & 15, g = lane >> 4;
+    const int group = a.hq / a.c.heads;
+
+    // this workgroup's range, and the sequence that it begins in
+    int64_t total = 0, u0, u1;
+    {
+        int64_t mine = 0, incl = 0, t;
+        for (int base = 0; base < a.b.batch; base += 256) {
+            mine = base + tid < a.b.batch ? units_of<R>(a, base + tid).all : 0;
+            incl = block_scan(mine, part, t);
+            total += t;
+        }
+        u0 = range_start(total, blockIdx.x, lw);
+        u1 = range_start(total, blockIdx.x + 1, lw);
+        if (u0 >= u1) return;
+        int64_t before = 0;
+        for (int base = 0; base < a.b.batch; base += 256) {
+            if (a.b.batch > 256) {
+                mine = base + tid < a.b.batch ? units_of<R>(a, base + tid).all : 0;
+                incl = block_scan(mine, part, t);
+            } else {
+                t = total;
+            }
+            if (before + incl > u0 && before + incl - mine <= u0) {
+                found[0] = base + tid;
+                found[1] = before + incl - mine;
+            }
+            before += t;
+            if (before > u0) break;
+        }
+        __syncthreads();
+    }
+    int s = __builtin_amdgcn_readfirstlane((int)found[0]);
+    int64_t from = found[1];  // the first unit of sequence s
+    bool first_segment = true;
+
+    while (u0 < u1) {
+        const Units un = units_of<R>(a, s);
+        const int64_t local = u0 - from;
+        if (local >= un.all) {
+            from += un.all;
+            if (++s >= a.b.batch) return;
+            continue;
+        }
+        const int64_t seg = local / un.steps;
+        const int step0 = __builtin_amdgcn_readfirstlane((int)(local - seg * un.steps));
+        const int hk = __builtin_amdgcn_readfirstlane((int)(seg / un.tiles));
+        const int tile = (int)(seg - (int64_t)hk * un.tiles);
+        const int steps = __builtin_amdgcn_readfirstlane((int)min((int64_t)(un.steps - step0), u1 - u0));
+
+        // the tile's rows: queries as binary16 operands (bfloat16 ones scaled to the row's largest exponent, so
+        // that what binary16 cannot hold is below 2^-39 of the row's largest), the keys that each row sees
+        v8h qf[NQ][NC];
+        int lo[NQ], hi[NQ], pos[NQ], lo_max = 0, hi_min = INT32_MAX;
+        float f[NQ], slope[NQ], M[NQ], l[NQ];
+        v4f o[NQ][NT];
+#pragma unroll
+        for (int n = 0; n < NQ; ++n) {
+            const int r = tile * R + n * 16 + i;
+            const int tok = r / group, head = hk * group + r - tok * group;
+            const bool valid = tok < un.s.q.n;
+            pos[n] = un.s.q.p0 + tok;
+            lo[n] = 1;
+            hi[n] = 0;
+            float top = 0.0f;
+            float x[DL];
+            if (valid) {
+                row_keys(a, un.s, pos[n], lo[n], hi[n]);
+                const uint16_t* row = reinterpret_cast<const uint16_t*>(a.q) + (int64_t)(un.s.q.q0 + tok) * a.ldq +
+                                      (int64_t)head * D + g * DL;
+#pragma unroll
+                for (int c = 0; c < DL / 8; ++c) {
+                    float v[8];
+                    widen8<DT>(load_raw8<DT>(row, c), v);
+#pragma unroll
+                    for (int j = 0; j < 8; ++j) x[8 * c + j] = v[j];
+                }
+                lo_max = max(lo_max, lo[n]);
+                hi_min = min(hi_min, hi[n]);
+            } else {
+#pragma unroll
+                for (int j = 0; j < DL; ++j) x[j] = 0.0f;
+            }
+            int e = 14;
+            if constexpr (DT == kBF16) {
+#pragma unroll
+                for (int j = 0; j < DL; ++j) top = fmaxf(top, fabsf(x[j]));
+                top = fmaxf(top, __shfl_xor(top, 16));
+                top = fmaxf(top, __shfl_xor(top, 32));
+                e = top > 0.0f && top < INFINITY ? __builtin_amdgcn_frexp_expf(top) : 14;
+            }
+#pragma unroll
+            for (int c = 0; c < NC; ++c)
+#pragma unroll
+                for (int j = 0; j < 8; ++j)
+                    qf[n][c][j] = (_Float16)(DT == kBF16 ? ldexpf(x[8 * c + j], 14 - e) : x[8 * c + j]);
+            f[n] = ldexpf(a.softcap > 0.0f ? 2.0f * kLog2e / a.softcap * a.scale : kLog2e * a.scale, e - 14);
+            slope[n] = a.slopes && valid ? a.slopes[head] * kLog2e : 0.0f;
+            M[n] = kNone;
+            l[n] = 0.0f;
+#pragma unroll
+            for (int t = 0; t < NT; ++t) o[n][t] = (v4f){0.0f, 0.0f, 0.0f, 0.0f};
+        }
+#pragma unroll
+        for (int m = 8; m >= 1; m >>= 1) {
+            lo_max = max(lo_max, __shfl_xor(lo_max, m));
+            hi_min = min(hi_min, __shfl_xor(hi_min, m));
+        }
+        lo_max = __builtin_amdgcn_readfirstlane(lo_max);
+        hi_min = __builtin_amdgcn_readfirstlane(hi_min);
+        const float cap2 = a.softcap * kLog2e;
+
+        const int begin = un.k0 + (step0 * 4 + wave) * 32;
+        const int end = min(un.k0 + (step0 + steps) * kStep, un.s.last + 1);
+        const int32_t* table = a.b.page_table + (int64_t)s * a.b.ldt;
+        const int shift = __builtin_ctz(a.c.page);
+
+        // a tile's two groups of 16 tokens: page (-1: none, nothing is loaded and nothing seen), scales, codes
+        struct Tile {
+            int id[2];
+            float ks[2], vs[2];
+            uint4 k[2][W4], v[2][W4];
+        };
+        auto pages = [&](int t0, int (&id)[2]) {
+#pragma unroll
+            for (int u = 0; u < 2; ++u) {
+                const int t = t0 + 16 * u;
+                int p = -1;
+                if (t < end) {
+                    p = table[t >> shift];
+                    if ((uint32_t)p >= (uint32_t)a.c.pages) p = -1;
+                }
+                id[u] = __builtin_amdgcn_readfirstlane(p);
+            }
+        };
+        auto load = [&](int t0, const int (&id)[2], Tile& x) {
+#pragma unroll
+            for (int u = 0; u < 2; ++u) {
+                x.id[u] = id[u];
+                if (id[u] >= 0) {
+                    const int64_t at = (int64_t)id[u] * a.c.heads + hk;
+                    const int slot = (t0 + 16 * u) & (a.c.page - 1);
+                    const int64_t base = (at * a.c.page + slot) * D;
+                    const uint4* kp = reinterpret_cast<const uint4*>(a.c.k + base + i * D + g * DL);
+                    const uint4* vp = reinterpret_cast<const uint4*>(a.c.v + base + g * (4 * D) + i * DL);
+#pragma unroll
+                    for (int w = 0; w < W4; ++w) x.k[u][w] = kp[w];
+#pragma unroll
+                    for (int w = 0; w < W4; ++w) x.v[u][w] = vp[w];
+                    x.ks[u] = a.c.k_scale[at];
+                    x.vs[u] = a.c.v_scale[at];
+                } else {
+#pragma unroll
+                    for (int w = 0; w < W4; ++w) x.k[u][w] = x.v[u][w] = make_uint4(0, 0, 0, 0);
+                    x.ks[u] = 0.0f;
+                    x.vs[u] = 1.0f;
+                }
+            }
+        };
+        auto compute = [&](int t0, const Tile& x) {
+            v4f z[2][NQ];
+            float lv[2], rv[2];
+#pragma unroll
+            for (int u = 0; u < 2; ++u) {
+#pragma unroll
+                for (int n = 0; n < NQ; ++n) z[u][n] = (v4f){0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+                for (int c = 0; c < NC; ++c) {
+                    const uint4& w = x.k[u][c >> 1];
+                    const v8h kf = (c & 1) ? join(codes4(w.z), codes4(w.w)) : join(codes4(w.x), codes4(w.y));
+#pragma unroll
+                    for (int n = 0; n < NQ; ++n)
+                        z[u][n] = __builtin_amdgcn_mfma_f32_16x16x32_f16(kf, qf[n][c], z[u][n], 0, 0, 0);
+                }
+                lv[u] = __log2f(x.vs[u]);
+                rv[u] = __builtin_amdgcn_rcpf(x.vs[u]);
+            }
+            const bool masked = t0 < lo_max || t0 + 31 > hi_min || x.id[0] < 0 || x.id[1] < 0;
+            v8h pf[NQ];
+#pragma unroll
+            for (int n = 0; n < NQ; ++n) {
+                float e[2][4];
+#pragma unroll
+                for (int u = 0; u < 2; ++u)
+#pragma unroll
+                    for (int r = 0; r < 4; ++r) {
+                        float y = z[u][n][r] * (f[n] * x.ks[u]);
+                        if (a.softcap > 0.0f) y = capped(y, cap2);
+                        if (a.slopes) y += slope[n] * (float)(t0 + 16 * u + 4 * g + r - pos[n]);
+                        y += lv[u];
+                        if (masked) {
+                            const int key = t0 + 16 * u + 4 * g + r;
+                            y = key >= lo[n] && key <= hi[n] && x.id[u] >= 0 ? y : -INFINITY;
+                        }
+                        e[u][r] = y;
+                    }
+                float top = fmaxf(fmaxf(fmaxf(e[0][0], e[0][1]), fmaxf(e[0][2], e[0][3])),
+                                  fmaxf(fmaxf(e[1][0], e[1][1]), fmaxf(e[1][2], e[1][3])));
+                if (__any(top > M[n] + (kLift + kSlack))) {
+                    top = fmaxf(top, __shfl_xor(top, 16));
+                    top = fmaxf(top, __shfl_xor(top, 32));
+                    if (top > M[n] + (kLift + kSlack)) {
+                        const float now = ceilf(top) - kLift;
+                        const float keep = exp2_(M[n] - now);
+                        M[n] = now;
+                        l[n] *= keep;
+#pragma unroll
+                        for (int t = 0; t < NT; ++t) o[n][t] *= keep;
+                    }
+                }
+                float p[2][4];
+#pragma unroll
+                for (int u = 0; u < 2; ++u) {
+#pragma unroll
+                    for (int r = 0; r < 4; ++r) p[u][r] = exp2_(e[u][r] - M[n]);
+                    const float sum = (p[u][0] + p[u][1]) + (p[u][2] + p[u][3]);
+                    l[n] += sum == 0.0f ? 0.0f : sum * rv[u];  // hidden keys of a page whose scale is not finite: 0
+                }
+                const uint4 w = make_uint4(f32x2_to_16<kF16>(p[0][0], p[0][1]), f32x2_to_16<kF16>(p[0][2], p[0][3]),
+                                           f32x2_to_16<kF16>(p[1][0], p[1][1]), f32x2_to_16<kF16>(p[1][2], p[1][3]));
+                pf[n] = __builtin_bit_cast(v8h, w);
+            }
+#pragma unroll
+            for (int t = 0; t < NT; ++t) {
+                const uint32_t w0 = reinterpret_cast<const uint32_t*>(x.v[0])[t];
+                const uint32_t w1 = reinterpret_cast<const uint32_t*>(x.v[1])[t];
+                const v8h vf = join(codes4(w0), codes4(w1));
+#pragma unroll
+                for (int n = 0; n < NQ; ++n)
+                    o[n][t] = __builtin_amdgcn_mfma_f32_16x16x32_f16(vf, pf[n], o[n][t], 0, 0, 0);
+            }
+        };
+
+        if (begin < end) {
+            int id[2];
+            Tile x, y;
+            pages(begin, id);
+            load(begin, id, x);
+            pages(begin + kStep, id);
+            for (int t0 = begin; t0 < end; t0 += 2 * kStep) {
+                load(t0 + kStep, id, y);
+                pages(t0 + 2 * kStep, id);
+                compute(t0, x);
+                if (t0 + kStep >= end) break;
+                load(t0 + 2 * kStep, id, x);
+                pages(t0 + 3 * kStep, id);
+                compute(t0 + kStep, y);
+            }
+        }
+
+        // join the four waves, 16 rows at a time
+        const bool whole = steps == un.steps;
+        const int64_t slot = 2 * (int64_t)blockIdx.x + (first_segment ? 0 : 1);
+        __syncthreads();
+#pragma unroll
+        for (int n = 0; n < NQ; ++n) {
+            l[n] += __shfl_xor(l[n], 16);
+            l[n] += __shfl_xor(l[n], 32);
+            if (g == 0) {
+                sM[wave][n * 16 + i] = M[n];
+                sl[wave][n * 16 + i] = l[n];
+            }
+        }
+#pragma unroll
+        for (int n = 0; n < NQ; ++n) {
+            __syncthreads();
+            const int row = n * 16 + i;
+            const float top = fmaxf(fmaxf(sM[0][row], sM[1][row]), fmaxf(sM[2][row], sM[3][row]));
+            const float keep = exp2_(M[n] - top);
+#pragma unroll
+            for (int r = 0; r < 4; ++r)
+#pragma unroll
+                for (int t = 0; t < NT; t += 4)
+                    *reinterpret_cast<float4*>(&so[wave][i][(4 * g + r) * NT + t]) =
+                        make_float4(o[n][t][r] * keep, o[n][t + 1][r] * keep, o[n][t + 2][r] * keep, o[n][t + 3][r] * keep);
+            __syncthreads();
+            for (int c = tid; c < 16 * (D / 8); c += 256) {
+                const int j = c / (D / 8), d = c % (D / 8) * 8;
+                const int rr = tile * R + n * 16 + j;
+                const int tok = rr / group;
+                if (tok < un.s.q.n) {
+                    const float Mj = fmaxf(fmaxf(sM[0][n * 16 + j], sM[1][n * 16 + j]),
+                                           fmaxf(sM[2][n * 16 + j], sM[3][n * 16 + j]));
+                    float lj = 0.0f, v[8] = {};
+#pragma unroll
+                    for (int w = 0; w < 4; ++w) {
+                        lj += sl[w][n * 16 + j] * exp2_(sM[w][n * 16 + j] - Mj);
+#pragma unroll
+                        for (int k = 0; k < 8; ++k) v[k] += so[w][j][d + k];
+                    }
+                    if (whole) {
+                        write_row<DT, D>(a, un.s.q.q0 + tok, hk * group + rr - tok * group, d, v, Mj, lj);
+                    } else {
+                        float* p = slot_of<D, R>(a, slot);
+                        float4* q = reinterpret_cast<float4*>(p + (n * 16 + j) * D + d);
+                        q[0] = make_float4(v[0], v[1], v[2], v[3]);
+                        q[1] = make_float4(v[4], v[5], v[6], v[7]);
+                        if (d == 0) {
+                            p[R * D + n * 16 + j] = Mj;
+                            p[R * D + R + n * 16 + j] = lj;
+                        }
+                    }
+                }
+            }
+        }
+        first_segment = false;
+        u0 += steps;
+    }
+}
+
+// Joins the partial results of a segment that was cut: one workgroup for each
+// (row tile of a sequence, head; row), D / 8 threads for each of 2048 / D parts
+// at a time.
+template <int DT, int D, int R>
+__global__ __launch_bounds__(256) void k_attention_join(AttentionArgs a, int lw) {
+    constexpr int NP = 2048 / D;  // parts taken at once
+    __shared__ int64_t part[4];
+    __shared__ float sm[NP], sl[NP], so[NP][D];
+    const int tid = threadIdx.x, group = a.hq / a.c.heads;
+    const int64_t item = blockIdx.x / a.c.heads;
+    const int hk = (int)(blockIdx.x - item * a.c.heads), j = blockIdx.y;
+    int s;
+    int64_t tile;
+    if (a.b.cu_q) {
+        s = item_seq(a.b, item, group, R, 1);
+        tile = item - item_start(a.b, s, group, R, 1);
+    } else {
+        const int tiles = (group + R - 1) / R;
+        s = (int)(item / tiles);
+        tile = item - (int64_t)s * tiles;
+    }
+    const Units un = units_of<R>(a, s);
+    const int64_t rr = tile * R + j;
+    if (tile >= un.tiles || rr >= (int64_t)un.s.q.n * group) return;
+
+    int64_t before = 0, total = 0, t;
+    for (int b = tid; b < a.b.batch; b += 256) {
+        const int64_t u = units_of<R>(a, b).all;
+        total += u;
+        if (b < s) before += u;
+    }
+    block_scan(before, part, t);
+    before = t;
+    block_scan(total, part, t);
+    total = t;
+    const int64_t S = before + ((int64_t)hk * un.tiles + tile) * un.steps;
+    const int w0 = range_of(total, S, lw), w1 = range_of(total, S + un.steps - 1, lw);
+    if (w0 == w1) return;  // one range held it whole
+    const bool begins = range_start(total, w0, lw) >= S;
+
+    const int p = tid / (D / 8), d = tid % (D / 8) * 8;
+    float M = kNone, l = 0.0f, o[8] = {};
+    for (int w = w0 + p; w <= w1; w += NP) {
+        const float* x = slot_of<D, R>(a, 2 * (int64_t)w + (w == w0 && !begins ? 1 : 0));
+        const float Mw = x[R * D + j], lw_ = x[R * D + R + j];
+        const float4 v0 = *reinterpret_cast<const float4*>(x + j * D + d);
+        const float4 v1 = *reinterpret_cast<const float4*>(x + j * D + d + 4);
+        const float v[8] = {v0.x, v0.y, v0.z, v0.w, v1.x, v1.y, v1.z, v1.w};
+        const float now = fmaxf(M, Mw), fo = exp2_(M - now), fw = exp2_(Mw - now);
+        M = now;
+        l = l * fo + lw_ * fw;
+#pragma unroll
+        for (int k = 0; k < 8; ++k) o[k] = o[k] * fo + v[k] * fw;
+    }
+#pragma unroll
+    for (int k = 0; k < 8; ++k) so[p][d + k] = o[k];
+    if (d == 0) {
+        sm[p] = M;
+        sl[p] = l;
+    }
+    __syncthreads();
+    if (p != 0) return;
+    float top = sm[0];
+    for (int w = 1; w < NP; ++w) top = fmaxf(top, sm[w]);
+    l = 0.0f;
+#pragma unroll
+    for (int k = 0; k < 8; ++k) o[k] = 0.0f;
+#pragma unroll 2
+    for (int w = 0; w < NP; ++w) {
+        const float keep = exp2_(sm[w] - top);
+        l += sl[w] * keep;
+#pragma unroll
+        for (int k = 0; k < 8; ++k) o[k] += so[w][d + k] * keep;
+    }
+    const int64_t tok = rr / group;
+    write_row<DT, D>(a, un.s.q.q0 + tok, hk * group + (int)(rr - tok * group), d, o, top, l);
+}
+
+constexpr int kWaysLog2 = 9;  // ranges of the few-row kernel
+
+// 16-row tiles of the few-row kernel for a batch: enough for the rows that a
+// sequence has on average.
+int row_tiles(int64_t tokens, int64_t batch, int hq, int hkv, int dim) {
+    const int64_t rows = (tokens * (hq / hkv) + batch - 1) / batch;
+    if (rows <= 16) return 1;
+    if (rows <= 32 || dim == 256) return 2;
+    return 4;
+}
+
+template <int DT, int D, int NQ>
+void launch_few(const AttentionArgs& a, hipStream_t st) {
+    constexpr int R = 16 * NQ;
+    const int group = a.hq / a.c.heads;
+    const int64_t items = a.b.cu_q ? (int64_t)a.b.tokens * group / R + a.b.batch
+                                   : (int64_t)a.b.batch * ((group + R - 1) / R);
+    k_attention_few<DT, D, NQ><<<1 << kWaysLog2, 256, 0, st>>>(a, kWaysLog2);
+    k_attention_join<DT, D, R><<<dim3((uint32_t)(items * a.c.heads), a.b.cu_q ? R : std::min(R, group)), 256, 0, st>>>(
+        a, kWaysLog2);
+}
+
+template <int DT, int D>
 void launch(const AttentionArgs& a, hipStream_t st) {
-    const dim3 grid((uint32_t)((int64_t)a.b.tokens * a.hq));
-    if (a.c.dim == 64) k_attention_rows<DT, 64><<<grid, 256, 0, st>>>(a);
-    else if (a.c.dim == 128) k_attention_rows<DT, 128><<<grid, 256, 0, st>>>(a);
-    else k_attention_rows<DT, 256><<<grid, 256, 0, st>>>(a);
+    const int nq = row_tiles(a.b.tokens, a.b.batch, a.hq, a.c.heads, D);
+    if (nq == 1) launch_few<DT, D, 1>(a, st);
+    else if (nq == 2) launch_few<DT, D, 2>(a, st);
+    else if constexpr (D < 256) launch_few<DT, D, 4>(a, st);
 }
 
 }  // namespace
 
-size_t attention_workspace(int64_t tokens, int64_t batch, int hq, int hkv, int dim) { return 0; }
+size_t attention_workspace(int64_t tokens, int64_t batch, int hq, int hkv, int dim) {
+    const size_t rows = 16 * row_tiles(tokens, batch, hq, hkv, dim);
+    return (size_t(2) << kWaysLog2) * rows * (dim + 2) * sizeof(float);
+}
 
-int64_t attention_threads(const AttentionArgs& a) { return (int64_t)a.b.tokens * a.hq * 256; }
+int64_t attention_threads(const AttentionArgs& a) {
+    const int group = a.hq / a.c.heads;
+    if (a.b.batch == 0) return 0;
+    const int R = 16 * row_tiles(a.b.tokens, a.b.batch, a.hq, a.c.heads, a.c.dim);
+    const int64_t items = a.b.cu_q ? (int64_t)a.b.tokens * group / R + a.b.batch
+                                   : (int64_t)a.b.batch * ((group + R - 1) / R);
+    return items * a.c.heads * (a.b.cu_q ? R : std::min(R, group)) * 256;
+}
 
 void launch_attention(const AttentionArgs& a, int dt, hipStream_t st) {
-    if (dt == kBF16) launch<kBF16>(a, st);
-    else launch<kF16>(a, st);
+    if (dt == kBF16) {
+        if (a.c.dim == 64) launch<kBF16, 64>(a, st);
+        else if (a.c.dim == 128) launch<kBF16, 128>(a, st);
+        else launch<kBF16, 256>(a, st);
+    } else {
+        if (a.c.dim == 64) launch<kF16, 64>(a, st);
+        else if (a.c.dim == 128) launch<kF16, 128>(a, st);
+        else launch<kF16, 256>(a, st);
+    }
 }
 
 }  // namespace pdq

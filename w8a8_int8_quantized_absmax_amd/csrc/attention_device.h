@@ -1,0 +1,78 @@
+// What the attention kernels over the INT8 key/value cache share.
+//
+// Both take K codes and V codes as binary16 matrix operands (integers up to 127
+// are exact there) and leave the scales outside the products: a score is
+// (q . codes) * S_k, and the value scale goes into the weight's exponent,
+//   p = 2^(z log2 e + log2 S_v - M),   O = sum p * codes,   l = sum p / S_v,
+// so that a weight, rounded to binary16 for the value product, keeps its 11 bits
+// whatever the scales are, and a page's scale costs one addition a score.
+//
+// M is an integer no more than kSlack below the largest exponent seen, moved
+// only when a weight would pass 2^(kLift + kSlack): moving it multiplies by
+// powers of two, so when it moves does not change a row's result beyond
+// what binary16's range cuts off (weights under 2^-25 of 2^kLift), and most
+// tiles need no maximum across lanes.
+#pragma once
+
+#include "kv_device.h"
+
+namespace pdq {
+
+typedef float v4f __attribute__((ext_vector_type(4)));
+typedef _Float16 v2h __attribute__((ext_vector_type(2)));
+typedef _Float16 v4h __attribute__((ext_vector_type(4)));
+
+constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
+constexpr float kLift = 5.0f, kSlack = 8.0f;  // weights stay below 2^13
+constexpr float kNone = -3e38f;               // M before the first visible key
+
+__device__ __forceinline__ float exp2_(float x) { return __builtin_amdgcn_exp2f(x); }
+
+// Four codes as binary16: the byte b ^ 0x80 under the exponent byte 0x64 is
+// 1024 + 128 + code, exactly; subtracting 1152 is exact too.
+__device__ __forceinline__ v4h codes4(uint32_t w) {
+    w ^= 0x80808080u;
+    const v2h lo = __builtin_bit_cast(v2h, __builtin_amdgcn_perm(0x64646464u, w, 0x04010400u));
+    const v2h hi = __builtin_bit_cast(v2h, __builtin_amdgcn_perm(0x64646464u, w, 0x04030402u));
+    const v2h off = {(_Float16)1152.0f, (_Float16)1152.0f};
+    const v2h a = lo - off, b = hi - off;
+    return __builtin_shufflevector(a, b, 0, 1, 2, 3);
+}
+
+__device__ __forceinline__ v8h join(v4h a, v4h b) { return __builtin_shufflevector(a, b, 0, 1, 2, 3, 4, 5, 6, 7); }
+
+// The score (q . codes) * f, capped or not, in units of log2: cap2 = softcap *
+// log2 e, and f = scale * S_k * log2 e without a cap, 2 log2 e * scale * S_k /
+// softcap with one: tanh(x) = 1 - 2 / (2^(2 x log2 e) + 1), exact at both ends,
+// off by an ulp of 1 between.
+__device__ __forceinline__ float capped(float x2, float cap2) {
+    const float r = __builtin_amdgcn_rcpf(exp2_(x2) + 1.0f);
+    return cap2 * (1.0f - 2.0f * r);
+}
+
+// A sequence's rows and keys as a tile of R rows takes them: rows are (token,
+// query head of the group), the keys seen by any of its rows k0 .. last.
+struct AttnSeq {
+    KvSeq q;
+    int len;       // min(length, what the table can name)
+    int prefix;    // keys that every row sees (0: none)
+    int k0, last;  // keys that some row sees (last < k0: none)
+};
+
+__device__ __forceinline__ AttnSeq attn_seq(const AttentionArgs& a, int s) {
+    AttnSeq r;
+    r.q = kv_seq(a.b, s);
+    r.len = min(r.q.len, a.b.max_pages * a.c.page);
+    r.prefix = a.prefix ? max(a.prefix[s], 0) : 0;
+    r.k0 = a.window ? (int)max((int64_t)r.q.p0 - a.window + 1, (int64_t)0) : 0;
+    r.last = min(max(r.q.p0 + r.q.n, r.prefix), r.len) - 1;
+    return r;
+}
+
+// The keys lo .. hi that a row at position pos sees.
+__device__ __forceinline__ void row_keys(const AttentionArgs& a, const AttnSeq& s, int pos, int& lo, int& hi) {
+    lo = a.window ? (int)max((int64_t)pos - a.window + 1, (int64_t)0) : 0;
+    hi = min(max(pos + 1, s.prefix), s.len) - 1;
+}
+
+}  // namespace pdq
