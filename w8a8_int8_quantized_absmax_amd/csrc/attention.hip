@@ -493,58 +493,69 @@ __global__ __launch_bounds__(256) void k_attention_join(AttentionArgs a, int lw)
 constexpr int kWaysLog2 = 9;  // ranges of the few-row kernel
 
 // 16-row tiles of the few-row kernel for a batch: enough for the rows that a
-// sequence has on average.
+// sequence has on average; 0: the prompt kernel.
 int row_tiles(int64_t tokens, int64_t batch, int hq, int hkv, int dim) {
     const int64_t rows = (tokens * (hq / hkv) + batch - 1) / batch;
-    if (rows <= 16) return 1;
-    if (rows <= 32 || dim == 256) return 2;
-    return 4;
+    return rows <= 16 ? 1 : rows <= 32 ? 2 : 0;
+}
+
+int64_t few_items(const AttentionArgs& a, int R) {
+    const int group = a.hq / a.c.heads;
+    return a.b.cu_q ? (int64_t)a.b.tokens * group / R + a.b.batch : (int64_t)a.b.batch * ((group + R - 1) / R);
+}
+
+// What the table can name bounds the parts that are worth cutting.
+int prompt_splits(const AttentionArgs& a) {
+    const int64_t keys = (int64_t)a.b.max_pages * a.c.page;
+    return (int)std::max<int64_t>(1, std::min<int64_t>(attention_prompt_splits(a.b.tokens, a.hq, a.c.heads, a.c.dim),
+                                                       keys / 256));
 }
 
 template <int DT, int D, int NQ>
 void launch_few(const AttentionArgs& a, hipStream_t st) {
     constexpr int R = 16 * NQ;
     const int group = a.hq / a.c.heads;
-    const int64_t items = a.b.cu_q ? (int64_t)a.b.tokens * group / R + a.b.batch
-                                   : (int64_t)a.b.batch * ((group + R - 1) / R);
+    const int64_t items = few_items(a, R);
     k_attention_few<DT, D, NQ><<<1 << kWaysLog2, 256, 0, st>>>(a, kWaysLog2);
     k_attention_join<DT, D, R><<<dim3((uint32_t)(items * a.c.heads), a.b.cu_q ? R : std::min(R, group)), 256, 0, st>>>(
         a, kWaysLog2);
 }
 
 template <int DT, int D>
-void launch(const AttentionArgs& a, hipStream_t st) {
-    const int nq = row_tiles(a.b.tokens, a.b.batch, a.hq, a.c.heads, D);
-    if (nq == 1) launch_few<DT, D, 1>(a, st);
-    else if (nq == 2) launch_few<DT, D, 2>(a, st);
-    else if constexpr (D < 256) launch_few<DT, D, 4>(a, st);
+void launch(const AttentionArgs& a, int tiles, hipStream_t st) {
+    if (tiles == 1) launch_few<DT, D, 1>(a, st);
+    else launch_few<DT, D, 2>(a, st);
 }
 
 }  // namespace
 
 size_t attention_workspace(int64_t tokens, int64_t batch, int hq, int hkv, int dim) {
-    const size_t rows = 16 * row_tiles(tokens, batch, hq, hkv, dim);
-    return (size_t(2) << kWaysLog2) * rows * (dim + 2) * sizeof(float);
+    const int tiles = row_tiles(tokens, batch, hq, hkv, dim);
+    if (tiles > 0) return (size_t(2) << kWaysLog2) * (16 * tiles) * (dim + 2) * sizeof(float);
+    const int splits = attention_prompt_splits(tokens, hq, hkv, dim);
+    return splits > 1 ? (size_t)splits * tokens * hq * (dim + 2) * sizeof(float) : 0;
 }
 
 int64_t attention_threads(const AttentionArgs& a) {
-    const int group = a.hq / a.c.heads;
     if (a.b.batch == 0) return 0;
-    const int R = 16 * row_tiles(a.b.tokens, a.b.batch, a.hq, a.c.heads, a.c.dim);
-    const int64_t items = a.b.cu_q ? (int64_t)a.b.tokens * group / R + a.b.batch
-                                   : (int64_t)a.b.batch * ((group + R - 1) / R);
-    return items * a.c.heads * (a.b.cu_q ? R : std::min(R, group)) * 256;
+    const int tiles = row_tiles(a.b.tokens, a.b.batch, a.hq, a.c.heads, a.c.dim);
+    if (tiles == 0) return attention_prompt_threads(a, prompt_splits(a));
+    const int R = 16 * tiles;
+    return few_items(a, R) * a.c.heads * (a.b.cu_q ? R : std::min(R, a.hq / a.c.heads)) * 256;
 }
 
 void launch_attention(const AttentionArgs& a, int dt, hipStream_t st) {
-    if (dt == kBF16) {
-        if (a.c.dim == 64) launch<kBF16, 64>(a, st);
-        else if (a.c.dim == 128) launch<kBF16, 128>(a, st);
-        else launch<kBF16, 256>(a, st);
+    const int tiles = row_tiles(a.b.tokens, a.b.batch, a.hq, a.c.heads, a.c.dim);
+    if (tiles == 0) {
+        launch_attention_prompt(a, dt, prompt_splits(a), st);
+    } else if (dt == kBF16) {
+        if (a.c.dim == 64) launch<kBF16, 64>(a, tiles, st);
+        else if (a.c.dim == 128) launch<kBF16, 128>(a, tiles, st);
+        else launch<kBF16, 256>(a, tiles, st);
     } else {
-        if (a.c.dim == 64) launch<kF16, 64>(a, st);
-        else if (a.c.dim == 128) launch<kF16, 128>(a, st);
-        else launch<kF16, 256>(a, st);
+        if (a.c.dim == 64) launch<kF16, 64>(a, tiles, st);
+        else if (a.c.dim == 128) launch<kF16, 128>(a, tiles, st);
+        else launch<kF16, 256>(a, tiles, st);
     }
 }
 

@@ -75,4 +75,10 @@ __device__ __forceinline__ void row_keys(const AttentionArgs& a, const AttnSeq& 
     hi = min(max(pos + 1, s.prefix), s.len) - 1;
 }
 
+// attention_prompt.hip: many rows for each sequence.  splits: parts of the keys,
+// joined through the workspace ([splits, tokens, hq, dim + 2] floats) beyond one.
+int attention_prompt_splits(int64_t tokens, int hq, int hkv, int dim);
+int64_t attention_prompt_threads(const AttentionArgs& a, int splits);
+void launch_attention_prompt(const AttentionArgs& a, int dt, int splits, hipStream_t st);
+
 }  // namespace pdq
