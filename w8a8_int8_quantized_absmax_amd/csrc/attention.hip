@@ -23,10 +23,10 @@ struct Units {
     int64_t all;           // heads * tiles * steps
 };
 
-template <int R>
+template <int R, bool Uniform = false>
 __device__ __forceinline__ Units units_of(const AttentionArgs& a, int s) {
     Units u;
-    u.s = attn_seq(a, s);
+    u.s = attn_seq<Uniform>(a, s);
     u.tiles = (u.s.q.n * (a.hq / a.c.heads) + R - 1) / R;
     u.k0 = u.s.k0 & ~31;
     u.steps = u.s.last < u.k0 ? 1 : (u.s.last - u.k0) / kStep + 1;
@@ -102,7 +102,7 @@ __global__ __launch_bounds__(256, D < 256 && (D / 64) * NQ <= 4 ? 2 : 1) void k_
     __shared__ float sM[4][R], sl[4][R];
     __shared__ int64_t part[4];
     __shared__ int64_t found[2];
-    const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, i = lane & 15, g = lane >> 4;
+    const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6), i = lane & 15, g = lane >> 4;
     const int group = a.hq / a.c.heads;
 
     // this workgroup's range, and the sequence that it begins in
@@ -139,7 +139,7 @@ __global__ __launch_bounds__(256, D < 256 && (D / 64) * NQ <= 4 ? 2 : 1) void k_
     bool first_segment = true;
 
     while (u0 < u1) {
-        const Units un = units_of<R>(a, s);
+        const Units un = units_of<R, true>(a, s);
         const int64_t local = u0 - from;
         if (local >= un.all) {
             from += un.all;
@@ -219,9 +219,10 @@ __global__ __launch_bounds__(256, D < 256 && (D / 64) * NQ <= 4 ? 2 : 1) void k_
         const int32_t* table = a.b.page_table + (int64_t)s * a.b.ldt;
         const int shift = __builtin_ctz(a.c.page);
 
-        // a tile's two groups of 16 tokens: page (-1: none, nothing is loaded and nothing seen), scales, codes
+        // a tile's two groups of 16 tokens: whether the table names a page of the pool for them (if not, page 0 is
+        // loaded and not seen: with no pool at all no sequence has keys), its scales and codes
         struct Tile {
-            int id[2];
+            bool there[2];
             float ks[2], vs[2];
             uint4 k[2][W4], v[2][W4];
         };
@@ -229,36 +230,24 @@ __global__ __launch_bounds__(256, D < 256 && (D / 64) * NQ <= 4 ? 2 : 1) void k_
 #pragma unroll
             for (int u = 0; u < 2; ++u) {
                 const int t = t0 + 16 * u;
-                int p = -1;
-                if (t < end) {
-                    p = table[t >> shift];
-                    if ((uint32_t)p >= (uint32_t)a.c.pages) p = -1;
-                }
-                id[u] = __builtin_amdgcn_readfirstlane(p);
+                id[u] = t < end ? uniform_load(table + (t >> shift)) : -1;
             }
         };
         auto load = [&](int t0, const int (&id)[2], Tile& x) {
 #pragma unroll
             for (int u = 0; u < 2; ++u) {
-                x.id[u] = id[u];
-                if (id[u] >= 0) {
-                    const int64_t at = (int64_t)id[u] * a.c.heads + hk;
-                    const int slot = (t0 + 16 * u) & (a.c.page - 1);
-                    const int64_t base = (at * a.c.page + slot) * D;
-                    const uint4* kp = reinterpret_cast<const uint4*>(a.c.k + base + i * D + g * DL);
-                    const uint4* vp = reinterpret_cast<const uint4*>(a.c.v + base + g * (4 * D) + i * DL);
+                x.there[u] = (uint32_t)id[u] < (uint32_t)a.c.pages;
+                const int64_t at = (int64_t)(x.there[u] ? id[u] : 0) * a.c.heads + hk;
+                const int slot = (t0 + 16 * u) & (a.c.page - 1);
+                const int64_t base = (at * a.c.page + slot) * D;
+                const uint4* kp = reinterpret_cast<const uint4*>(a.c.k + base + i * D + g * DL);
+                const uint4* vp = reinterpret_cast<const uint4*>(a.c.v + base + g * (4 * D) + i * DL);
 #pragma unroll
-                    for (int w = 0; w < W4; ++w) x.k[u][w] = kp[w];
+                for (int w = 0; w < W4; ++w) x.k[u][w] = kp[w];
 #pragma unroll
-                    for (int w = 0; w < W4; ++w) x.v[u][w] = vp[w];
-                    x.ks[u] = a.c.k_scale[at];
-                    x.vs[u] = a.c.v_scale[at];
-                } else {
-#pragma unroll
-                    for (int w = 0; w < W4; ++w) x.k[u][w] = x.v[u][w] = make_uint4(0, 0, 0, 0);
-                    x.ks[u] = 0.0f;
-                    x.vs[u] = 1.0f;
-                }
+                for (int w = 0; w < W4; ++w) x.v[u][w] = vp[w];
+                x.ks[u] = uniform_load(a.c.k_scale + at);
+                x.vs[u] = uniform_load(a.c.v_scale + at);
             }
         };
         auto compute = [&](int t0, const Tile& x) {
@@ -279,7 +268,7 @@ __global__ __launch_bounds__(256, D < 256 && (D / 64) * NQ <= 4 ? 2 : 1) void k_
                 lv[u] = __log2f(x.vs[u]);
                 rv[u] = __builtin_amdgcn_rcpf(x.vs[u]);
             }
-            const bool masked = t0 < lo_max || t0 + 31 > hi_min || x.id[0] < 0 || x.id[1] < 0;
+            const bool masked = t0 < lo_max || t0 + 31 > hi_min || !x.there[0] || !x.there[1];
             v8h pf[NQ];
 #pragma unroll
             for (int n = 0; n < NQ; ++n) {
@@ -287,17 +276,32 @@ __global__ __launch_bounds__(256, D < 256 && (D / 64) * NQ <= 4 ? 2 : 1) void k_
 #pragma unroll
                 for (int u = 0; u < 2; ++u)
 #pragma unroll
-                    for (int r = 0; r < 4; ++r) {
-                        float y = z[u][n][r] * (f[n] * x.ks[u]);
-                        if (a.softcap > 0.0f) y = capped(y, cap2);
-                        if (a.slopes) y += slope[n] * (float)(t0 + 16 * u + 4 * g + r - pos[n]);
-                        y += lv[u];
-                        if (masked) {
+                    for (int r = 0; r < 4; ++r) e[u][r] = z[u][n][r] * (f[n] * x.ks[u]);
+                if (a.softcap > 0.0f) {
+#pragma unroll
+                    for (int u = 0; u < 2; ++u)
+#pragma unroll
+                        for (int r = 0; r < 4; ++r) e[u][r] = capped(e[u][r], cap2);
+                }
+                if (a.slopes) {
+#pragma unroll
+                    for (int u = 0; u < 2; ++u)
+#pragma unroll
+                        for (int r = 0; r < 4; ++r) e[u][r] += slope[n] * (float)(t0 + 16 * u + 4 * g + r - pos[n]);
+                }
+#pragma unroll
+                for (int u = 0; u < 2; ++u)
+#pragma unroll
+                    for (int r = 0; r < 4; ++r) e[u][r] += lv[u];
+                if (masked) {
+#pragma unroll
+                    for (int u = 0; u < 2; ++u)
+#pragma unroll
+                        for (int r = 0; r < 4; ++r) {
                             const int key = t0 + 16 * u + 4 * g + r;
-                            y = key >= lo[n] && key <= hi[n] && x.id[u] >= 0 ? y : -INFINITY;
+                            e[u][r] = key >= lo[n] && key <= hi[n] && x.there[u] ? e[u][r] : -INFINITY;
                         }
-                        e[u][r] = y;
-                    }
+                }
                 float top = fmaxf(fmaxf(fmaxf(e[0][0], e[0][1]), fmaxf(e[0][2], e[0][3])),
                                   fmaxf(fmaxf(e[1][0], e[1][1]), fmaxf(e[1][2], e[1][3])));
                 if (__any(top > M[n] + (kLift + kSlack))) {
@@ -341,14 +345,21 @@ __global__ __launch_bounds__(256, D < 256 && (D / 64) * NQ <= 4 ? 2 : 1) void k_
             pages(begin, id);
             load(begin, id, x);
             pages(begin + kStep, id);
-            for (int t0 = begin; t0 < end; t0 += 2 * kStep) {
-                load(t0 + kStep, id, y);
-                pages(t0 + 2 * kStep, id);
+            for (int t0 = begin;; t0 += 2 * kStep) {
+                const bool more = t0 + kStep < end;
+                if (more) {
+                    load(t0 + kStep, id, y);
+                    pages(t0 + 2 * kStep, id);
+                }
                 compute(t0, x);
-                if (t0 + kStep >= end) break;
-                load(t0 + 2 * kStep, id, x);
-                pages(t0 + 3 * kStep, id);
+                if (!more) break;
+                const bool even = t0 + 2 * kStep < end;
+                if (even) {
+                    load(t0 + 2 * kStep, id, x);
+                    pages(t0 + 3 * kStep, id);
+                }
                 compute(t0 + kStep, y);
+                if (!even) break;
             }
         }
 
@@ -433,7 +444,7 @@ __global__ __launch_bounds__(256) void k_attention_join(AttentionArgs a, int lw)
         s = (int)(item / tiles);
         tile = item - (int64_t)s * tiles;
     }
-    const Units un = units_of<R>(a, s);
+    const Units un = units_of<R, true>(a, s);
     const int64_t rr = tile * R + j;
     if (tile >= un.tiles || rr >= (int64_t)un.s.q.n * group) return;
 

@@ -54,16 +54,17 @@ __device__ __forceinline__ float capped(float x2, float cap2) {
 // query head of the group), the keys seen by any of its rows k0 .. last.
 struct AttnSeq {
     KvSeq q;
-    int len;       // min(length, what the table can name)
+    int len;       // min(length, what the table can name); 0 without a pool
     int prefix;    // keys that every row sees (0: none)
     int k0, last;  // keys that some row sees (last < k0: none)
 };
 
+template <bool Uniform = false>
 __device__ __forceinline__ AttnSeq attn_seq(const AttentionArgs& a, int s) {
     AttnSeq r;
-    r.q = kv_seq(a.b, s);
-    r.len = min(r.q.len, a.b.max_pages * a.c.page);
-    r.prefix = a.prefix ? max(a.prefix[s], 0) : 0;
+    r.q = kv_seq<Uniform>(a.b, s);
+    r.len = a.c.pages > 0 ? min(r.q.len, a.b.max_pages * a.c.page) : 0;
+    r.prefix = a.prefix ? max(load_as<Uniform>(a.prefix + s), 0) : 0;
     r.k0 = a.window ? (int)max((int64_t)r.q.p0 - a.window + 1, (int64_t)0) : 0;
     r.last = min(max(r.q.p0 + r.q.n, r.prefix), r.len) - 1;
     return r;

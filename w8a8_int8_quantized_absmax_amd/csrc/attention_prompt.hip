@@ -47,7 +47,7 @@ __global__ __launch_bounds__(256, D <= 128 ? 2 : 1) void k_attention_prompt(Atte
     const int s = a.b.cu_q ? item_seq(a.b, item, group, kRows, 1) : (int)(item / ((group + kRows - 1) / kRows));
     const int64_t tile = a.b.cu_q ? item - item_start(a.b, s, group, kRows, 1)
                                   : item - (int64_t)s * ((group + kRows - 1) / kRows);
-    const AttnSeq sq = attn_seq(a, s);
+    const AttnSeq sq = attn_seq<true>(a, s);
     const int64_t rows = (int64_t)sq.q.n * group, r0 = tile * kRows;
     if (r0 >= rows) return;
 
@@ -135,36 +135,23 @@ __global__ __launch_bounds__(256, D <= 128 ? 2 : 1) void k_attention_prompt(Atte
     const int kt = lane >> 2, kj = lane & 3;  // token of the 16, quarter of its channels
     auto page_at = [&](int t0) -> int {
         const int t = t0 + 16 * wave;
-        int p = -1;
-        if (t < end) {
-            p = table[t >> shift];
-            if ((uint32_t)p >= (uint32_t)a.c.pages) p = -1;
-        }
-        return __builtin_amdgcn_readfirstlane(p);
+        return t < end ? uniform_load(table + (t >> shift)) : -1;
     };
     auto load = [&](int t0, int id) {
-        if (id >= 0) {
-            const int64_t at = (int64_t)id * a.c.heads + hk;
-            const int64_t base = (at * a.c.page + ((t0 + 16 * wave) & (a.c.page - 1))) * D;
-            const uint4* kp = reinterpret_cast<const uint4*>(a.c.k + base + kt * D + kj * (D / 4));
+        // without a page of the pool page 0 is loaded and not seen (with no pool at all no sequence has keys)
+        const bool there = (uint32_t)id < (uint32_t)a.c.pages;
+        const int64_t at = (int64_t)(there ? id : 0) * a.c.heads + hk;
+        const int64_t base = (at * a.c.page + ((t0 + 16 * wave) & (a.c.page - 1))) * D;
+        const uint4* kp = reinterpret_cast<const uint4*>(a.c.k + base + kt * D + kj * (D / 4));
 #pragma unroll
-            for (int w = 0; w < KW; ++w) rk[w] = kp[w];
+        for (int w = 0; w < KW; ++w) rk[w] = kp[w];
 #pragma unroll
-            for (int q = 0; q < 2; ++q) {
-                const uint2* vp = reinterpret_cast<const uint2*>(a.c.v + base + (h + 2 * q) * (4 * D) + i * VB);
+        for (int q = 0; q < 2; ++q) {
+            const uint2* vp = reinterpret_cast<const uint2*>(a.c.v + base + (h + 2 * q) * (4 * D) + i * VB);
 #pragma unroll
-                for (int w = 0; w < VB / 8; ++w) rv[q][w] = vp[w];
-            }
-            rs = make_float4(a.c.k_scale[at], a.c.v_scale[at], 0.0f, 1.0f);
-        } else {
-#pragma unroll
-            for (int w = 0; w < KW; ++w) rk[w] = make_uint4(0, 0, 0, 0);
-#pragma unroll
-            for (int q = 0; q < 2; ++q)
-#pragma unroll
-                for (int w = 0; w < VB / 8; ++w) rv[q][w] = make_uint2(0, 0);
-            rs = make_float4(0.0f, 1.0f, 0.0f, 0.0f);
+            for (int w = 0; w < VB / 8; ++w) rv[q][w] = vp[w];
         }
+        rs = make_float4(uniform_load(a.c.k_scale + at), uniform_load(a.c.v_scale + at), 0.0f, there ? 1.0f : 0.0f);
     };
     auto put = [&](Stage<D>& st) {
         uint8_t* k = st.k + (kj * (D / 32)) * Stage<D>::kPitchK + (16 * wave + kt) * 16;
