@@ -12,7 +12,7 @@ namespace {
 constexpr int kStep = 128;  // tokens of a step: four waves of 32
 
 // The work: units of kStep keys, numbered over (sequence, key/value head, tile
-// of R rows, step), cut into equal ranges, one for each of 2^lw workgroups,
+// of R rows, step), cut into equal ranges, one for each workgroup,
 // whatever the lengths are.  A (sequence, head, row tile) that lies in one range
 // is written out by its workgroup; one that is cut leaves a partial result (the
 // unnormalised output, M and l of each row) in each range's slot (2 w: the
@@ -34,21 +34,33 @@ __device__ __forceinline__ Units units_of(const AttentionArgs& a, int s) {
     return u;
 }
 
-// Range w of 2^lw: floor(w all / 2^lw), or one unit each while there are fewer
-// units than ranges.  range_of is the range that holds unit u.
-__device__ __forceinline__ int64_t range_start(int64_t all, int w, int lw) {
-    if (all >> lw == 0) return min((int64_t)w, all);
-    const int64_t r = all & (((int64_t)1 << lw) - 1);
-    return w * (all >> lw) + ((w * r) >> lw);
+// Workgroups of the few-row kernel that the chip holds at once, one range each.
+constexpr int resident(int D, int NQ) { return D == 256 ? 1 : D == 128 ? 2 : NQ == 1 ? 4 : 2; }
+constexpr int ways(int D, int R) { return 256 * resident(D, R / 16); }
+
+// Range w of W: floor(w all / W), or one unit each while there are fewer units
+// than ranges.  range_of is the range that holds unit u.
+template <int W>
+__device__ __forceinline__ int64_t range_start(int64_t all, int w) {
+    if (all < W) return min((int64_t)w, all);
+    const uint32_t r = (uint32_t)((uint64_t)all % W);
+    return w * (int64_t)((uint64_t)all / W) + (uint32_t)(w * r) / W;
 }
 
-__device__ __forceinline__ int range_of(int64_t all, int64_t u, int lw) {
-    return all >> lw == 0 ? (int)u : (int)((((u + 1) << lw) - 1) / all);
+template <int W>
+__device__ __forceinline__ int range_of(int64_t all, int64_t u) {
+    if (all < W) return (int)u;
+    if (all < (int64_t)0xffffffffu / W) return (int)((uint32_t)((u + 1) * W - 1) / (uint32_t)all);
+    return (int)(((u + 1) * W - 1) / all);
 }
 
 __device__ __forceinline__ int64_t shfl64(int64_t v, int lane) {
     const int lo = __shfl((int)v, lane), hi = __shfl((int)(v >> 32), lane);
     return (int64_t)hi << 32 | (uint32_t)lo;
+}
+
+__device__ __forceinline__ int64_t quotient(int64_t a, int b) {
+    return (uint64_t)a >> 32 == 0 ? (int64_t)((uint32_t)a / (uint32_t)b) : a / b;
 }
 
 // Inclusive sums over the workgroup's 256 threads, and the total.
@@ -67,10 +79,24 @@ __device__ __forceinline__ int64_t block_scan(int64_t v, int64_t* part, int64_t&
     return v;
 }
 
-// Partial results of a slot: R rows of D values, then M and l of each row.
+// The workspace: for each range two slots of R rows of D values, then M and l of
+// each row; then for each segment where its parts are: the slot of the first, and
+// the last range (-1: written out whole).
 template <int D, int R>
 __device__ __forceinline__ float* slot_of(const AttentionArgs& a, int64_t slot) {
     return a.ws + slot * (R * (D + 2));
+}
+
+template <int D, int R>
+__device__ __forceinline__ int2* parts_of(const AttentionArgs& a, int64_t item, int hk) {
+    return reinterpret_cast<int2*>(slot_of<D, R>(a, 2 * ways(D, R))) + item * a.c.heads + hk;
+}
+
+// The number of a sequence's first row tile.
+template <int R>
+__device__ __forceinline__ int64_t first_item(const AttentionArgs& a, int s) {
+    const int group = a.hq / a.c.heads;
+    return a.b.cu_q ? item_start(a.b, s, group, R, 1) : (int64_t)s * ((group + R - 1) / R);
 }
 
 template <int DT, int D>
@@ -95,8 +121,8 @@ __device__ __forceinline__ void write_row(const AttentionArgs& a, int64_t row, i
 // weights' operand of the value product as it stands.  The next tile's codes are
 // loaded while one is computed.
 template <int DT, int D, int NQ>
-__global__ __launch_bounds__(256, D < 256 && (D / 64) * NQ <= 4 ? 2 : 1) void k_attention_few(AttentionArgs a, int lw) {
-    constexpr int R = 16 * NQ, DL = D / 4, NC = D / 32, NT = D / 16, W4 = D / 64;
+__global__ __launch_bounds__(256, resident(D, NQ)) void k_attention_few(AttentionArgs a) {
+    constexpr int R = 16 * NQ, W = ways(D, R), DL = D / 4, NC = D / 32, NT = D / 16, W4 = D / 64;
     constexpr int kPitch = D + 4;
     __shared__ float so[4][16][kPitch];
     __shared__ float sM[4][R], sl[4][R];
@@ -114,8 +140,8 @@ __global__ __launch_bounds__(256, D < 256 && (D / 64) * NQ <= 4 ? 2 : 1) void k_
             incl = block_scan(mine, part, t);
             total += t;
         }
-        u0 = range_start(total, blockIdx.x, lw);
-        u1 = range_start(total, blockIdx.x + 1, lw);
+        u0 = range_start<W>(total, blockIdx.x);
+        u1 = range_start<W>(total, blockIdx.x + 1);
         if (u0 >= u1) return;
         int64_t before = 0;
         for (int base = 0; base < a.b.batch; base += 256) {
@@ -134,61 +160,128 @@ __global__ __launch_bounds__(256, D < 256 && (D / 64) * NQ <= 4 ? 2 : 1) void k_
         }
         __syncthreads();
     }
-    int s = __builtin_amdgcn_readfirstlane((int)found[0]);
-    int64_t from = found[1];  // the first unit of sequence s
-    bool first_segment = true;
-
-    while (u0 < u1) {
-        const Units un = units_of<R, true>(a, s);
-        const int64_t local = u0 - from;
-        if (local >= un.all) {
-            from += un.all;
-            if (++s >= a.b.batch) return;
-            continue;
+    // a segment of the range, or what of it the range holds: steps step0 .. step0 + steps - 1 of row tile `tile`
+    // of head hk of sequence s
+    struct Segment {
+        Units un;
+        int64_t from;  // the first unit of the sequence
+        int s, hk, tile, step0, steps;
+        int begin, end;  // this wave's first tile of 32 keys; the keys' end
+        const int32_t* table;
+    } sg;
+    sg.s = __builtin_amdgcn_readfirstlane((int)found[0]);
+    sg.from = found[1];
+    sg.un = units_of<R, true>(a, sg.s);
+    const int shift = __builtin_ctz(a.c.page);
+    auto find = [&](int64_t u) {  // the segment that holds unit u, at or behind the present one
+        while (u - sg.from >= sg.un.all) {
+            sg.from += sg.un.all;
+            sg.s = min(sg.s + 1, a.b.batch - 1);
+            sg.un = units_of<R, true>(a, sg.s);
+            if (sg.s == a.b.batch - 1) break;  // lengths that changed under the call: stay within the batch
         }
-        const int64_t seg = local / un.steps;
-        const int step0 = __builtin_amdgcn_readfirstlane((int)(local - seg * un.steps));
-        const int hk = __builtin_amdgcn_readfirstlane((int)(seg / un.tiles));
-        const int tile = (int)(seg - (int64_t)hk * un.tiles);
-        const int steps = __builtin_amdgcn_readfirstlane((int)min((int64_t)(un.steps - step0), u1 - u0));
+        const int64_t local = u - sg.from;
+        const int64_t seg = quotient(local, sg.un.steps);
+        sg.step0 = __builtin_amdgcn_readfirstlane((int)(local - seg * sg.un.steps));
+        sg.hk = min(__builtin_amdgcn_readfirstlane((int)quotient(seg, max(sg.un.tiles, 1))), a.c.heads - 1);
+        sg.tile = __builtin_amdgcn_readfirstlane((int)(seg - (int64_t)sg.hk * sg.un.tiles));
+        sg.steps = __builtin_amdgcn_readfirstlane((int)min((int64_t)(sg.un.steps - sg.step0), u1 - u));
+        sg.begin = sg.un.k0 + (sg.step0 * 4 + wave) * 32;
+        sg.end = min(sg.un.k0 + (sg.step0 + sg.steps) * kStep, sg.un.s.last + 1);
+        sg.table = a.b.page_table + (int64_t)sg.s * a.b.ldt;
+    };
 
-        // the tile's rows: queries as binary16 operands (bfloat16 ones scaled to the row's largest exponent, so
-        // that what binary16 cannot hold is below 2^-39 of the row's largest), the keys that each row sees
+    // a tile's two groups of 16 tokens: whether the table names a page of the pool for them (if not, page 0 is loaded
+    // and not seen: with no pool at all no sequence has keys), its scales and codes
+    struct Tile {
+        bool there[2];
+        float ks[2], vs[2];
+        uint4 k[2][W4], v[2][W4];
+    };
+    auto pages = [&](int t0, int (&id)[2]) {
+#pragma unroll
+        for (int u = 0; u < 2; ++u) {
+            const int t = t0 + 16 * u;
+            id[u] = t < sg.end ? uniform_load(sg.table + (t >> shift)) : -1;
+        }
+    };
+    auto load = [&](int t0, const int (&id)[2], Tile& x) {
+#pragma unroll
+        for (int u = 0; u < 2; ++u) {
+            x.there[u] = (uint32_t)id[u] < (uint32_t)a.c.pages;
+            const int64_t at = (int64_t)(x.there[u] ? id[u] : 0) * a.c.heads + sg.hk;
+            const int slot = (t0 + 16 * u) & (a.c.page - 1);
+            const int64_t base = (at * a.c.page + slot) * D;
+            const uint4* kp = reinterpret_cast<const uint4*>(a.c.k + base + i * D + g * DL);
+            const uint4* vp = reinterpret_cast<const uint4*>(a.c.v + base + g * (4 * D) + i * DL);
+#pragma unroll
+            for (int w = 0; w < W4; ++w) x.k[u][w] = kp[w];
+#pragma unroll
+            for (int w = 0; w < W4; ++w) x.v[u][w] = vp[w];
+            x.ks[u] = uniform_load(a.c.k_scale + at);
+            x.vs[u] = uniform_load(a.c.v_scale + at);
+        }
+    };
+    // what a segment begins with: its first tile, and its rows' queries
+    Tile x, y;
+    int id[2];
+    Raw8<DT> raw[NQ][DL / 8];
+    auto queries = [&]() {
+#pragma unroll
+        for (int n = 0; n < NQ; ++n) {
+            const int r = sg.tile * R + n * 16 + i;
+            const int tok = r / group, head = sg.hk * group + r - tok * group;
+            const uint16_t* row = reinterpret_cast<const uint16_t*>(a.q) + (int64_t)(sg.un.s.q.q0 + tok) * a.ldq +
+                                  (int64_t)head * D + g * DL;
+#pragma unroll
+            for (int c = 0; c < DL / 8; ++c) raw[n][c] = tok < sg.un.s.q.n ? load_raw8<DT>(row, c) : zero_raw8<DT>();
+        }
+    };
+    auto ahead = [&]() {
+        if (sg.begin < sg.end) {
+            pages(sg.begin, id);
+            load(sg.begin, id, x);
+            pages(sg.begin + kStep, id);
+        }
+        if (NQ == 1) queries();  // two row tiles have no registers left for it
+    };
+
+    bool first_segment = true;
+    find(u0);
+    ahead();
+    for (;;) {
+        if (NQ > 1) queries();
+        // the tile's rows: queries as binary16 operands (bfloat16 ones scaled to the row's largest exponent, so that
+        // what binary16 cannot hold is below 2^-39 of the row's largest), the keys that each row sees
         v8h qf[NQ][NC];
-        int lo[NQ], hi[NQ], pos[NQ], lo_max = 0, hi_min = INT32_MAX;
+        int lo[NQ], hi[NQ], pos[NQ];
         float f[NQ], slope[NQ], M[NQ], l[NQ];
         v4f o[NQ][NT];
 #pragma unroll
         for (int n = 0; n < NQ; ++n) {
-            const int r = tile * R + n * 16 + i;
-            const int tok = r / group, head = hk * group + r - tok * group;
-            const bool valid = tok < un.s.q.n;
-            pos[n] = un.s.q.p0 + tok;
+            const int r = sg.tile * R + n * 16 + i;
+            const int tok = r / group, head = sg.hk * group + r - tok * group;
+            pos[n] = sg.un.s.q.p0 + tok;
             lo[n] = 1;
             hi[n] = 0;
-            float top = 0.0f;
-            float x[DL];
-            if (valid) {
-                row_keys(a, un.s, pos[n], lo[n], hi[n]);
-                const uint16_t* row = reinterpret_cast<const uint16_t*>(a.q) + (int64_t)(un.s.q.q0 + tok) * a.ldq +
-                                      (int64_t)head * D + g * DL;
+            slope[n] = 0.0f;
+            if (tok < sg.un.s.q.n) {
+                row_keys(a, sg.un.s, pos[n], lo[n], hi[n]);
+                if (a.slopes) slope[n] = a.slopes[head] * kLog2e;
+            }
+            float top = 0.0f, v[DL];
 #pragma unroll
-                for (int c = 0; c < DL / 8; ++c) {
-                    float v[8];
-                    widen8<DT>(load_raw8<DT>(row, c), v);
+            for (int c = 0; c < DL / 8; ++c) {
+                float w[8];
+                widen8<DT>(raw[n][c], w);
 #pragma unroll
-                    for (int j = 0; j < 8; ++j) x[8 * c + j] = v[j];
+                for (int j = 0; j < 8; ++j) {
+                    v[8 * c + j] = w[j];
+                    top = fmaxf(top, fabsf(w[j]));
                 }
-                lo_max = max(lo_max, lo[n]);
-                hi_min = min(hi_min, hi[n]);
-            } else {
-#pragma unroll
-                for (int j = 0; j < DL; ++j) x[j] = 0.0f;
             }
             int e = 14;
             if constexpr (DT == kBF16) {
-#pragma unroll
-                for (int j = 0; j < DL; ++j) top = fmaxf(top, fabsf(x[j]));
                 top = fmaxf(top, __shfl_xor(top, 16));
                 top = fmaxf(top, __shfl_xor(top, 32));
                 e = top > 0.0f && top < INFINITY ? __builtin_amdgcn_frexp_expf(top) : 14;
@@ -197,59 +290,24 @@ __global__ __launch_bounds__(256, D < 256 && (D / 64) * NQ <= 4 ? 2 : 1) void k_
             for (int c = 0; c < NC; ++c)
 #pragma unroll
                 for (int j = 0; j < 8; ++j)
-                    qf[n][c][j] = (_Float16)(DT == kBF16 ? ldexpf(x[8 * c + j], 14 - e) : x[8 * c + j]);
+                    qf[n][c][j] = (_Float16)(DT == kBF16 ? ldexpf(v[8 * c + j], 14 - e) : v[8 * c + j]);
             f[n] = ldexpf(a.softcap > 0.0f ? 2.0f * kLog2e / a.softcap * a.scale : kLog2e * a.scale, e - 14);
-            slope[n] = a.slopes && valid ? a.slopes[head] * kLog2e : 0.0f;
             M[n] = kNone;
             l[n] = 0.0f;
 #pragma unroll
             for (int t = 0; t < NT; ++t) o[n][t] = (v4f){0.0f, 0.0f, 0.0f, 0.0f};
         }
-#pragma unroll
-        for (int m = 8; m >= 1; m >>= 1) {
-            lo_max = max(lo_max, __shfl_xor(lo_max, m));
-            hi_min = min(hi_min, __shfl_xor(hi_min, m));
+        // keys from lo_max to hi_min are seen by all of the tile's rows: the bounds grow with the position
+        int lo_max, hi_min, unused;
+        {
+            const int rows = sg.un.s.q.n * group, r0 = sg.tile * R;
+            row_keys(a, sg.un.s, sg.un.s.q.p0 + r0 / group, unused, hi_min);
+            row_keys(a, sg.un.s, sg.un.s.q.p0 + (min(r0 + R, rows) - 1) / group, lo_max, unused);
+            lo_max = __builtin_amdgcn_readfirstlane(lo_max);
+            hi_min = __builtin_amdgcn_readfirstlane(hi_min);
         }
-        lo_max = __builtin_amdgcn_readfirstlane(lo_max);
-        hi_min = __builtin_amdgcn_readfirstlane(hi_min);
         const float cap2 = a.softcap * kLog2e;
 
-        const int begin = un.k0 + (step0 * 4 + wave) * 32;
-        const int end = min(un.k0 + (step0 + steps) * kStep, un.s.last + 1);
-        const int32_t* table = a.b.page_table + (int64_t)s * a.b.ldt;
-        const int shift = __builtin_ctz(a.c.page);
-
-        // a tile's two groups of 16 tokens: whether the table names a page of the pool for them (if not, page 0 is
-        // loaded and not seen: with no pool at all no sequence has keys), its scales and codes
-        struct Tile {
-            bool there[2];
-            float ks[2], vs[2];
-            uint4 k[2][W4], v[2][W4];
-        };
-        auto pages = [&](int t0, int (&id)[2]) {
-#pragma unroll
-            for (int u = 0; u < 2; ++u) {
-                const int t = t0 + 16 * u;
-                id[u] = t < end ? uniform_load(table + (t >> shift)) : -1;
-            }
-        };
-        auto load = [&](int t0, const int (&id)[2], Tile& x) {
-#pragma unroll
-            for (int u = 0; u < 2; ++u) {
-                x.there[u] = (uint32_t)id[u] < (uint32_t)a.c.pages;
-                const int64_t at = (int64_t)(x.there[u] ? id[u] : 0) * a.c.heads + hk;
-                const int slot = (t0 + 16 * u) & (a.c.page - 1);
-                const int64_t base = (at * a.c.page + slot) * D;
-                const uint4* kp = reinterpret_cast<const uint4*>(a.c.k + base + i * D + g * DL);
-                const uint4* vp = reinterpret_cast<const uint4*>(a.c.v + base + g * (4 * D) + i * DL);
-#pragma unroll
-                for (int w = 0; w < W4; ++w) x.k[u][w] = kp[w];
-#pragma unroll
-                for (int w = 0; w < W4; ++w) x.v[u][w] = vp[w];
-                x.ks[u] = uniform_load(a.c.k_scale + at);
-                x.vs[u] = uniform_load(a.c.v_scale + at);
-            }
-        };
         auto compute = [&](int t0, const Tile& x) {
             v4f z[2][NQ];
             float lv[2], rv[2];
@@ -339,21 +397,16 @@ __global__ __launch_bounds__(256, D < 256 && (D / 64) * NQ <= 4 ? 2 : 1) void k_
             }
         };
 
-        if (begin < end) {
-            int id[2];
-            Tile x, y;
-            pages(begin, id);
-            load(begin, id, x);
-            pages(begin + kStep, id);
-            for (int t0 = begin;; t0 += 2 * kStep) {
-                const bool more = t0 + kStep < end;
+        if (sg.begin < sg.end) {
+            for (int t0 = sg.begin;; t0 += 2 * kStep) {
+                const bool more = t0 + kStep < sg.end;
                 if (more) {
                     load(t0 + kStep, id, y);
                     pages(t0 + 2 * kStep, id);
                 }
                 compute(t0, x);
                 if (!more) break;
-                const bool even = t0 + 2 * kStep < end;
+                const bool even = t0 + 2 * kStep < sg.end;
                 if (even) {
                     load(t0 + 2 * kStep, id, x);
                     pages(t0 + 3 * kStep, id);
@@ -363,8 +416,18 @@ __global__ __launch_bounds__(256, D < 256 && (D / 64) * NQ <= 4 ? 2 : 1) void k_
             }
         }
 
+        // the next segment's loads run while this one is written out
+        const int s = sg.s, hk = sg.hk, tile = sg.tile, step0 = sg.step0, steps = sg.steps;
+        const int all_steps = sg.un.steps, n_rows = sg.un.s.q.n, q0 = sg.un.s.q.q0;
+        const int64_t u = u0;
+        u0 += steps;
+        if (u0 < u1) {
+            find(u0);
+            ahead();
+        }
+
         // join the four waves, 16 rows at a time
-        const bool whole = steps == un.steps;
+        const bool whole = steps == all_steps;
         const int64_t slot = 2 * (int64_t)blockIdx.x + (first_segment ? 0 : 1);
         __syncthreads();
 #pragma unroll
@@ -393,7 +456,7 @@ __global__ __launch_bounds__(256, D < 256 && (D / 64) * NQ <= 4 ? 2 : 1) void k_
                 const int j = c / (D / 8), d = c % (D / 8) * 8;
                 const int rr = tile * R + n * 16 + j;
                 const int tok = rr / group;
-                if (tok < un.s.q.n) {
+                if (tok < n_rows) {
                     const float Mj = fmaxf(fmaxf(sM[0][n * 16 + j], sM[1][n * 16 + j]),
                                            fmaxf(sM[2][n * 16 + j], sM[3][n * 16 + j]));
                     float lj = 0.0f, v[8] = {};
@@ -404,7 +467,7 @@ __global__ __launch_bounds__(256, D < 256 && (D / 64) * NQ <= 4 ? 2 : 1) void k_
                         for (int k = 0; k < 8; ++k) v[k] += so[w][j][d + k];
                     }
                     if (whole) {
-                        write_row<DT, D>(a, un.s.q.q0 + tok, hk * group + rr - tok * group, d, v, Mj, lj);
+                        write_row<DT, D>(a, q0 + tok, hk * group + rr - tok * group, d, v, Mj, lj);
                     } else {
                         float* p = slot_of<D, R>(a, slot);
                         float4* q = reinterpret_cast<float4*>(p + (n * 16 + j) * D + d);
@@ -418,8 +481,12 @@ __global__ __launch_bounds__(256, D < 256 && (D / 64) * NQ <= 4 ? 2 : 1) void k_
                 }
             }
         }
+        if (step0 == 0 && tid == 0) {
+            const int last = whole ? -1 : range_of<W>(total, u + all_steps - 1);
+            *parts_of<D, R>(a, first_item<R>(a, s) + tile, hk) = make_int2((int)slot, last);
+        }
+        if (u0 >= u1) break;
         first_segment = false;
-        u0 += steps;
     }
 }
 
@@ -427,46 +494,25 @@ __global__ __launch_bounds__(256, D < 256 && (D / 64) * NQ <= 4 ? 2 : 1) void k_
 // (row tile of a sequence, head; row), D / 8 threads for each of 2048 / D parts
 // at a time.
 template <int DT, int D, int R>
-__global__ __launch_bounds__(256) void k_attention_join(AttentionArgs a, int lw) {
+__global__ __launch_bounds__(256) void k_attention_join(AttentionArgs a) {
     constexpr int NP = 2048 / D;  // parts taken at once
-    __shared__ int64_t part[4];
     __shared__ float sm[NP], sl[NP], so[NP][D];
     const int tid = threadIdx.x, group = a.hq / a.c.heads;
     const int64_t item = blockIdx.x / a.c.heads;
     const int hk = (int)(blockIdx.x - item * a.c.heads), j = blockIdx.y;
-    int s;
-    int64_t tile;
-    if (a.b.cu_q) {
-        s = item_seq(a.b, item, group, R, 1);
-        tile = item - item_start(a.b, s, group, R, 1);
-    } else {
-        const int tiles = (group + R - 1) / R;
-        s = (int)(item / tiles);
-        tile = item - (int64_t)s * tiles;
-    }
-    const Units un = units_of<R, true>(a, s);
-    const int64_t rr = tile * R + j;
-    if (tile >= un.tiles || rr >= (int64_t)un.s.q.n * group) return;
-
-    int64_t before = 0, total = 0, t;
-    for (int b = tid; b < a.b.batch; b += 256) {
-        const int64_t u = units_of<R>(a, b).all;
-        total += u;
-        if (b < s) before += u;
-    }
-    block_scan(before, part, t);
-    before = t;
-    block_scan(total, part, t);
-    total = t;
-    const int64_t S = before + ((int64_t)hk * un.tiles + tile) * un.steps;
-    const int w0 = range_of(total, S, lw), w1 = range_of(total, S + un.steps - 1, lw);
-    if (w0 == w1) return;  // one range held it whole
-    const bool begins = range_start(total, w0, lw) >= S;
+    const int2 parts = *parts_of<D, R>(a, item, hk);
+    const int s = a.b.cu_q ? item_seq(a.b, item, group, R, 1) : (int)(item / ((group + R - 1) / R));
+    const KvSeq q = kv_seq<true>(a.b, s);
+    const int64_t rr = (item - first_item<R>(a, s)) * R + j;
+    if (rr >= (int64_t)q.n * group) return;  // also: no tile, whose parts nobody wrote
+    const int w0 = parts.x >> 1, w1 = parts.y;
+    if (w1 < 0) return;
 
     const int p = tid / (D / 8), d = tid % (D / 8) * 8;
     float M = kNone, l = 0.0f, o[8] = {};
+#pragma unroll 4
     for (int w = w0 + p; w <= w1; w += NP) {
-        const float* x = slot_of<D, R>(a, 2 * (int64_t)w + (w == w0 && !begins ? 1 : 0));
+        const float* x = slot_of<D, R>(a, w == w0 ? parts.x : 2 * (int64_t)w);
         const float Mw = x[R * D + j], lw_ = x[R * D + R + j];
         const float4 v0 = *reinterpret_cast<const float4*>(x + j * D + d);
         const float4 v1 = *reinterpret_cast<const float4*>(x + j * D + d + 4);
@@ -498,10 +544,8 @@ __global__ __launch_bounds__(256) void k_attention_join(AttentionArgs a, int lw)
         for (int k = 0; k < 8; ++k) o[k] += so[w][d + k] * keep;
     }
     const int64_t tok = rr / group;
-    write_row<DT, D>(a, un.s.q.q0 + tok, hk * group + (int)(rr - tok * group), d, o, top, l);
+    write_row<DT, D>(a, q.q0 + tok, hk * group + (int)(rr - tok * group), d, o, top, l);
 }
-
-constexpr int kWaysLog2 = 9;  // ranges of the few-row kernel
 
 // 16-row tiles of the few-row kernel for a batch: enough for the rows that a
 // sequence has on average; 0: the prompt kernel.
@@ -510,9 +554,12 @@ int row_tiles(int64_t tokens, int64_t batch, int hq, int hkv, int dim) {
     return rows <= 16 ? 1 : rows <= 32 ? 2 : 0;
 }
 
+int64_t few_items(int64_t tokens, int64_t batch, int group, int R, bool ragged) {
+    return ragged ? tokens * group / R + batch : batch * ((group + R - 1) / R);
+}
+
 int64_t few_items(const AttentionArgs& a, int R) {
-    const int group = a.hq / a.c.heads;
-    return a.b.cu_q ? (int64_t)a.b.tokens * group / R + a.b.batch : (int64_t)a.b.batch * ((group + R - 1) / R);
+    return few_items(a.b.tokens, a.b.batch, a.hq / a.c.heads, R, a.b.cu_q);
 }
 
 // What the table can name bounds the parts that are worth cutting.
@@ -526,10 +573,10 @@ template <int DT, int D, int NQ>
 void launch_few(const AttentionArgs& a, hipStream_t st) {
     constexpr int R = 16 * NQ;
     const int group = a.hq / a.c.heads;
-    const int64_t items = few_items(a, R);
-    k_attention_few<DT, D, NQ><<<1 << kWaysLog2, 256, 0, st>>>(a, kWaysLog2);
-    k_attention_join<DT, D, R><<<dim3((uint32_t)(items * a.c.heads), a.b.cu_q ? R : std::min(R, group)), 256, 0, st>>>(
-        a, kWaysLog2);
+    k_attention_few<DT, D, NQ><<<ways(D, R), 256, 0, st>>>(a);
+    if ((int64_t)a.b.max_pages * a.c.page > kStep)  // else no segment has a second step to be cut at
+        k_attention_join<DT, D, R><<<dim3((uint32_t)(few_items(a, R) * a.c.heads), a.b.cu_q ? R : std::min(R, group)),
+                                     256, 0, st>>>(a);
 }
 
 template <int DT, int D>
@@ -542,7 +589,11 @@ void launch(const AttentionArgs& a, int tiles, hipStream_t st) {
 
 size_t attention_workspace(int64_t tokens, int64_t batch, int hq, int hkv, int dim) {
     const int tiles = row_tiles(tokens, batch, hq, hkv, dim);
-    if (tiles > 0) return (size_t(2) << kWaysLog2) * (16 * tiles) * (dim + 2) * sizeof(float);
+    if (tiles > 0) {
+        const int group = hq / hkv, R = 16 * tiles;
+        const int64_t items = std::max(few_items(tokens, batch, group, R, true), few_items(tokens, batch, group, R, false));
+        return (size_t)2 * ways(dim, R) * R * (dim + 2) * sizeof(float) + items * hkv * sizeof(int2);
+    }
     const int splits = attention_prompt_splits(tokens, hq, hkv, dim);
     return splits > 1 ? (size_t)splits * tokens * hq * (dim + 2) * sizeof(float) : 0;
 }
