@@ -8,8 +8,8 @@ is raised.
 """
 from __future__ import annotations
 
-import contextlib
 import ctypes
+import functools
 import os
 import re
 
@@ -603,7 +603,7 @@ class KVCache:
     k_scale and v_scale [pages, heads] float32, all contiguous on one device.
     """
 
-    __slots__ = ("k", "v", "k_scale", "v_scale", "pages", "heads", "page", "dim", "device", "_c", "_ref")
+    __slots__ = ("k", "v", "k_scale", "v_scale", "pages", "heads", "page", "dim", "device", "index", "_c", "_ref")
 
     def __init__(self, k: torch.Tensor, v: torch.Tensor, k_scale: torch.Tensor, v_scale: torch.Tensor):
         if k.dim() != 4:
@@ -617,6 +617,7 @@ class KVCache:
             raise ValueError("the cache's tensors must be on one device")
         self.k, self.v, self.k_scale, self.v_scale = k, v, k_scale, v_scale
         self.pages, self.heads, self.page, self.dim, self.device = pages, heads, page, dim, k.device
+        self.index = k.get_device()
         self._c = _KVCacheC(k.data_ptr(), v.data_ptr(), k_scale.data_ptr(), v_scale.data_ptr(), pages, heads, page, dim)
         self._ref = ctypes.byref(self._c)
 
@@ -635,7 +636,7 @@ class KVBatch:
     tensors are read when the calls run on the device, so that a program may
     update them in place between calls (or between replays of a graph)."""
 
-    __slots__ = ("page_table", "seq_len", "cu_q", "batch", "device", "_c", "_ref")
+    __slots__ = ("page_table", "seq_len", "cu_q", "batch", "device", "index", "_c", "_ref")
 
     def __init__(self, page_table: torch.Tensor, seq_len: torch.Tensor, cu_q: torch.Tensor | None = None):
         _check_mat(page_table, "page_table", (torch.int32,))
@@ -646,15 +647,15 @@ class KVBatch:
         if page_table.device != seq_len.device or (cu_q is not None and cu_q.device != seq_len.device):
             raise ValueError("the batch's tensors must be on one device")
         self.page_table, self.seq_len, self.cu_q, self.batch = page_table, seq_len, cu_q, batch
-        self.device = seq_len.device
+        self.device, self.index = seq_len.device, seq_len.get_device()
         self._c = _KVBatchC(page_table.data_ptr(), _ld(page_table), seq_len.data_ptr(),
                             cu_q.data_ptr() if cu_q is not None else None, batch, max_pages)
         self._ref = ctypes.byref(self._c)
 
 
-def _check_kv_rows(t, name, cache, batch, heads=None, dtype=None):
+def _check_kv_rows(t, name, cache, heads=None, dtype=None):
     """A [tokens, heads, dim] operand, the heads of a row side by side -> its row pitch."""
-    if t.device != cache.device or t.device != batch.device:
+    if t.get_device() != cache.index:
         raise ValueError(f"{name}, the cache and the batch must be on one device")
     if t.dtype not in _HALF or (dtype is not None and t.dtype != dtype):
         raise ValueError(f"{name}: unsupported dtype {t.dtype}")
@@ -668,11 +669,15 @@ def _check_kv_rows(t, name, cache, batch, heads=None, dtype=None):
     return stride[0] if rows > 1 else shape[1] * shape[2]
 
 
-def _on(device):
-    """The device's current stream, with the device current (its kernels are launched there)."""
-    if device.index is not None and device.index != torch.cuda.current_device():
-        return torch.cuda.device(device)
-    return contextlib.nullcontext()
+def _kv_call(fn, index: int, *args) -> None:
+    """A key/value call on the current stream of device `index`, with that device current.  These calls run once a
+    layer and token, where the host's microseconds count: the raw stream is asked for, no stream object made."""
+    if index != torch._C._cuda_getDevice():
+        with torch.cuda.device(index):
+            return _kv_call(fn, index, *args)
+    st = getattr(lib(), fn)(*args, torch._C._cuda_getCurrentRawStream(index))
+    if st != 0:
+        raise PdqError(fn, st)
 
 
 def kv_append(k, v, cache: KVCache, batch: KVBatch, q=None, cos=None, sin=None, interleaved: bool = False,
@@ -682,42 +687,46 @@ def kv_append(k, v, cache: KVCache, batch: KVBatch, q=None, cos=None, sin=None, 
 
     k, v: [tokens, heads, dim] bf16 or f16; q: [tokens, hq, dim]; cos, sin: float32
     [positions, rot / 2] (None: no rotation)."""
-    ldk = _check_kv_rows(k, "k", cache, batch, cache.heads)
+    index = cache.index
+    if batch.index != index:
+        raise ValueError("the cache and the batch must be on one device")
+    ldk = _check_kv_rows(k, "k", cache, cache.heads)
     tokens, dtype = k.shape[0], k.dtype
-    ldv = _check_kv_rows(v, "v", cache, batch, cache.heads, dtype)
+    ldv = _check_kv_rows(v, "v", cache, cache.heads, dtype)
     if v.shape[0] != tokens:
         raise ValueError("k and v must have the same rows")
     if (cos is None) != (sin is None) or (q is not None and cos is None):
         raise ValueError("a rotation needs both tables, and q is there to be rotated")
     positions = rot = hq = ldq = ldqo = 0
     if cos is not None:
-        _check_dense(cos, "cos", torch.float32)
-        _check_dense(sin, "sin", torch.float32, cos.shape)
-        if cos.dim() != 2 or cos.device != k.device or sin.device != k.device:
-            raise ValueError("cos and sin must be [positions, rot / 2] on k's device")
-        positions, rot = cos.shape[0], 2 * cos.shape[1]
+        if (cos.dtype != torch.float32 or sin.dtype != torch.float32 or cos.dim() != 2 or cos.shape != sin.shape
+                or cos.get_device() != index or sin.get_device() != index or not cos.is_contiguous()
+                or not sin.is_contiguous()):
+            raise ValueError("cos and sin must be contiguous float32 [positions, rot / 2] on k's device")
+        positions, rot = cos.shape
+        rot *= 2
     if q is not None:
-        ldq = _check_kv_rows(q, "q", cache, batch, None, dtype)
+        ldq = _check_kv_rows(q, "q", cache, None, dtype)
         if q.shape[0] != tokens:
             raise ValueError("q and k must have the same rows")
         hq = q.shape[1]
         if q_out is None:
-            q_out = torch.empty((tokens, hq, cache.dim), dtype=dtype, device=k.device)
+            q_out = torch.empty((tokens, hq, cache.dim), dtype=dtype, device=cache.device)
             ldqo = hq * cache.dim
         else:
-            ldqo = _check_kv_rows(q_out, "q_out", cache, batch, hq, dtype)
+            ldqo = _check_kv_rows(q_out, "q_out", cache, hq, dtype)
             if q_out.shape[0] != tokens:
                 raise ValueError("q_out and q must have the same rows")
     elif q_out is not None:
         raise ValueError("q_out without q")
-    with _on(k.device):
-        _call("pdq_kv_append", k.data_ptr(), v.data_ptr(), q.data_ptr() if q is not None else None, _DT[dtype], tokens,
-              hq, ldk, ldv, ldq, cos.data_ptr() if cos is not None else None,
-              sin.data_ptr() if sin is not None else None, positions, rot, int(interleaved), cache._ref, batch._ref,
-              q_out.data_ptr() if q_out is not None else None, ldqo, torch.cuda.current_stream(k.device).cuda_stream)
+    _kv_call("pdq_kv_append", index, k.data_ptr(), v.data_ptr(), q.data_ptr() if q is not None else None, _DT[dtype],
+             tokens, hq, ldk, ldv, ldq, cos.data_ptr() if cos is not None else None,
+             sin.data_ptr() if sin is not None else None, positions, rot, 1 if interleaved else 0, cache._ref, batch._ref,
+             q_out.data_ptr() if q_out is not None else None, ldqo)
     return q_out
 
 
+@functools.lru_cache(maxsize=4096)
 def kv_attention_workspace_bytes(tokens: int, batch: int, hq: int, heads: int, dim: int) -> int:
     return int(lib().pdq_kv_attention_workspace(tokens, batch, hq, heads, dim))
 
@@ -731,44 +740,47 @@ def kv_attention(q, cache: KVCache, batch: KVBatch, scale: float | None = None, 
     scale: 1 / sqrt(dim) by default; softcap > 0: scores capped by softcap *
     tanh(z / softcap); window > 0: the last window keys; alibi_slopes float32 [hq]:
     a bias by distance; prefix_len int32 [batch]: tokens that every row sees."""
-    ldq = _check_kv_rows(q, "q", cache, batch)
+    index = cache.index
+    if batch.index != index:
+        raise ValueError("the cache and the batch must be on one device")
+    ldq = _check_kv_rows(q, "q", cache)
     tokens, hq, dim = q.shape
-    dev = q.device
+    dev = cache.device
     if alibi_slopes is not None:
         _check_dense(alibi_slopes, "alibi_slopes", torch.float32, (hq,))
-        if alibi_slopes.device != dev:
+        if alibi_slopes.get_device() != index:
             raise ValueError("alibi_slopes must be on q's device")
     if prefix_len is not None:
         _check_dense(prefix_len, "prefix_len", torch.int32, (batch.batch,))
-        if prefix_len.device != dev:
+        if prefix_len.get_device() != index:
             raise ValueError("prefix_len must be on q's device")
     if out is None:
         y = torch.empty((tokens, hq, dim), dtype=q.dtype, device=dev)
         ldy = hq * dim
     else:
         y = out
-        ldy = _check_kv_rows(y, "out", cache, batch, hq, q.dtype)
+        ldy = _check_kv_rows(y, "out", cache, hq, q.dtype)
         if y.shape[0] != tokens:
             raise ValueError("out and q must have the same rows")
     if lse is not None:
         _check_dense(lse, "lse", torch.float32, (tokens, hq))
-        if lse.device != dev:
+        if lse.get_device() != index:
             raise ValueError("lse must be on q's device")
     elif want_lse:
         lse = torch.empty((tokens, hq), dtype=torch.float32, device=dev)
-    need = int(lib().pdq_kv_attention_workspace(tokens, batch.batch, hq, cache.heads, dim))
+    size = 0
     if workspace is None:
-        if need:
-            workspace = torch.empty(need, dtype=torch.uint8, device=dev)
+        size = kv_attention_workspace_bytes(tokens, batch.batch, hq, cache.heads, dim)
+        if size:
+            workspace = torch.empty(size, dtype=torch.uint8, device=dev)
     else:
         _check_dense(workspace, "workspace", torch.uint8)
-        if workspace.device != dev:
+        if workspace.get_device() != index:
             raise ValueError("workspace must be on q's device")
-    with _on(dev):
-        _call("pdq_kv_attention", q.data_ptr(), _DT[q.dtype], tokens, hq, ldq, cache._ref, batch._ref,
-              dim ** -0.5 if scale is None else float(scale), float(softcap), int(window),
-              alibi_slopes.data_ptr() if alibi_slopes is not None else None,
-              prefix_len.data_ptr() if prefix_len is not None else None, y.data_ptr(), ldy,
-              lse.data_ptr() if lse is not None else None, workspace.data_ptr() if workspace is not None else None,
-              workspace.numel() if workspace is not None else 0, torch.cuda.current_stream(dev).cuda_stream)
+        size = workspace.numel()
+    _kv_call("pdq_kv_attention", index, q.data_ptr(), _DT[q.dtype], tokens, hq, ldq, cache._ref, batch._ref,
+             dim ** -0.5 if scale is None else scale, softcap, window,
+             alibi_slopes.data_ptr() if alibi_slopes is not None else None,
+             prefix_len.data_ptr() if prefix_len is not None else None, y.data_ptr(), ldy,
+             lse.data_ptr() if lse is not None else None, workspace.data_ptr() if size else None, size)
     return dict(y=y, lse=lse)
