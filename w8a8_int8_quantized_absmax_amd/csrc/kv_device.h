@@ -73,22 +73,20 @@ __device__ __forceinline__ int item_seq(const KvBatch& b, int64_t w, int mul, in
     return __builtin_amdgcn_readfirstlane(lo);
 }
 
-// The sequence of row t, by one thread.
+// The sequence of row t, the same in the whole wavefront: the last one that
+// begins at or before it, 64 candidates a step.
 __device__ __forceinline__ int row_seq(const KvBatch& b, int t) {
     if (!b.cu_q) return t;
-    int lo = 0, hi = b.batch;  // the last s with cu_q[s] <= t
-    while (hi - lo > 1) {
-        const int mid = (lo + hi) >> 1;
-        if (b.cu_q[mid] <= t) lo = mid;
-        else hi = mid;
+    const int lane = threadIdx.x & 63;
+    int lo = 0, n = b.batch;
+    while (n > 1) {
+        const int step = (n + 63) / 64;
+        const bool in = lane * step < n && b.cu_q[lo + lane * step] <= t;
+        const int k = max(__popcll(__ballot(in)), 1) - 1;
+        lo += k * step;
+        n = min(step, n - k * step);
     }
-    return lo;
-}
-
-// A page's number, or -1 where the table names none of the pool.
-__device__ __forceinline__ int kv_page(const KvCache& c, const KvBatch& b, int s, int j) {
-    const int id = b.page_table[(int64_t)s * b.ldt + j];
-    return (uint32_t)id < (uint32_t)c.pages ? id : -1;
+    return __builtin_amdgcn_readfirstlane(lo);
 }
 
 }  // namespace pdq
