@@ -10,35 +10,52 @@ namespace pdq {
 
 namespace {
 
-constexpr int kRows = 128;  // rows of a workgroup: four waves of 32
-constexpr int kKeys = 64;   // keys of a step
+constexpr int kKeys = 64;  // keys of a step
+constexpr float kMost = 0x1p14f;  // a sum of eight weights beyond which M moves
+
+// Waves of a workgroup, 32 rows each.  Eight share the conversion of a step's
+// codes between them and fill a compute unit (two to a SIMD, 256 registers); with
+// 256 channels a wave needs more registers than that, and with 64 there is room
+// for three smaller workgroups.
+constexpr int waves(int D) { return D == 128 ? 8 : 4; }
+constexpr int per_simd(int D) { return D == 256 ? 1 : D == 128 ? 2 : 3; }
+constexpr int tile_rows(int D) { return 32 * waves(D); }
 
 // LDS of one step's operands, in 16-byte pieces of 8 binary16 values.
 // K: piece (c, t) = channels 8 c .. 8 c + 7 of token t.  V: piece (2 u + h, d) =
-// channel (D / 32) (d % 32) + d / 32 of the tokens 4 h .. 4 h + 3 and 8 + 4 h .. 8 +
-// 4 h + 3 of the u-th 16 tokens, the order in which a lane of half h holds its
+// channel NT m + t (NT = D / 32, d = 32 t + m) of the tokens 4 h .. 4 h + 3 and 8 + 4 h ..
+// 8 + 4 h + 3 of the u-th 16 tokens, the order in which a lane of half h holds its
 // weights.  A lane of a product reads the piece of its own row, a whole half wave
-// 512 contiguous bytes; rows of pieces are padded so that the conversion's
-// writes (four lanes to a token) fall into different banks too.
+// 512 contiguous bytes; the paddings let the conversion's writes fall into
+// different banks too.
 template <int D>
-struct Stage {
-    static constexpr int kPitchK = kKeys * 16 + (D == 64 ? 32 : 16), kPitchV = D * 16 + 16;
-    uint8_t k[D / 8 * kPitchK];
-    uint8_t v[8 * kPitchV];
-    float4 scale[4];  // of each 16 tokens: S_k (0 without a page), log2 S_v, 1 / S_v, 0 or 1: a page is there
+struct KeyStage {
+    static constexpr int kPitch = kKeys * 16 + (D == 64 ? 32 : 16);
+    uint8_t at[D / 8 * kPitch];
+};
+template <int D>
+struct ValueStage {
+    static constexpr int kSkew = D == 128 ? 128 : 0;  // behind every second t
+    static constexpr int kPitch = D * 16 + (D / 64 - 1) * kSkew + 16;
+    uint8_t at[8 * kPitch];
+    float4 scale[4];  // of each 16 tokens: S_k, log2 S_v, 1 / S_v, 0 or 1: a page is there
+    static __device__ __forceinline__ int piece(int t, int m) { return t * 512 + (t >> 1) * kSkew + m * 16; }
 };
 
-// One workgroup of four waves takes kRows rows (token, query head of the group)
-// of one key/value head over a part of their keys.  Scores are computed
-// transposed, keys x rows, in 32x32x16 products, so that a row's scores lie in
-// one lane (and the one 32 lanes on) and its weights are the operand of the
-// value product as they stand; the output is accumulated transposed too.  Each
-// step's codes are loaded a step ahead, converted once for the four waves and
-// staged in one of two LDS buffers: one barrier a step.
-template <int DT, int D>
-__global__ __launch_bounds__(256, D <= 128 ? 2 : 1) void k_attention_prompt(AttentionArgs a, int64_t items, int splits) {
-    constexpr int NC = D / 16, NT = D / 32, KW = D / 64, VB = D / 8;  // VB: bytes of a lane's V channels of a quad
-    __shared__ Stage<D> stage[2];
+// One workgroup takes tile_rows(D) rows (token, query head of the group) of one
+// key/value head over a part of their keys.  Scores are computed transposed, keys
+// x rows, in 32x32x16 products, so that a row's scores lie in one lane (and the one
+// 32 lanes on) and its weights are the operand of the value product as they stand;
+// the output is accumulated transposed too.  Codes are loaded ahead, converted once
+// for all waves and staged in double-buffered LDS, one barrier a step; a step
+// computes the next step's scores beside its own softmax, so that the matrix and
+// the vector units both have work.  OPT: softcap or slopes are given.
+template <int DT, int D, bool OPT>
+__global__ __launch_bounds__(64 * waves(D), per_simd(D)) void k_attention_prompt(AttentionArgs a, int64_t items, int splits) {
+    constexpr int NW = waves(D), kRows = tile_rows(D), NC = D / 16, NT = D / 32;
+    constexpr int KB = D / NW, VD = D / (8 * NW);  // bytes of K, channels of V that a thread brings
+    __shared__ KeyStage<D> ks[2];
+    __shared__ ValueStage<D> vs[2];
     const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int i = lane & 31, h = lane >> 5;
     const int group = a.hq / a.c.heads;
@@ -69,7 +86,7 @@ __global__ __launch_bounds__(256, D <= 128 ? 2 : 1) void k_attention_prompt(Atte
     int lo = 1, hi = 0, lo_max = 0, hi_min = INT32_MAX, lo_min = INT32_MAX, hi_max = -1;
     v8h qf[NC];
     float f, slope = 0.0f, l = 0.0f;
-    float M = 0.0f, limit = -INFINITY;  // limit: the exponent less M that moves M; any, before the first visible key
+    float M = 0.0f, limit = -1.0f;  // limit: the sum of weights that moves M; any, before the first visible key
     {
         Raw8<DT> raw[NC];
         const uint16_t* row = reinterpret_cast<const uint16_t*>(a.q) + (int64_t)(sq.q.q0 + tok) * a.ldq + (int64_t)head * D;
@@ -126,152 +143,178 @@ __global__ __launch_bounds__(256, D <= 128 ? 2 : 1) void k_attention_prompt(Atte
 #pragma unroll
         for (int k = 0; k < 16; ++k) o[t][k] = 0.0f;
 
-    // staging: this wave brings the wave-th 16 tokens of a step
+    // staging: a wave brings 64 / NW tokens of K, and 8 / NW pieces' rows of V, of one 16 tokens of a step
     const int32_t* table = a.b.page_table + (int64_t)s * a.b.ldt;
     const int shift = __builtin_ctz(a.c.page);
-    uint4 rk[KW];
-    uint2 rv[2][VB / 8];
+    const int mine = wave * 4 / NW;  // the 16 tokens of a step that this wave brings
+    const int kt = wave * (64 / NW) + lane / NW, kj = lane % NW;       // token of the step, part of its channels
+    const int vp = wave * (8 / NW) + lane / (8 * NW), vd = lane % (8 * NW) * VD;  // 2 u + h, first channel
+    uint4 rk[KB / 16];
+    uint2 rv[2][VD / 2];
     float4 rs;
-    const int kt = lane >> 2, kj = lane & 3;  // token of the 16, quarter of its channels
     auto page_at = [&](int t0) -> int {
-        const int t = t0 + 16 * wave;
+        const int t = t0 + 16 * mine;
         return t < end ? uniform_load(table + (t >> shift)) : -1;
     };
-    auto load = [&](int t0, int id) {
-        // without a page of the pool page 0 is loaded and not seen (with no pool at all no sequence has keys)
+    // without a page of the pool page 0 is loaded and not seen (with no pool at all no sequence has keys)
+    auto load_k = [&](int t0, int id) {
+        const int64_t at = (int64_t)((uint32_t)id < (uint32_t)a.c.pages ? id : 0) * a.c.heads + hk;
+        const uint4* p = reinterpret_cast<const uint4*>(
+            a.c.k + (at * a.c.page + ((t0 + 16 * mine) & (a.c.page - 1))) * D + (kt & 15) * D + kj * KB);
+#pragma unroll
+        for (int w = 0; w < KB / 16; ++w) rk[w] = p[w];
+    };
+    auto load_v = [&](int t0, int id) {
         const bool there = (uint32_t)id < (uint32_t)a.c.pages;
         const int64_t at = (int64_t)(there ? id : 0) * a.c.heads + hk;
-        const int64_t base = (at * a.c.page + ((t0 + 16 * wave) & (a.c.page - 1))) * D;
-        const uint4* kp = reinterpret_cast<const uint4*>(a.c.k + base + kt * D + kj * (D / 4));
-#pragma unroll
-        for (int w = 0; w < KW; ++w) rk[w] = kp[w];
+        const int8_t* base = a.c.v + (at * a.c.page + ((t0 + 16 * mine) & (a.c.page - 1))) * D;
 #pragma unroll
         for (int q = 0; q < 2; ++q) {
-            const uint2* vp = reinterpret_cast<const uint2*>(a.c.v + base + (h + 2 * q) * (4 * D) + i * VB);
+            const uint2* p = reinterpret_cast<const uint2*>(base + ((vp & 1) + 2 * q) * (4 * D) + vd * 4);
 #pragma unroll
-            for (int w = 0; w < VB / 8; ++w) rv[q][w] = vp[w];
+            for (int w = 0; w < VD / 2; ++w) rv[q][w] = p[w];
         }
         rs = make_float4(uniform_load(a.c.k_scale + at), uniform_load(a.c.v_scale + at), 0.0f, there ? 1.0f : 0.0f);
     };
-    auto put = [&](Stage<D>& st) {
-        uint8_t* k = st.k + (kj * (D / 32)) * Stage<D>::kPitchK + (16 * wave + kt) * 16;
+    auto put_k = [&](KeyStage<D>& st) {
+        uint8_t* p = st.at + kj * (KB / 8) * KeyStage<D>::kPitch + kt * 16;
 #pragma unroll
-        for (int w = 0; w < KW; ++w) {
-            *reinterpret_cast<v8h*>(k + (2 * w) * Stage<D>::kPitchK) = join(codes4(rk[w].x), codes4(rk[w].y));
-            *reinterpret_cast<v8h*>(k + (2 * w + 1) * Stage<D>::kPitchK) = join(codes4(rk[w].z), codes4(rk[w].w));
+        for (int w = 0; w < KB / 16; ++w) {
+            *reinterpret_cast<v8h*>(p + (2 * w) * KeyStage<D>::kPitch) = join(codes4(rk[w].x), codes4(rk[w].y));
+            *reinterpret_cast<v8h*>(p + (2 * w + 1) * KeyStage<D>::kPitch) = join(codes4(rk[w].z), codes4(rk[w].w));
         }
-        uint8_t* v = st.v + (2 * wave + h) * Stage<D>::kPitchV + i * 16;
+    };
+    auto put_v = [&](ValueStage<D>& st) {
+        uint8_t* p = st.at + vp * ValueStage<D>::kPitch;
 #pragma unroll
-        for (int w = 0; w < VB / 8; ++w) {
-            *reinterpret_cast<v8h*>(v + (2 * w) * 512) = join(codes4(rv[0][w].x), codes4(rv[1][w].x));
-            *reinterpret_cast<v8h*>(v + (2 * w + 1) * 512) = join(codes4(rv[0][w].y), codes4(rv[1][w].y));
+        for (int w = 0; w < VD / 2; ++w) {
+            const int t = (vd + 2 * w) % NT, m = (vd + 2 * w) / NT;
+            *reinterpret_cast<v8h*>(p + ValueStage<D>::piece(t, m)) = join(codes4(rv[0][w].x), codes4(rv[1][w].x));
+            *reinterpret_cast<v8h*>(p + ValueStage<D>::piece(t + 1, m)) = join(codes4(rv[0][w].y), codes4(rv[1][w].y));
         }
-        if (lane == 0) st.scale[wave] = make_float4(rs.x, __log2f(rs.y), __builtin_amdgcn_rcpf(rs.y), rs.w);
+        if (lane == 0) st.scale[mine] = make_float4(rs.x, __log2f(rs.y), __builtin_amdgcn_rcpf(rs.y), rs.w);
     };
 
-    auto compute = [&](int t0, const Stage<D>& st) {
+    struct Scores {
         v16f z[2];
+    };
+    auto products = [&](const KeyStage<D>& st, Scores& x) {
 #pragma unroll
         for (int u = 0; u < 2; ++u)
 #pragma unroll
-            for (int k = 0; k < 16; ++k) z[u][k] = 0.0f;
+            for (int k = 0; k < 16; ++k) x.z[u][k] = 0.0f;
 #pragma unroll
         for (int c = 0; c < NC; ++c)
 #pragma unroll
             for (int u = 0; u < 2; ++u) {
-                const v8h kf = *reinterpret_cast<const v8h*>(st.k + (2 * c + h) * Stage<D>::kPitchK + (32 * u + i) * 16);
-                z[u] = __builtin_amdgcn_mfma_f32_32x32x16_f16(kf, qf[c], z[u], 0, 0, 0);
+                const v8h kf = *reinterpret_cast<const v8h*>(st.at + (2 * c + h) * KeyStage<D>::kPitch + (32 * u + i) * 16);
+                x.z[u] = __builtin_amdgcn_mfma_f32_32x32x16_f16(kf, qf[c], x.z[u], 0, 0, 0);
             }
+    };
+    // the weights of 16 tokens (u) from their exponents: as an operand, and their sum
+    auto weights = [&](const Scores& x, int u, v8h& pf) {
+        float p[8];
+#pragma unroll
+        for (int k = 0; k < 8; ++k) p[k] = exp2_(x.z[u >> 1][8 * (u & 1) + k]);
+        pf = __builtin_bit_cast(v8h, make_uint4(f32x2_to_16<kF16>(p[0], p[1]), f32x2_to_16<kF16>(p[2], p[3]),
+                                                f32x2_to_16<kF16>(p[4], p[5]), f32x2_to_16<kF16>(p[6], p[7])));
+        return ((p[0] + p[1]) + (p[2] + p[3])) + ((p[4] + p[5]) + (p[6] + p[7]));
+    };
+    auto step = [&](int t0, const KeyStage<D>& kst, const ValueStage<D>& vst) {
+        Scores x;
+        products(kst, x);
         float4 sc[4];
 #pragma unroll
-        for (int u = 0; u < 4; ++u) sc[u] = st.scale[u];
-        const bool pages = sc[0].w * sc[1].w * sc[2].w * sc[3].w != 0.0f;
-        const bool masked = t0 < lo_max || t0 + kKeys - 1 > hi_min || !pages;
-        float top = -INFINITY;
-        if (a.softcap > 0.0f || a.slopes) {
+        for (int u = 0; u < 4; ++u) sc[u] = vst.scale[u];
 #pragma unroll
-            for (int u = 0; u < 4; ++u) {
-                const float fs = f * sc[u].x;
+        for (int u = 0; u < 4; ++u) {
+            const float fs = f * sc[u].x, base = sc[u].y - M;
 #pragma unroll
-                for (int k = 0; k < 8; ++k) {
-                    float y = z[u >> 1][8 * (u & 1) + k] * fs;
-                    if (a.softcap > 0.0f) y = capped(y, cap2);
-                    if (a.slopes) y += slope * (float)(t0 + 16 * u + 8 * (k >> 2) + 4 * h + (k & 3) - pos);
-                    z[u >> 1][8 * (u & 1) + k] = y + (sc[u].y - M);
+            for (int k = 0; k < 8; ++k) {
+                float e = x.z[u >> 1][8 * (u & 1) + k];
+                const int off = 16 * u + 8 * (k >> 2) + (k & 3);
+                if constexpr (OPT) {
+                    e *= fs;
+                    if (a.softcap > 0.0f) e = capped(e, cap2);
+                    // the bias: slope (t0 + 4 h - pos), and the rest of the key's distance times slope
+                    e += __builtin_fmaf(slope, (float)off, __builtin_fmaf(slope, (float)(t0 + 4 * h - pos), base));
+                } else {
+                    e = __builtin_fmaf(e, fs, base);
                 }
-            }
-        } else {
-#pragma unroll
-            for (int u = 0; u < 4; ++u) {
-                const float fs = f * sc[u].x, base = sc[u].y - M;
-#pragma unroll
-                for (int k = 0; k < 8; ++k)
-                    z[u >> 1][8 * (u & 1) + k] = __builtin_fmaf(z[u >> 1][8 * (u & 1) + k], fs, base);
+                x.z[u >> 1][8 * (u & 1) + k] = e;
             }
         }
+        const bool masked = t0 < lo_max || t0 + kKeys - 1 > hi_min || sc[0].w * sc[1].w * sc[2].w * sc[3].w == 0.0f;
         if (masked) {
 #pragma unroll
             for (int u = 0; u < 4; ++u)
 #pragma unroll
                 for (int k = 0; k < 8; ++k) {
-                    const int key = t0 + 16 * u + 8 * (k >> 2) + 4 * h + (k & 3);
-                    const float y = z[u >> 1][8 * (u & 1) + k];
-                    z[u >> 1][8 * (u & 1) + k] = key >= lo && key <= hi && sc[u].w != 0.0f ? y : -INFINITY;
+                    const int key = t0 + 4 * h + 16 * u + 8 * (k >> 2) + (k & 3);
+                    const float e = x.z[u >> 1][8 * (u & 1) + k];
+                    x.z[u >> 1][8 * (u & 1) + k] = key >= lo && key <= hi && sc[u].w != 0.0f ? e : -INFINITY;
                 }
         }
-#pragma unroll
-        for (int u = 0; u < 2; ++u)
-#pragma unroll
-            for (int k = 0; k < 16; ++k) top = fmaxf(top, z[u][k]);
-        // z is the exponent less M already
-        if (__any(top > limit)) {
-            top = fmaxf(top, __shfl_xor(top, 32));
-            if (top > limit) {
-                const float by = ceilf(top) - kLift;
-                const float keep = limit < 0.0f ? 0.0f : exp2_(-by);
-                limit = kLift + kSlack;
-                M += by;
-                l *= keep;
-#pragma unroll
-                for (int t = 0; t < NT; ++t) o[t] *= keep;
-#pragma unroll
-                for (int u = 0; u < 2; ++u)
-#pragma unroll
-                    for (int k = 0; k < 16; ++k) z[u][k] -= by;
-            }
-        }
         v8h pf[4];
+        float sum[4];
+#pragma unroll
+        for (int u = 0; u < 4; ++u) sum[u] = weights(x, u, pf[u]);
+        const float most = fmaxf(fmaxf(sum[0], sum[1]), fmaxf(sum[2], sum[3]));
+        if (__any(most > limit)) {
+            // a weight is near binary16's end, or this is a row's first step: M moves
+            float top = -INFINITY;
+#pragma unroll
+            for (int u = 0; u < 2; ++u)
+#pragma unroll
+                for (int k = 0; k < 16; ++k) top = fmaxf(top, x.z[u][k]);
+            top = fmaxf(top, __shfl_xor(top, 32));
+            const bool over = fmaxf(most, __shfl_xor(most, 32)) > limit && top > -INFINITY;
+            const float by = over ? ceilf(top) - kLift : 0.0f;
+            const float keep = !over ? 1.0f : limit < 0.0f ? 0.0f : exp2_(-by);
+            if (over) limit = kMost;
+            M += by;
+            l *= keep;
+#pragma unroll
+            for (int t = 0; t < NT; ++t) o[t] *= keep;
+#pragma unroll
+            for (int u = 0; u < 2; ++u)
+#pragma unroll
+                for (int k = 0; k < 16; ++k) x.z[u][k] -= by;
+#pragma unroll
+            for (int u = 0; u < 4; ++u) sum[u] = weights(x, u, pf[u]);
+        }
 #pragma unroll
         for (int u = 0; u < 4; ++u) {
-            float p[8];
-#pragma unroll
-            for (int k = 0; k < 8; ++k) p[k] = exp2_(z[u >> 1][8 * (u & 1) + k]);
-            const float sum = ((p[0] + p[1]) + (p[2] + p[3])) + ((p[4] + p[5]) + (p[6] + p[7]));
-            l += sum == 0.0f ? 0.0f : sum * sc[u].z;  // hidden keys of a page whose scale is not finite: 0
-            pf[u] = __builtin_bit_cast(v8h, make_uint4(f32x2_to_16<kF16>(p[0], p[1]), f32x2_to_16<kF16>(p[2], p[3]),
-                                                       f32x2_to_16<kF16>(p[4], p[5]), f32x2_to_16<kF16>(p[6], p[7])));
+            l += sum[u] == 0.0f ? 0.0f : sum[u] * sc[u].z;  // hidden keys of a page whose scale is not finite: 0
         }
 #pragma unroll
         for (int u = 0; u < 4; ++u)
 #pragma unroll
             for (int t = 0; t < NT; ++t) {
-                const v8h vf = *reinterpret_cast<const v8h*>(st.v + (2 * u + h) * Stage<D>::kPitchV + (32 * t + i) * 16);
+                const v8h vf = *reinterpret_cast<const v8h*>(vst.at + (2 * u + h) * ValueStage<D>::kPitch + ValueStage<D>::piece(t, i));
                 o[t] = __builtin_amdgcn_mfma_f32_32x32x16_f16(vf, pf[u], o[t], 0, 0, 0);
             }
     };
 
     if (begin < end) {
-        load(begin, page_at(begin));
-        put(stage[0]);
-        load(begin + kKeys, page_at(begin + kKeys));
-        int id = page_at(begin + 2 * kKeys);
+        int id = page_at(begin);
+        load_k(begin, id);
+        load_v(begin, id);
+        put_k(ks[0]);
+        put_v(vs[0]);
+        id = page_at(begin + kKeys);
+        load_k(begin + kKeys, id);
+        load_v(begin + kKeys, id);
+        id = page_at(begin + 2 * kKeys);
         __syncthreads();
         int buf = 0;
         for (int t0 = begin; t0 < end; t0 += kKeys) {
-            if (t0 <= hi_max && t0 + kKeys > lo_min) compute(t0, stage[buf]);
+            if (t0 <= hi_max && t0 + kKeys > lo_min) step(t0, ks[buf], vs[buf]);
             if (t0 + kKeys < end) {
-                put(stage[buf ^ 1]);
-                load(t0 + 2 * kKeys, id);
+                put_k(ks[buf ^ 1]);
+                put_v(vs[buf ^ 1]);
+                load_k(t0 + 2 * kKeys, id);
+                load_v(t0 + 2 * kKeys, id);
                 id = page_at(t0 + 3 * kKeys);
             }
             __syncthreads();
@@ -344,7 +387,7 @@ __global__ __launch_bounds__(256) void k_attention_prompt_join(AttentionArgs a, 
 }
 
 int64_t prompt_items(const AttentionArgs& a) {
-    const int group = a.hq / a.c.heads;
+    const int group = a.hq / a.c.heads, kRows = tile_rows(a.c.dim);
     return a.b.cu_q ? (int64_t)a.b.tokens * group / kRows + a.b.batch
                     : (int64_t)a.b.batch * ((group + kRows - 1) / kRows);
 }
@@ -352,7 +395,9 @@ int64_t prompt_items(const AttentionArgs& a) {
 template <int DT, int D>
 void launch(const AttentionArgs& a, int splits, hipStream_t st) {
     const int64_t items = prompt_items(a);
-    k_attention_prompt<DT, D><<<dim3((uint32_t)(items * a.c.heads), splits), 256, 0, st>>>(a, items, splits);
+    const dim3 grid((uint32_t)(items * a.c.heads), splits);
+    if (a.softcap > 0.0f || a.slopes) k_attention_prompt<DT, D, true><<<grid, 64 * waves(D), 0, st>>>(a, items, splits);
+    else k_attention_prompt<DT, D, false><<<grid, 64 * waves(D), 0, st>>>(a, items, splits);
     if (splits > 1) {
         const int64_t n = (int64_t)a.b.tokens * a.hq * (D / 8);
         k_attention_prompt_join<DT, D><<<(uint32_t)((n + 255) / 256), 256, 0, st>>>(a, splits);
@@ -362,12 +407,12 @@ void launch(const AttentionArgs& a, int splits, hipStream_t st) {
 }  // namespace
 
 // Parts of the keys that each tile of rows is cut into: what fills the chip's
-// workgroup slots (two a compute unit, one with 256 channels) in the fewest
+// workgroup slots (three a compute unit with 64 channels, else one) in the fewest
 // rounds of the shortest parts, a part more counted as 2% for its partial
 // results.
 int attention_prompt_splits(int64_t tokens, int hq, int hkv, int dim) {
-    const int64_t slots = dim == 256 ? 256 : 512;
-    const int64_t tiles = (tokens * (hq / hkv) + kRows - 1) / kRows * hkv;
+    const int64_t slots = 256 * per_simd(dim) * 4 / waves(dim), rows = tile_rows(dim);
+    const int64_t tiles = (tokens * (hq / hkv) + rows - 1) / rows * hkv;
     int best = 1;
     double least = 1e30;
     for (int s = 1; s <= 16 && tiles < slots; ++s) {
@@ -381,7 +426,7 @@ int attention_prompt_splits(int64_t tokens, int hq, int hkv, int dim) {
 }
 
 int64_t attention_prompt_threads(const AttentionArgs& a, int splits) {
-    return std::max(prompt_items(a) * a.c.heads * splits * 256, (int64_t)a.b.tokens * a.hq * (a.c.dim / 8));
+    return std::max(prompt_items(a) * a.c.heads * splits * 64 * waves(a.c.dim), (int64_t)a.b.tokens * a.hq * (a.c.dim / 8));
 }
 
 void launch_attention_prompt(const AttentionArgs& a, int dt, int splits, hipStream_t st) {
