@@ -3,6 +3,7 @@
 // between them.  include/pdq.h (pdq_kv_attention) states the arithmetic,
 // attention_device.h how it is taken.
 #include <algorithm>
+#include <type_traits>
 
 #include "attention_device.h"
 
@@ -10,8 +11,9 @@ namespace pdq {
 
 namespace {
 
-constexpr int kKeys = 64;  // keys of a step
 constexpr float kMost = 0x1p14f;  // a sum of eight weights beyond which M moves
+
+constexpr int kKeys = 64;  // keys of a step
 
 // Waves of a workgroup, 32 rows each.  Eight share the conversion of a step's
 // codes between them and fill a compute unit (two to a SIMD, 256 registers); with
@@ -37,8 +39,8 @@ template <int D>
 struct ValueStage {
     static constexpr int kSkew = D == 128 ? 128 : 0;  // behind every second t
     static constexpr int kPitch = D * 16 + (D / 64 - 1) * kSkew + 16;
-    uint8_t at[8 * kPitch];
-    float4 scale[4];  // of each 16 tokens: S_k, log2 S_v, 1 / S_v, 0 or 1: a page is there
+    uint8_t at[kKeys / 8 * kPitch];
+    float4 scale[kKeys / 16];  // of each 16 tokens: S_k, log2 S_v, 1 / S_v, 0 or 1: a page is there
     static __device__ __forceinline__ int piece(int t, int m) { return t * 512 + (t >> 1) * kSkew + m * 16; }
 };
 
@@ -46,14 +48,14 @@ struct ValueStage {
 // key/value head over a part of their keys.  Scores are computed transposed, keys
 // x rows, in 32x32x16 products, so that a row's scores lie in one lane (and the one
 // 32 lanes on) and its weights are the operand of the value product as they stand;
-// the output is accumulated transposed too.  Codes are loaded ahead, converted once
-// for all waves and staged in double-buffered LDS, one barrier a step; a step
-// computes the next step's scores beside its own softmax, so that the matrix and
-// the vector units both have work.  OPT: softcap or slopes are given.
-template <int DT, int D, bool OPT>
+// the output is accumulated transposed too.  Codes are loaded a step ahead,
+// converted once for all waves and staged in one of two LDS buffers, one barrier
+// a step.  CAP, BIAS: softcap, slopes are given.
+template <int DT, int D, bool CAP, bool BIAS>
 __global__ __launch_bounds__(64 * waves(D), per_simd(D)) void k_attention_prompt(AttentionArgs a, int64_t items, int splits) {
-    constexpr int NW = waves(D), kRows = tile_rows(D), NC = D / 16, NT = D / 32;
-    constexpr int KB = D / NW, VD = D / (8 * NW);  // bytes of K, channels of V that a thread brings
+    constexpr int KU = kKeys / 32, NU = kKeys / 16, NW = waves(D), kRows = tile_rows(D), NC = D / 16, NT = D / 32;
+    constexpr int kAhead = D == 128 ? 8 : 0;  // operands on their way from LDS while one is multiplied (where registers allow)
+    constexpr int KB = kKeys * D / (64 * NW), VD = kKeys * D / (512 * NW);  // bytes of K, channels of V that a thread brings
     __shared__ KeyStage<D> ks[2];
     __shared__ ValueStage<D> vs[2];
     const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
@@ -117,12 +119,12 @@ __global__ __launch_bounds__(64 * waves(D), per_simd(D)) void k_attention_prompt
                 qf[c] = __builtin_bit_cast(v8h, raw[c].w[0]);
             }
         }
-        f = ldexpf(a.softcap > 0.0f ? 2.0f * kLog2e / a.softcap * a.scale : kLog2e * a.scale, e - 14);
+        f = ldexpf(CAP ? 2.0f * kLog2e / a.softcap * a.scale : kLog2e * a.scale, e - 14);
         if (valid) {
             row_keys(a, sq, pos, lo, hi);
             lo_max = lo_min = lo;
             hi_min = hi_max = hi;
-            if (a.slopes) slope = a.slopes[head] * kLog2e;
+            if constexpr (BIAS) slope = a.slopes[head] * kLog2e;
         }
 #pragma unroll
         for (int m = 16; m >= 1; m >>= 1) {
@@ -146,35 +148,35 @@ __global__ __launch_bounds__(64 * waves(D), per_simd(D)) void k_attention_prompt
     // staging: a wave brings 64 / NW tokens of K, and 8 / NW pieces' rows of V, of one 16 tokens of a step
     const int32_t* table = a.b.page_table + (int64_t)s * a.b.ldt;
     const int shift = __builtin_ctz(a.c.page);
-    const int mine = wave * 4 / NW;  // the 16 tokens of a step that this wave brings
-    const int kt = wave * (64 / NW) + lane / NW, kj = lane % NW;       // token of the step, part of its channels
-    const int vp = wave * (8 / NW) + lane / (8 * NW), vd = lane % (8 * NW) * VD;  // 2 u + h, first channel
+    const int mine = wave * NU / NW;  // the 16 tokens of a step that this wave brings
+    constexpr int KL = D / KB, VL = D / VD;  // lanes of a token of K, of a row of V
+    const int kt = wave * (kKeys / NW) + lane / KL, kj = lane % KL;       // token of the step, part of its channels
+    const int vp = wave * (kKeys / 8 / NW) + lane / VL, vd = lane % VL * VD;  // 2 u + h, first channel
     uint4 rk[KB / 16];
     uint2 rv[2][VD / 2];
-    float4 rs;
-    auto page_at = [&](int t0) -> int {
-        const int t = t0 + 16 * mine;
-        return t < end ? uniform_load(table + (t >> shift)) : -1;
-    };
-    // without a page of the pool page 0 is loaded and not seen (with no pool at all no sequence has keys)
-    auto load_k = [&](int t0, int id) {
-        const int64_t at = (int64_t)((uint32_t)id < (uint32_t)a.c.pages ? id : 0) * a.c.heads + hk;
-        const uint4* p = reinterpret_cast<const uint4*>(
-            a.c.k + (at * a.c.page + ((t0 + 16 * mine) & (a.c.page - 1))) * D + (kt & 15) * D + kj * KB);
+    float2 rs;
+    bool rs_there;
+    // Page numbers and scales come by vector loads, issued before the codes that they are used with or after: scalar
+    // loads would have to arrive before the next barrier, which waits for the counter that LDS and they share.
+    auto page_at = [&](int t0) -> int { return table[min(t0 + 16 * mine, end - 1) >> shift]; };
+    // Where a step's 16 tokens of this wave lie in the pool: the same for K and V.  Without a page of the pool page 0
+    // is loaded and not seen (with no pool at all no sequence has keys).
+    const uint32_t page_bytes = (uint32_t)(a.c.heads * a.c.page * D), head_bytes = (uint32_t)(hk * a.c.page * D);
+    const uint32_t k_lane = (kt & 15) * D + kj * KB, v_lane = (vp & 1) * (4 * D) + vd * 4;
+    auto load = [&](int t0, int id) {
+        const uint32_t p = (uint32_t)__builtin_amdgcn_readfirstlane(id);
+        rs_there = p < (uint32_t)a.c.pages && t0 + 16 * mine < end;
+        const uint32_t page = rs_there ? p : 0u, slot = (t0 + 16 * mine) & (a.c.page - 1);
+        const uint64_t at = (uint64_t)page * page_bytes + (head_bytes + slot * D);
+        const uint64_t s = (uint64_t)page * (uint32_t)a.c.heads + (uint32_t)hk;
+        rs = make_float2(a.c.k_scale[s], a.c.v_scale[s]);
 #pragma unroll
-        for (int w = 0; w < KB / 16; ++w) rk[w] = p[w];
-    };
-    auto load_v = [&](int t0, int id) {
-        const bool there = (uint32_t)id < (uint32_t)a.c.pages;
-        const int64_t at = (int64_t)(there ? id : 0) * a.c.heads + hk;
-        const int8_t* base = a.c.v + (at * a.c.page + ((t0 + 16 * mine) & (a.c.page - 1))) * D;
+        for (int w = 0; w < KB / 16; ++w) rk[w] = *reinterpret_cast<const uint4*>(a.c.k + at + (k_lane + 16 * w));
 #pragma unroll
-        for (int q = 0; q < 2; ++q) {
-            const uint2* p = reinterpret_cast<const uint2*>(base + ((vp & 1) + 2 * q) * (4 * D) + vd * 4);
+        for (int q = 0; q < 2; ++q)
 #pragma unroll
-            for (int w = 0; w < VD / 2; ++w) rv[q][w] = p[w];
-        }
-        rs = make_float4(uniform_load(a.c.k_scale + at), uniform_load(a.c.v_scale + at), 0.0f, there ? 1.0f : 0.0f);
+            for (int w = 0; w < VD / 2; ++w)
+                rv[q][w] = *reinterpret_cast<const uint2*>(a.c.v + at + (v_lane + q * 8 * D + 8 * w));
     };
     auto put_k = [&](KeyStage<D>& st) {
         uint8_t* p = st.at + kj * (KB / 8) * KeyStage<D>::kPitch + kt * 16;
@@ -192,24 +194,36 @@ __global__ __launch_bounds__(64 * waves(D), per_simd(D)) void k_attention_prompt
             *reinterpret_cast<v8h*>(p + ValueStage<D>::piece(t, m)) = join(codes4(rv[0][w].x), codes4(rv[1][w].x));
             *reinterpret_cast<v8h*>(p + ValueStage<D>::piece(t + 1, m)) = join(codes4(rv[0][w].y), codes4(rv[1][w].y));
         }
-        if (lane == 0) st.scale[mine] = make_float4(rs.x, __log2f(rs.y), __builtin_amdgcn_rcpf(rs.y), rs.w);
+        if (lane == 0) {
+            // a scale that is not finite reaches the weights of the keys that are seen; hidden ones add 0 times 0 to l
+            const float inv = __builtin_amdgcn_rcpf(rs.y);
+            st.scale[mine] = make_float4(rs.x, __log2f(rs.y), fabsf(inv) < INFINITY ? inv : 0.0f, rs_there ? 1.0f : 0.0f);
+        }
     };
 
     struct Scores {
-        v16f z[2];
+        v16f z[KU];
     };
     auto products = [&](const KeyStage<D>& st, Scores& x) {
 #pragma unroll
-        for (int u = 0; u < 2; ++u)
+        for (int u = 0; u < KU; ++u)
 #pragma unroll
             for (int k = 0; k < 16; ++k) x.z[u][k] = 0.0f;
 #pragma unroll
         for (int c = 0; c < NC; ++c)
 #pragma unroll
-            for (int u = 0; u < 2; ++u) {
+            for (int u = 0; u < KU; ++u) {
                 const v8h kf = *reinterpret_cast<const v8h*>(st.at + (2 * c + h) * KeyStage<D>::kPitch + (32 * u + i) * 16);
                 x.z[u] = __builtin_amdgcn_mfma_f32_32x32x16_f16(kf, qf[c], x.z[u], 0, 0, 0);
             }
+        if constexpr (kAhead > 0) {
+            __builtin_amdgcn_sched_group_barrier(0x100, kAhead, 0);
+#pragma unroll
+            for (int j = 0; j < KU * NC; ++j) {
+                __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
+                if (j < KU * NC - kAhead) __builtin_amdgcn_sched_group_barrier(0x100, 1, 0);
+            }
+        }
     };
     // the weights of 16 tokens (u) from their exponents: as an operand, and their sum
     auto weights = [&](const Scores& x, int u, v8h& pf) {
@@ -221,50 +235,63 @@ __global__ __launch_bounds__(64 * waves(D), per_simd(D)) void k_attention_prompt
         return ((p[0] + p[1]) + (p[2] + p[3])) + ((p[4] + p[5]) + (p[6] + p[7]));
     };
     auto step = [&](int t0, const KeyStage<D>& kst, const ValueStage<D>& vst) {
+        float4 sc[NU];
+#pragma unroll
+        for (int u = 0; u < NU; ++u) sc[u] = vst.scale[u];
         Scores x;
         products(kst, x);
-        float4 sc[4];
+        bool pages = true;
 #pragma unroll
-        for (int u = 0; u < 4; ++u) sc[u] = vst.scale[u];
+        for (int u = 0; u < NU; ++u) pages &= sc[u].w != 0.0f;
+        auto exponents = [&](auto masked) {
 #pragma unroll
-        for (int u = 0; u < 4; ++u) {
-            const float fs = f * sc[u].x, base = sc[u].y - M;
-#pragma unroll
-            for (int k = 0; k < 8; ++k) {
-                float e = x.z[u >> 1][8 * (u & 1) + k];
-                const int off = 16 * u + 8 * (k >> 2) + (k & 3);
-                if constexpr (OPT) {
-                    e *= fs;
-                    if (a.softcap > 0.0f) e = capped(e, cap2);
-                    // the bias: slope (t0 + 4 h - pos), and the rest of the key's distance times slope
-                    e += __builtin_fmaf(slope, (float)off, __builtin_fmaf(slope, (float)(t0 + 4 * h - pos), base));
-                } else {
-                    e = __builtin_fmaf(e, fs, base);
-                }
-                x.z[u >> 1][8 * (u & 1) + k] = e;
-            }
-        }
-        const bool masked = t0 < lo_max || t0 + kKeys - 1 > hi_min || sc[0].w * sc[1].w * sc[2].w * sc[3].w == 0.0f;
-        if (masked) {
-#pragma unroll
-            for (int u = 0; u < 4; ++u)
+            for (int u = 0; u < NU; ++u) {
+                const float fs = f * sc[u].x;
+                float base = sc[u].y - M;
+                // the bias: slope (t0 + 4 h - pos), and the rest of the key's distance times slope
+                if constexpr (BIAS) base = __builtin_fmaf(slope, (float)(t0 + 4 * h - pos), base);
+                // the cap: cap (1 - 2 / (2^(2 x log2 e) + 1)), the constant part with the base
+                if constexpr (CAP) base += cap2;
 #pragma unroll
                 for (int k = 0; k < 8; ++k) {
-                    const int key = t0 + 4 * h + 16 * u + 8 * (k >> 2) + (k & 3);
-                    const float e = x.z[u >> 1][8 * (u & 1) + k];
-                    x.z[u >> 1][8 * (u & 1) + k] = key >= lo && key <= hi && sc[u].w != 0.0f ? e : -INFINITY;
+                    float e = x.z[u >> 1][8 * (u & 1) + k];
+                    const int off = 16 * u + 8 * (k >> 2) + (k & 3);
+                    const float add = BIAS ? __builtin_fmaf(slope, (float)off, base) : base;
+                    if constexpr (CAP)
+                        e = __builtin_fmaf(-2.0f * cap2, __builtin_amdgcn_rcpf(exp2_(e * fs) + 1.0f), add);
+                    else
+                        e = __builtin_fmaf(e, fs, add);
+                    if constexpr (masked.value) {
+                        const int key = t0 + 4 * h + off;
+                        e = key >= lo && key <= hi && sc[u].w != 0.0f ? e : -INFINITY;
+                    }
+                    x.z[u >> 1][8 * (u & 1) + k] = e;
                 }
-        }
-        v8h pf[4];
-        float sum[4];
+            }
+        };
+        if (t0 < lo_max || t0 + kKeys - 1 > hi_min || !pages)
+            exponents(std::true_type{});
+        else
+            exponents(std::false_type{});
+        v8h pf[NU], vf[NU][NT];
+        auto values = [&](int u) {
 #pragma unroll
-        for (int u = 0; u < 4; ++u) sum[u] = weights(x, u, pf[u]);
-        const float most = fmaxf(fmaxf(sum[0], sum[1]), fmaxf(sum[2], sum[3]));
+            for (int t = 0; t < NT; ++t)
+                vf[u][t] = *reinterpret_cast<const v8h*>(vst.at + (2 * u + h) * ValueStage<D>::kPitch + ValueStage<D>::piece(t, i));
+        };
+#pragma unroll
+        for (int u = 0; u < kAhead / NT; ++u) values(u);
+        float sum[NU];
+#pragma unroll
+        for (int u = 0; u < NU; ++u) sum[u] = weights(x, u, pf[u]);
+        float most = sum[0];
+#pragma unroll
+        for (int u = 1; u < NU; ++u) most = fmaxf(most, sum[u]);
         if (__any(most > limit)) {
             // a weight is near binary16's end, or this is a row's first step: M moves
             float top = -INFINITY;
 #pragma unroll
-            for (int u = 0; u < 2; ++u)
+            for (int u = 0; u < KU; ++u)
 #pragma unroll
                 for (int k = 0; k < 16; ++k) top = fmaxf(top, x.z[u][k]);
             top = fmaxf(top, __shfl_xor(top, 32));
@@ -277,35 +304,38 @@ __global__ __launch_bounds__(64 * waves(D), per_simd(D)) void k_attention_prompt
 #pragma unroll
             for (int t = 0; t < NT; ++t) o[t] *= keep;
 #pragma unroll
-            for (int u = 0; u < 2; ++u)
+            for (int u = 0; u < KU; ++u)
 #pragma unroll
                 for (int k = 0; k < 16; ++k) x.z[u][k] -= by;
 #pragma unroll
-            for (int u = 0; u < 4; ++u) sum[u] = weights(x, u, pf[u]);
+            for (int u = 0; u < NU; ++u) sum[u] = weights(x, u, pf[u]);
         }
 #pragma unroll
-        for (int u = 0; u < 4; ++u) {
-            l += sum[u] == 0.0f ? 0.0f : sum[u] * sc[u].z;  // hidden keys of a page whose scale is not finite: 0
+        for (int u = 0; u < NU; ++u) {
+            l = __builtin_fmaf(sum[u], sc[u].z, l);
         }
 #pragma unroll
-        for (int u = 0; u < 4; ++u)
+        for (int u = 0; u < NU; ++u) {
+            if (u >= kAhead / NT) values(u);
 #pragma unroll
-            for (int t = 0; t < NT; ++t) {
-                const v8h vf = *reinterpret_cast<const v8h*>(vst.at + (2 * u + h) * ValueStage<D>::kPitch + ValueStage<D>::piece(t, i));
-                o[t] = __builtin_amdgcn_mfma_f32_32x32x16_f16(vf, pf[u], o[t], 0, 0, 0);
+            for (int t = 0; t < NT; ++t) o[t] = __builtin_amdgcn_mfma_f32_32x32x16_f16(vf[u][t], pf[u], o[t], 0, 0, 0);
+        }
+        if constexpr (kAhead > 0) {
+#pragma unroll
+            for (int j = 0; j < NU * NT; ++j) {
+                __builtin_amdgcn_sched_group_barrier(0x008, 1, 1);
+                if (j < NU * NT - kAhead) __builtin_amdgcn_sched_group_barrier(0x100, 1, 1);
             }
+        }
     };
 
     if (begin < end) {
-        int id = page_at(begin);
-        load_k(begin, id);
-        load_v(begin, id);
+        int id = page_at(begin), next = page_at(begin + kKeys);
+        load(begin, id);
         put_k(ks[0]);
         put_v(vs[0]);
-        id = page_at(begin + kKeys);
-        load_k(begin + kKeys, id);
-        load_v(begin + kKeys, id);
         id = page_at(begin + 2 * kKeys);
+        load(begin + kKeys, next);
         __syncthreads();
         int buf = 0;
         for (int t0 = begin; t0 < end; t0 += kKeys) {
@@ -313,9 +343,9 @@ __global__ __launch_bounds__(64 * waves(D), per_simd(D)) void k_attention_prompt
             if (t0 + kKeys < end) {
                 put_k(ks[buf ^ 1]);
                 put_v(vs[buf ^ 1]);
-                load_k(t0 + 2 * kKeys, id);
-                load_v(t0 + 2 * kKeys, id);
+                next = id;
                 id = page_at(t0 + 3 * kKeys);
+                load(t0 + 2 * kKeys, next);
             }
             __syncthreads();
             buf ^= 1;
@@ -396,8 +426,13 @@ template <int DT, int D>
 void launch(const AttentionArgs& a, int splits, hipStream_t st) {
     const int64_t items = prompt_items(a);
     const dim3 grid((uint32_t)(items * a.c.heads), splits);
-    if (a.softcap > 0.0f || a.slopes) k_attention_prompt<DT, D, true><<<grid, 64 * waves(D), 0, st>>>(a, items, splits);
-    else k_attention_prompt<DT, D, false><<<grid, 64 * waves(D), 0, st>>>(a, items, splits);
+    if (a.softcap > 0.0f) {
+        if (a.slopes) k_attention_prompt<DT, D, true, true><<<grid, 64 * waves(D), 0, st>>>(a, items, splits);
+        else k_attention_prompt<DT, D, true, false><<<grid, 64 * waves(D), 0, st>>>(a, items, splits);
+    } else {
+        if (a.slopes) k_attention_prompt<DT, D, false, true><<<grid, 64 * waves(D), 0, st>>>(a, items, splits);
+        else k_attention_prompt<DT, D, false, false><<<grid, 64 * waves(D), 0, st>>>(a, items, splits);
+    }
     if (splits > 1) {
         const int64_t n = (int64_t)a.b.tokens * a.hq * (D / 8);
         k_attention_prompt_join<DT, D><<<(uint32_t)((n + 255) / 256), 256, 0, st>>>(a, splits);
