@@ -78,7 +78,8 @@ __device__ __forceinline__ void row_keys(const AttentionArgs& a, const AttnSeq& 
 
 // attention_prompt.hip: many rows for each sequence.  splits: parts of the keys,
 // joined through the workspace ([splits, tokens, hq, dim + 2] floats) beyond one.
-int attention_prompt_splits(int64_t tokens, int hq, int hkv, int dim);
+int attention_prompt_most_splits(int64_t tokens, int64_t batch, int hq, int hkv, int dim);
+int attention_prompt_splits(int64_t tokens, int64_t batch, int hq, int hkv, int dim, int64_t keys);
 int64_t attention_prompt_threads(const AttentionArgs& a, int splits);
 void launch_attention_prompt(const AttentionArgs& a, int dt, int splits, hipStream_t st);
 

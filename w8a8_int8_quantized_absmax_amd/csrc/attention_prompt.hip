@@ -393,6 +393,7 @@ __global__ __launch_bounds__(256) void k_attention_prompt_join(AttentionArgs a, 
     const float* p = a.ws + row * (D + 2);
     const int64_t step = rows * (D + 2);
     float M = kNone, l = 0.0f, o[8] = {};
+#pragma unroll 8
     for (int w = 0; w < splits; ++w, p += step) {
         const float2 ml = *reinterpret_cast<const float2*>(p + D);
         const float now = fmaxf(M, ml.x), fo = exp2_(M - now), fw = exp2_(ml.x - now);
@@ -441,17 +442,30 @@ void launch(const AttentionArgs& a, int splits, hipStream_t st) {
 
 }  // namespace
 
-// Parts of the keys that each tile of rows is cut into: what fills the chip's
-// workgroup slots (three a compute unit with 64 channels, else one) in the fewest
-// rounds of the shortest parts, a part more counted as 2% for its partial
-// results.
-int attention_prompt_splits(int64_t tokens, int hq, int hkv, int dim) {
-    const int64_t slots = 256 * per_simd(dim) * 4 / waves(dim), rows = tile_rows(dim);
-    const int64_t tiles = (tokens * (hq / hkv) + rows - 1) / rows * hkv;
+// Workgroups that the chip holds at once, and row tiles of a batch (of sequences
+// of the average length, times heads).
+static int64_t slots(int dim) { return 256 * per_simd(dim) * 4 / waves(dim); }
+static int64_t tiles(int64_t tokens, int64_t batch, int hq, int hkv, int dim) {
+    const int64_t each = (tokens * (hq / hkv) + batch - 1) / batch;
+    return (each + tile_rows(dim) - 1) / tile_rows(dim) * batch * hkv;
+}
+
+int attention_prompt_most_splits(int64_t tokens, int64_t batch, int hq, int hkv, int dim) {
+    return (int)std::min<int64_t>(32, std::max<int64_t>(1, 2 * slots(dim) / tiles(tokens, batch, hq, hkv, dim)));
+}
+
+// Parts of the keys that each tile of rows is cut into: the fewest microseconds
+// of rounds of workgroups, each some 6 and 2 a step, and of the join, some 4 and
+// 0.4 a part (measured with 128 channels: 110 rows x 2 heads of a group over 4842
+// keys 34 / 31 / 36 us in 8 / 16 / 32 parts).  keys: what the table can name.
+int attention_prompt_splits(int64_t tokens, int64_t batch, int hq, int hkv, int dim, int64_t keys) {
+    const int most = attention_prompt_most_splits(tokens, batch, hq, hkv, dim);
+    const int64_t n = tiles(tokens, batch, hq, hkv, dim), steps = (keys + kKeys - 1) / kKeys;
     int best = 1;
     double least = 1e30;
-    for (int s = 1; s <= 16 && tiles < slots; ++s) {
-        const double t = (double)((tiles * s + slots - 1) / slots) / s * (1.0 + 0.02 * s);
+    for (int s = 1; s <= most; ++s) {
+        const double rounds = (double)((n * s + slots(dim) - 1) / slots(dim));
+        const double t = rounds * (6.0 + 2.0 * (double)((steps + s - 1) / s)) + (s > 1 ? 4.0 + 0.4 * s : 0.0);
         if (t < least) {
             least = t;
             best = s;
