@@ -495,6 +495,8 @@ pdq_status pdq_linear_int8_outlier_noalloc(const void* x, pdq_dtype dt, int64_t 
  *               are the new tokens of sequence s, its last ones; NULL: one row for
  *               each sequence (tokens == batch)
  *   batch       0 .. 65536; max_pages * page at most 2^30
+ * A call whose launch would take more than 2^31 threads is PDQ_ERR_SHAPE (far
+ * beyond 10^6 rows or 10^5 sequences in the usual shapes).
  * The position of row t of sequence s is seq_len[s] - (cu_q[s + 1] - t).
  *
  * What the device arrays hold cannot be refused.  A page number outside the pool
@@ -527,7 +529,8 @@ typedef struct pdq_kv_batch {
  *   k, v     [tokens, heads, dim] of dt (BF16 or F16), row pitches ldk, ldv, the
  *            heads of a row side by side (e.g. columns of the projection's output)
  *   q        [tokens, hq, dim] of dt, row pitch ldq, or NULL; q_out likewise, row
- *            pitch ldqo: q rotated, rounded to dt (must not overlap q)
+ *            pitch ldqo: q rotated, rounded to dt (q itself with ldqo == ldq, or
+ *            memory that does not overlap it)
  *   cos, sin float [positions, rot / 2] or both NULL (no rotation; rot is ignored,
  *            q must be NULL): the first rot channels of a head are rotated,
  *            (a, b) -> (a cos - b sin, b cos + a sin) with a, b the channels

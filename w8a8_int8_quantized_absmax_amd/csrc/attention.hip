@@ -119,7 +119,19 @@ __device__ __forceinline__ void write_row(const AttentionArgs& a, int64_t row, i
 // channels i D/16 .. of tokens 4 g .. 4 g + 3 as V; scores come out with a row
 // of queries in lane i and tokens 4 g .. 4 g + 3 in its registers, which is the
 // weights' operand of the value product as it stands.  The next tile's codes are
-// loaded while one is computed.
+// loaded while one is computed, the next segment's first tile while one is
+// written out.
+//
+// Bound by the cache's bytes, 2 D a key and head, at long contexts (one read at
+// the card's best, 6.2 TB/s): 96 sequences up to 16384 keys (1.93 GB) 344 us, 5.6
+// TB/s; one of 131071 (268 MB) 52 us, 5.2 TB/s, of which some 5 us are its begin:
+// lengths, range, page, codes, one after the other.  32 sequences up to 4096 (139
+// MB) 38 us, 3.7 TB/s: beside the begin, the 1.5 segments of a workgroup.  The
+// equal ranges are what ragged lengths need; three workgroups a compute unit
+// instead of two with 128 channels: 48.0 against 48.3 us there, 61.5 against 60.0 for
+// the one long sequence; four: 64 and 93.  K straight into the operand layout
+// keeps LDS out of the loop; converting the codes takes 160 of some 250 vector
+// instructions a tile, 22% of the time at most.
 template <int DT, int D, int NQ>
 __global__ __launch_bounds__(256, resident(D, NQ)) void k_attention_few(AttentionArgs a) {
     constexpr int R = 16 * NQ, W = ways(D, R), DL = D / 4, NC = D / 32, NT = D / 16, W4 = D / 64;
@@ -493,7 +505,7 @@ __global__ __launch_bounds__(256, resident(D, NQ)) void k_attention_few(Attentio
 
 // Joins the partial results of a segment that was cut: one workgroup for each
 // (row tile of a sequence, head; row), D / 8 threads for each of 2048 / D parts
-// at a time.
+// at a time.  All latency: 4.7 us for 32 x 4096 and for 1 x 131071 keys.
 template <int DT, int D, int R>
 __global__ __launch_bounds__(256) void k_attention_join(AttentionArgs a) {
     constexpr int NP = 2048 / D;  // parts taken at once

@@ -7,11 +7,11 @@
 // so that a weight, rounded to binary16 for the value product, keeps its 11 bits
 // whatever the scales are, and a page's scale costs one addition a score.
 //
-// M is an integer no more than kSlack below the largest exponent seen, moved
-// only when a weight would pass 2^(kLift + kSlack): moving it multiplies by
-// powers of two, so when it moves does not change a row's result beyond
-// what binary16's range cuts off (weights under 2^-25 of 2^kLift), and most
-// tiles need no maximum across lanes.
+// M is an integer, kLift below the largest exponent where it was set, and moved
+// only when weights pass 2^(kLift + kSlack), by the row itself, whatever the other
+// rows do: moving it multiplies what is accumulated by a power of two, exactly,
+// and most tiles need no maximum across lanes.  A weight under 2^-14 (2^-19 of the
+// largest when M was set) is subnormal in binary16: off by 2^-25 at most.
 #pragma once
 
 #include "kv_device.h"

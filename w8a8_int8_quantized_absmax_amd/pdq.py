@@ -686,7 +686,8 @@ def kv_append(k, v, cache: KVCache, batch: KVBatch, q=None, cos=None, sin=None, 
     and writes them into the cache -> the rotated q (None without q).
 
     k, v: [tokens, heads, dim] bf16 or f16; q: [tokens, hq, dim]; cos, sin: float32
-    [positions, rot / 2] (None: no rotation)."""
+    [positions, rot / 2] (None: no rotation); q_out: where the rotated q goes (q itself
+    for in place)."""
     index = cache.index
     if batch.index != index:
         raise ValueError("the cache and the batch must be on one device")
@@ -779,7 +780,7 @@ def kv_attention(q, cache: KVCache, batch: KVBatch, scale: float | None = None, 
             raise ValueError("workspace must be on q's device")
         size = workspace.numel()
     _kv_call("pdq_kv_attention", index, q.data_ptr(), _DT[q.dtype], tokens, hq, ldq, cache._ref, batch._ref,
-             dim ** -0.5 if scale is None else scale, softcap, window,
+             dim ** -0.5 if scale is None else float(scale), float(softcap), int(window),
              alibi_slopes.data_ptr() if alibi_slopes is not None else None,
              prefix_len.data_ptr() if prefix_len is not None else None, y.data_ptr(), ldy,
              lse.data_ptr() if lse is not None else None, workspace.data_ptr() if size else None, size)
