@@ -57,14 +57,17 @@ struct ValueStage {
 // here).  No unit is full: of the cycles the matrix units are busy for 42%, the
 // vector units for 46% (a weight costs a multiply-add, an exponential of two issue
 // slots, an addition and half a conversion; a code of K or V two and a half), LDS
-// for 40%; the waves of a SIMD wait for one another's unit and at the
-// step's barrier.  Tried and slower: the two waves of a SIMD held half a step
+// for 40%.  They overlap badly: beside a wave that issues matrix instructions back to
+// back, another wave's binary32 additions and multiply-adds hardly advance (57 in
+// 33000 cycles; exponentials and packed binary16 do, where the first leaves it a few
+// cycles between), so the two waves of a SIMD add their matrix and vector time.  Tried and slower: the two waves of a SIMD held half a step
 // apart by a second barrier (620 us), 64 rows a wave (790), 32 keys a step with
 // three waves a SIMD (609), four-wave workgroups, two a compute unit (590).
 template <int DT, int D, bool CAP, bool BIAS>
 __global__ __launch_bounds__(64 * waves(D), per_simd(D)) void k_attention_prompt(AttentionArgs a, int64_t items, int splits) {
     constexpr int KU = kKeys / 32, NU = kKeys / 16, NW = waves(D), kRows = tile_rows(D), NC = D / 16, NT = D / 32;
-    constexpr int kAhead = D == 128 ? 8 : 0;  // operands on their way from LDS while one is multiplied (where registers allow)
+    // operands on their way from LDS while one is multiplied, where registers allow (8192 tokens: 593 us without, 579 with)
+    constexpr int kAhead = D == 128 ? 8 : 0;
     constexpr int KB = kKeys * D / (64 * NW), VD = kKeys * D / (512 * NW);  // bytes of K, channels of V that a thread brings
     __shared__ KeyStage<D> ks[2];
     __shared__ ValueStage<D> vs[2];
