@@ -659,14 +659,20 @@ def _check_kv_rows(t, name, cache, heads=None, dtype=None):
         raise ValueError(f"{name}, the cache and the batch must be on one device")
     if t.dtype not in _HALF or (dtype is not None and t.dtype != dtype):
         raise ValueError(f"{name}: unsupported dtype {t.dtype}")
-    shape = t.shape
-    if len(shape) != 3 or shape[2] != cache.dim or (heads is not None and shape[1] != heads):
+    shape, dim = t.shape, cache.dim
+    if len(shape) != 3 or shape[2] != dim or (heads is not None and shape[1] != heads):
         raise ValueError(f"{name} of shape {tuple(shape)} given, [tokens, "
-                         f"{heads if heads is not None else 'heads'}, {cache.dim}] needed")
-    rows, stride = shape[0], t.stride()
-    if rows and (stride[2] != 1 or (shape[1] > 1 and stride[1] != cache.dim)):
+                         f"{heads if heads is not None else 'heads'}, {dim}] needed")
+    rows, each, _ = shape
+    pitch, head, one = t.stride()
+    if rows and (one != 1 or (each > 1 and head != dim)):
         raise ValueError(f"{name}: the heads of a row must lie side by side")
-    return stride[0] if rows > 1 else shape[1] * shape[2]
+    return pitch if rows > 1 else each * dim
+
+
+def _dense2(t):
+    """Whether a 2-D tensor is contiguous (is_contiguous() costs more than the strides)."""
+    return t.stride() == (t.shape[1], 1) or t.is_contiguous()
 
 
 def _kv_call(fn, index: int, *args) -> None:
@@ -675,7 +681,7 @@ def _kv_call(fn, index: int, *args) -> None:
     if index != torch._C._cuda_getDevice():
         with torch.cuda.device(index):
             return _kv_call(fn, index, *args)
-    st = getattr(lib(), fn)(*args, torch._C._cuda_getCurrentRawStream(index))
+    st = getattr(_lib or lib(), fn)(*args, torch._C._cuda_getCurrentRawStream(index))
     if st != 0:
         raise PdqError(fn, st)
 
@@ -701,8 +707,7 @@ def kv_append(k, v, cache: KVCache, batch: KVBatch, q=None, cos=None, sin=None, 
     positions = rot = hq = ldq = ldqo = 0
     if cos is not None:
         if (cos.dtype != torch.float32 or sin.dtype != torch.float32 or cos.dim() != 2 or cos.shape != sin.shape
-                or cos.get_device() != index or sin.get_device() != index or not cos.is_contiguous()
-                or not sin.is_contiguous()):
+                or cos.get_device() != index or sin.get_device() != index or not _dense2(cos) or not _dense2(sin)):
             raise ValueError("cos and sin must be contiguous float32 [positions, rot / 2] on k's device")
         positions, rot = cos.shape
         rot *= 2
@@ -712,7 +717,7 @@ def kv_append(k, v, cache: KVCache, batch: KVBatch, q=None, cos=None, sin=None, 
             raise ValueError("q and k must have the same rows")
         hq = q.shape[1]
         if q_out is None:
-            q_out = torch.empty((tokens, hq, cache.dim), dtype=dtype, device=cache.device)
+            q_out = q.new_empty((tokens, hq, cache.dim))
             ldqo = hq * cache.dim
         else:
             ldqo = _check_kv_rows(q_out, "q_out", cache, hq, dtype)
@@ -746,7 +751,6 @@ def kv_attention(q, cache: KVCache, batch: KVBatch, scale: float | None = None, 
         raise ValueError("the cache and the batch must be on one device")
     ldq = _check_kv_rows(q, "q", cache)
     tokens, hq, dim = q.shape
-    dev = cache.device
     if alibi_slopes is not None:
         _check_dense(alibi_slopes, "alibi_slopes", torch.float32, (hq,))
         if alibi_slopes.get_device() != index:
@@ -756,7 +760,7 @@ def kv_attention(q, cache: KVCache, batch: KVBatch, scale: float | None = None, 
         if prefix_len.get_device() != index:
             raise ValueError("prefix_len must be on q's device")
     if out is None:
-        y = torch.empty((tokens, hq, dim), dtype=q.dtype, device=dev)
+        y = q.new_empty((tokens, hq, dim))  # half the time of torch.empty with a dtype and a device
         ldy = hq * dim
     else:
         y = out
@@ -768,12 +772,12 @@ def kv_attention(q, cache: KVCache, batch: KVBatch, scale: float | None = None, 
         if lse.get_device() != index:
             raise ValueError("lse must be on q's device")
     elif want_lse:
-        lse = torch.empty((tokens, hq), dtype=torch.float32, device=dev)
+        lse = q.new_empty((tokens, hq), dtype=torch.float32)
     size = 0
     if workspace is None:
         size = kv_attention_workspace_bytes(tokens, batch.batch, hq, cache.heads, dim)
         if size:
-            workspace = torch.empty(size, dtype=torch.uint8, device=dev)
+            workspace = q.new_empty(size // 2)  # 16-bit values; size is a multiple of 256
     else:
         _check_dense(workspace, "workspace", torch.uint8)
         if workspace.get_device() != index:
