@@ -253,6 +253,18 @@ def test_attention_many_sequences():
     run_attention(Batch(421, length, new, 1, 64, 16), 2, "bf16")
 
 
+@pytest.mark.parametrize("n,hkv,dim", [(2, 1, 64), (9, 3, 64), (63, 2, 128), (64, 1, 64), (64, 7, 128), (65, 1, 64), (5, 2, 256)])
+def test_attention_many_prompts(n, hkv, dim):
+    # uneven prompts, some without rows, several of one length, rows before and behind them: every row once
+    r = np.random.default_rng(430 + n)
+    new = (r.choice([0, 1, 31, 32, 33, 97, 300], n) if n > 5 else r.integers(100, 400, n)).tolist()
+    new[-1] = 290
+    length = [int(m + k) for m, k in zip(new, r.choice([0, 0, 5, 130], n))]
+    run_attention(Batch(431 + n, length, new, hkv, dim, 32, lead=2, tail=3), 2 * hkv, "bf16")
+    if n < 10:
+        run_attention(Batch(432 + n, length[::-1], new[::-1], hkv, dim, 32), hkv, "f16", window=70)
+
+
 def test_attention_wide_scores():
     # scores of a few hundred, all weight on a key or two: the running maximum moves, nothing overflows
     b = Batch(430, [200, 130, 64], None, 1, 128, 32, single=True)

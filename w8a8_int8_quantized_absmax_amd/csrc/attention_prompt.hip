@@ -44,6 +44,47 @@ struct ValueStage {
     static __device__ __forceinline__ int piece(int t, int m) { return t * 512 + (t >> 1) * kSkew + m * 16; }
 };
 
+// The sum over a wavefront, in all lanes.
+__device__ __forceinline__ int lanes_sum(int v) {
+    v += __builtin_amdgcn_update_dpp(0, v, 0xB1, 0xf, 0xf, false);   // quad_perm [1, 0, 3, 2]
+    v += __builtin_amdgcn_update_dpp(0, v, 0x4E, 0xf, 0xf, false);   // quad_perm [2, 3, 0, 1]
+    v += __builtin_amdgcn_update_dpp(0, v, 0x141, 0xf, 0xf, false);  // row_half_mirror
+    v += __builtin_amdgcn_update_dpp(0, v, 0x140, 0xf, 0xf, false);  // row_mirror
+    return __builtin_amdgcn_readlane(v, 0) + __builtin_amdgcn_readlane(v, 16) + __builtin_amdgcn_readlane(v, 32) +
+           __builtin_amdgcn_readlane(v, 48);
+}
+
+// The row tile of rank `rank` when all sequences' tiles are taken by their number
+// from the last to the first (the later a tile, the more keys it sees), at equal
+// numbers by sequence; false: there are fewer.  One lane a sequence: with c(k) the
+// tiles numbered k or more, the tile's number is the k with c(k + 1) <= rank <
+// c(k).  Workgroups start in the order of their numbers, round the compute units:
+// prompts of uneven lengths then share them evenly (9 prompts of 347 to 1531
+// rows, 12 heads of 64: the busiest unit has 48 steps of 64 keys, 69 sequence by
+// sequence, of 35 on average; 52.6 us, 73).
+__device__ __forceinline__ bool heaviest_first(const AttentionArgs& a, int rows, int group, int rank, int& s, int64_t& tile) {
+    const int lane = threadIdx.x & 63;
+    const int mine = lane < a.b.batch ? (int)(((int64_t)kv_seq(a.b, lane).n * group + rows - 1) / rows) : 0;
+    int lo = 0, hi = lanes_sum(mine), above = 0;  // c(lo) > rank >= c(hi) = above
+    if (hi <= rank) return false;
+    while (hi - lo > 1) {
+        const int mid = lo + (hi - lo) / 2;
+        const int c = lanes_sum(max(mine - mid, 0));
+        if (c > rank) {
+            lo = mid;
+        } else {
+            hi = mid;
+            above = c;
+        }
+    }
+    const uint64_t level = __ballot(mine > lo);
+    const int before = __popcll(level & (((uint64_t)1 << lane) - 1));
+    const uint64_t at = __ballot(mine > lo && before == rank - above);
+    s = __builtin_amdgcn_readfirstlane(__ffsll((unsigned long long)at) - 1);
+    tile = lo;
+    return true;
+}
+
 // One workgroup takes tile_rows(D) rows (token, query head of the group) of one
 // key/value head over a part of their keys.  Scores are computed transposed, keys
 // x rows, in 32x32x16 products, so that a row's scores lie in one lane (and the one
@@ -75,10 +116,16 @@ __global__ __launch_bounds__(64 * waves(D), per_simd(D)) void k_attention_prompt
     const int i = lane & 31, h = lane >> 5;
     const int group = a.hq / a.c.heads;
     const int hk = blockIdx.x % a.c.heads;
-    const int64_t item = items - 1 - blockIdx.x / a.c.heads;  // the last rows of a prompt see most: first
-    const int s = a.b.cu_q ? item_seq(a.b, item, group, kRows, 1) : (int)(item / ((group + kRows - 1) / kRows));
-    const int64_t tile = a.b.cu_q ? item - item_start(a.b, s, group, kRows, 1)
-                                  : item - (int64_t)s * ((group + kRows - 1) / kRows);
+    int s;
+    int64_t tile;
+    if (a.b.cu_q && a.b.batch > 1 && a.b.batch <= 64 && gridDim.x <= 5 * 256 * (4 * per_simd(D) / NW)) {
+        if (!heaviest_first(a, kRows, group, (int)(blockIdx.x / a.c.heads), s, tile)) return;
+    } else {
+        const int64_t item = items - 1 - blockIdx.x / a.c.heads;  // a prompt's last rows see most: before its others
+        s = a.b.cu_q ? item_seq(a.b, item, group, kRows, 1) : (int)(item / ((group + kRows - 1) / kRows));
+        tile = a.b.cu_q ? item - item_start(a.b, s, group, kRows, 1)
+                        : item - (int64_t)s * ((group + kRows - 1) / kRows);
+    }
     const AttnSeq sq = attn_seq<true>(a, s);
     const int64_t rows = (int64_t)sq.q.n * group, r0 = tile * kRows;
     if (r0 >= rows) return;
