@@ -571,9 +571,10 @@ pdq_status pdq_kv_append(const void* k, const void* v, const void* q, pdq_dtype 
  *            hq, heads, dim) bytes, 256-byte aligned; its contents on entry do not
  *            matter and nothing in it carries over; calls that overlap in time
  *            (other streams, other graphs) need one each
- * Scores, the softmax's maximum and sum and both products are held in binary32; a
- * weight of the softmax is rounded to binary16 (11 bits) for the product with the
- * value codes.  Scales must be at least 2^-64 in magnitude (pdq_kv_append's are).
+ * Scores, the softmax's maximum and sum and both products are held in binary32: a
+ * score's error counts a few 2^-24 of the largest |z| that its row sees, and with a
+ * cap up to 2^-20 softcap.  A weight of the softmax is rounded to binary16 (11 bits)
+ * for the product with the value codes.  Scales must be at least 2^-64 in magnitude (pdq_kv_append's are).
  */
 size_t pdq_kv_attention_workspace(int64_t tokens, int64_t batch, int64_t hq, int64_t heads, int64_t dim);
 

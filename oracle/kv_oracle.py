@@ -68,7 +68,7 @@ def append(cache, table, seq_len, cu_q, k, v, q=None, cos=None, sin=None, interl
                 for h in range(heads):
                     x = np.stack([n[which][h] for n in new])
                     held = scale[p, h] if first > 0 else F(0)
-                    if not np.isfinite(x).all() or np.isnan(held):
+                    if not np.isfinite(x).all() or not np.isfinite(held):
                         scale[p, h] = np.nan
                         codes[p, h, first:first + len(new)] = 0
                         continue

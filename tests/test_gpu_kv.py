@@ -126,6 +126,18 @@ def test_append_extreme_values():
     check_cache(host_cache(c), ref)
 
 
+def test_append_behind_scales_that_are_not_finite():
+    b = Batch(55, [9, 9, 9, 9], [2] * 4, 1, 64, 16)
+    for s, value in enumerate((np.inf, -np.inf, np.nan, 0.5)):
+        b.cache["k_scale"][b.table[s, 0]] = b.cache["v_scale"][b.table[s, 0]] = value
+    c, ref = b.device_cache(), b.copy_cache()
+    x, y = b.rows(1, "bf16"), b.rows(1, "bf16")
+    pdq.kv_append(x.cuda(), y.cuda(), c, b.device_batch())
+    KO.append(ref, b.table, b.seq_len, b.cu_q, _f32(x), _f32(y))
+    assert np.isnan(ref["k_scale"][b.table[:3, 0], 0]).all()
+    check_cache(host_cache(c), ref)
+
+
 def test_append_positions_outside_the_tables():
     run_append(Batch(60, [20, 40], [5, 9], 2, 64, 16), "bf16", hq=2, rot=32, positions=18)
 

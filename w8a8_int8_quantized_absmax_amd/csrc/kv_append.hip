@@ -267,7 +267,7 @@ __global__ __launch_bounds__(NT) void k_kv_append(KvAppendArgs a, int64_t kv_blo
 #pragma unroll
         for (int i = 0; i < NT / 64; ++i) top = max(top, part[i]);
     }
-    const bool finite = top < 0x7f800000u && held == held;
+    const bool finite = top < 0x7f800000u && fabsf(held) < INFINITY;
     const float need = fmaxf(__uint_as_float(top) * (1.0f / 127.0f), kMinScale);
     const float now = finite ? fmaxf(held, need) : __builtin_nanf("");
     const float inv = 1.0f / now;
