@@ -95,8 +95,7 @@ __device__ __forceinline__ int2* parts_of(const AttentionArgs& a, int64_t item, 
 // The number of a sequence's first row tile.
 template <int R>
 __device__ __forceinline__ int64_t first_item(const AttentionArgs& a, int s) {
-    const int group = a.hq / a.c.heads;
-    return a.b.cu_q ? item_start(a.b, s, group, R, 1) : (int64_t)s * ((group + R - 1) / R);
+    return item_start(a.b, s, a.hq / a.c.heads, R, 1);
 }
 
 template <int DT, int D>
@@ -514,10 +513,13 @@ __global__ __launch_bounds__(256) void k_attention_join(AttentionArgs a) {
     const int64_t item = blockIdx.x / a.c.heads;
     const int hk = (int)(blockIdx.x - item * a.c.heads), j = blockIdx.y;
     const int2 parts = *parts_of<D, R>(a, item, hk);
-    const int s = a.b.cu_q ? item_seq(a.b, item, group, R, 1) : (int)(item / ((group + R - 1) / R));
+    int s;
+    int64_t tile;
+    // an item that is no tile: nobody wrote its parts, and nothing that they say may be used
+    if (!item_of(a.b, item, group, R, 1, s, tile)) return;
     const KvSeq q = kv_seq<true>(a.b, s);
-    const int64_t rr = (item - first_item<R>(a, s)) * R + j;
-    if (rr >= (int64_t)q.n * group) return;  // also: no tile, whose parts nobody wrote
+    const int64_t rr = tile * R + j;
+    if (rr >= (int64_t)q.n * group) return;
     const int w0 = parts.x >> 1, w1 = parts.y;
     if (w1 < 0) return;
 

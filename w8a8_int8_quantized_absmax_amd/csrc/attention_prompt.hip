@@ -122,9 +122,7 @@ __global__ __launch_bounds__(64 * waves(D), per_simd(D)) void k_attention_prompt
         if (!heaviest_first(a, kRows, group, (int)(blockIdx.x / a.c.heads), s, tile)) return;
     } else {
         const int64_t item = items - 1 - blockIdx.x / a.c.heads;  // a prompt's last rows see most: before its others
-        s = a.b.cu_q ? item_seq(a.b, item, group, kRows, 1) : (int)(item / ((group + kRows - 1) / kRows));
-        tile = a.b.cu_q ? item - item_start(a.b, s, group, kRows, 1)
-                        : item - (int64_t)s * ((group + kRows - 1) / kRows);
+        if (!item_of(a.b, item, group, kRows, 1, s, tile)) return;
     }
     const AttnSeq sq = attn_seq<true>(a, s);
     const int64_t rows = (int64_t)sq.q.n * group, r0 = tile * kRows;

@@ -164,14 +164,9 @@ __global__ __launch_bounds__(NT) void k_kv_append(KvAppendArgs a, int64_t kv_blo
     const int64_t item = rest / a.c.heads;
     const int h = (int)(rest - item * a.c.heads);
     const int page = a.c.page;
-    int s, j;
-    if (a.b.cu_q) {
-        s = item_seq(a.b, item, 1, page, 2);
-        j = (int)min(item - item_start(a.b, s, 1, page, 2), (int64_t)1 << 30);
-    } else {
-        s = (int)item;
-        j = 0;
-    }
+    int s;
+    int64_t j;
+    if (!item_of(a.b, item, 1, page, 2, s, j)) return;
     const KvSeq q = kv_seq<true>(a.b, s);
     if (q.n == 0) return;
     // the j-th page that the new tokens touch; tokens at negative positions are not written

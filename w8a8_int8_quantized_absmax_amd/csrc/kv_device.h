@@ -2,8 +2,8 @@
 // a sequence's new tokens lie, which rows a work item is.
 #pragma once
 
+#include "kv_items.h"
 #include "pdq_device.h"
-#include "pdq_kernels.h"
 
 namespace pdq {
 
@@ -46,31 +46,6 @@ __device__ __forceinline__ KvSeq kv_seq(const KvBatch& b, int s) {
     r.len = min(max(load_as<Uniform>(b.seq_len + s), 0), 1 << 30);
     r.p0 = r.len - r.n;
     return r;
-}
-
-// Work items of a sequence are numbered without a prefix sum: those of sequence
-// s begin at floor(cu_q[s] * mul / per) + extra * s.  floor(a + b) >= floor(a) +
-// floor(b), so a sequence of n rows has room for floor(n * mul / per) + extra
-// items.  item_seq finds the sequence of item w (the last one that begins at or
-// before it): 64 candidates a step, one step for up to 64 sequences.  The whole
-// wavefront calls it with the same w.
-__device__ __forceinline__ int64_t item_start(const KvBatch& b, int s, int mul, int per, int extra) {
-    const int q0 = b.cu_q ? min(max(b.cu_q[s], 0), b.tokens) : s;
-    return (int64_t)q0 * mul / per + (int64_t)extra * s;
-}
-
-__device__ __forceinline__ int item_seq(const KvBatch& b, int64_t w, int mul, int per, int extra) {
-    const int lane = threadIdx.x & 63;
-    int lo = 0, n = b.batch;
-    while (n > 1) {
-        const int step = (n + 63) / 64;
-        const int i = lo + lane * step;
-        const bool in = lane * step < n && item_start(b, i, mul, per, extra) <= w;
-        const int k = max(__popcll(__ballot(in)), 1) - 1;
-        lo += k * step;
-        n = min(step, n - k * step);
-    }
-    return __builtin_amdgcn_readfirstlane(lo);
 }
 
 // The sequence of row t, the same in the whole wavefront: the last one that
