@@ -263,8 +263,7 @@ __global__ __launch_bounds__(256, resident(D, NQ)) void k_attention_few(Attentio
     ahead();
     for (;;) {
         if (NQ > 1) queries();
-        // the tile's rows: queries as binary16 operands (bfloat16 ones scaled to the row's largest exponent, so that
-        // what binary16 cannot hold is below 2^-39 of the row's largest), the keys that each row sees
+        // the tile's rows: queries as binary16 operands (bfloat16 ones as row_exponent says), the keys that each row sees
         v8h qf[NQ][NC];
         int lo[NQ], hi[NQ], pos[NQ];
         float f[NQ], slope[NQ], M[NQ], l[NQ];
@@ -296,7 +295,7 @@ __global__ __launch_bounds__(256, resident(D, NQ)) void k_attention_few(Attentio
             if constexpr (DT == kBF16) {
                 top = fmaxf(top, __shfl_xor(top, 16));
                 top = fmaxf(top, __shfl_xor(top, 32));
-                e = top > 0.0f && top < INFINITY ? __builtin_amdgcn_frexp_expf(top) : 14;
+                e = row_exponent(top);
             }
 #pragma unroll
             for (int c = 0; c < NC; ++c)

@@ -50,6 +50,15 @@ __device__ __forceinline__ float capped(float x2, float cap2) {
     return cap2 * (1.0f - 2.0f * r);
 }
 
+// A row of bfloat16 queries with the largest magnitude `top` becomes binary16 times
+// 2^(14 - e): the largest lies in [2^13, 2^14), and what binary16 rounds away is at most
+// 2^-25, 2^-38 of it.  A row below 2^-96 takes 2^109, which makes every bfloat16 number,
+// a multiple of 2^-133, one of binary16's, exactly: its factor scale * 2^(e - 14) stays
+// among binary32's normal numbers (from a scale of 2^-17 on), whatever page scales follow.
+__device__ __forceinline__ int row_exponent(float top) {
+    return top > 0.0f && top < INFINITY ? max(__builtin_amdgcn_frexp_expf(top), -95) : 14;
+}
+
 // A sequence's rows and keys as a tile of R rows takes them: rows are (token,
 // query head of the group), the keys seen by any of its rows k0 .. last.
 struct AttnSeq {

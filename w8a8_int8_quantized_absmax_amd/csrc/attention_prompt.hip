@@ -164,7 +164,7 @@ __global__ __launch_bounds__(64 * waves(D), per_simd(D)) void k_attention_prompt
         int e = 14;
         if constexpr (DT == kBF16) {
             top = fmaxf(top, __shfl_xor(top, 32));
-            e = top > 0.0f && top < INFINITY ? __builtin_amdgcn_frexp_expf(top) : 14;
+            e = row_exponent(top);
         }
 #pragma unroll
         for (int c = 0; c < NC; ++c) {
