@@ -559,7 +559,9 @@ pdq_status pdq_kv_append(const void* k, const void* v, const void* q, pdq_dtype 
  *            the cache's heads (query head h reads key/value head h / (hq / heads))
  *   scores   z = scale * S_k[page] * (q . codes), then z = softcap * tanh(z /
  *            softcap) if softcap > 0, then z += slopes[h] * (key - row) positions
- *            if slopes (float [hq]) is not NULL
+ *            if slopes (float [hq]) is not NULL.  scale or softcap not
+ *            finite, softcap < 0, and a scale or a scale / softcap near binary32's
+ *            end (2 log2 e times it is not finite): PDQ_ERR_UNSUPPORTED
  *   mask     a row at position p sees the keys
  *            max(0, p - window + 1) (0 if window == 0) .. min(max(p, prefix[s] - 1),
  *            seq_len[s] - 1); prefix (int32 [batch], or NULL: causal) makes the

@@ -53,3 +53,13 @@ def test_many_weights_far_below_the_largest(rows):
 
     b.rows = ones
     run_attention(b, 2, "f16", scale=20 * np.log(2.0) / 64)
+
+
+def test_tiny_caps():
+    # far below any score, and still a cap: all of a row's keys weigh the same
+    b = Batch(940, [70, 33], None, 2, 64, 16, single=True)
+    b.cache["k"][b.table[0, 0], 0, 3:7] = 0  # products of zero among them
+    run_attention(b, 4, "bf16", softcap=2.0 ** -100)
+    b = Batch(941, [70], [60], 1, 128, 16)
+    b.cache["k"][b.table[0, 0], 0, 3:7] = 0
+    run_attention(b, 2, "f16", softcap=2.0 ** -100)

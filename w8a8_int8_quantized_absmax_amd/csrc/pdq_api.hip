@@ -856,6 +856,9 @@ pdq_status pdq_kv_attention(const void* q, pdq_dtype dt, int64_t tokens, int64_t
     PDQ_TRY(check_rows(q, tokens, hq, a.c.dim, ldq));
     PDQ_TRY(check_rows(y, tokens, hq, a.c.dim, ldy));
     if (!isfinite(scale) || !isfinite(softcap) || softcap < 0.0f) return PDQ_ERR_UNSUPPORTED;
+    // the factors that the kernels form of them, which times a zero product would be NaN
+    if (!isfinite(1.4426950408889634f * scale) || !isfinite(softcap > 0.0f ? 2.0f * 1.4426950408889634f / softcap * scale : 0.0f))
+        return PDQ_ERR_UNSUPPORTED;
     if (!aligned(slopes, 4) || !aligned(prefix, 4) || !aligned(lse, 4)) return PDQ_ERR_ALIGN;
     const size_t need = pdq_kv_attention_workspace(tokens, a.b.batch, hq, a.c.heads, a.c.dim);
     if (need > 0 && (!workspace || workspace_bytes < need)) return PDQ_ERR_WORKSPACE;
