@@ -25,7 +25,8 @@
  * Arithmetic (identical on every entry point):
  *   rne(v)            round to nearest integer, ties to even
  *   symmetric scale   S = C / 127 (binary32, correctly rounded division) for
- *                     an absmax C; S = 1 when C == 0
+ *                     an absmax C; S = 1 when C == 0 (the key/value cache's
+ *                     page scales follow their own rule: pdq_kv_append)
  *   symmetric code    q = clamp(rne(x / S), -127, 127)       (x / S correctly rounded)
  *   asymmetric code   q = clamp(rne(x / S) + Z, -128, 127)
  *   dequant epilogue  y = (S_x * S_w) * (float)acc' [+ bias], every operation
@@ -559,9 +560,11 @@ pdq_status pdq_kv_append(const void* k, const void* v, const void* q, pdq_dtype 
  *            the cache's heads (query head h reads key/value head h / (hq / heads))
  *   scores   z = scale * S_k[page] * (q . codes), then z = softcap * tanh(z /
  *            softcap) if softcap > 0, then z += slopes[h] * (key - row) positions
- *            if slopes (float [hq]) is not NULL.  scale or softcap not
- *            finite, softcap < 0, and a scale or a scale / softcap near binary32's
- *            end (2 log2 e times it is not finite): PDQ_ERR_UNSUPPORTED
+ *            if slopes (float [hq]) is not NULL: a signed distance, negative for the
+ *            keys before a row; where prefix shows a row keys ahead of it, a positive
+ *            slope raises those.  scale or softcap not finite, softcap < 0, and a
+ *            scale or a scale / softcap near binary32's end (2 log2 e times it is not
+ *            finite): PDQ_ERR_UNSUPPORTED
  *   mask     a row at position p sees the keys
  *            max(0, p - window + 1) (0 if window == 0) .. min(max(p, prefix[s] - 1),
  *            seq_len[s] - 1); prefix (int32 [batch], or NULL: causal) makes the
@@ -573,10 +576,21 @@ pdq_status pdq_kv_append(const void* k, const void* v, const void* q, pdq_dtype 
  *            hq, heads, dim) bytes, 256-byte aligned; its contents on entry do not
  *            matter and nothing in it carries over; calls that overlap in time
  *            (other streams, other graphs) need one each
- * Scores, the softmax's maximum and sum and both products are held in binary32: a
- * score's error counts a few 2^-24 of the largest |z| that its row sees, and with a
- * cap up to 2^-20 softcap.  A weight of the softmax is rounded to binary16 (11 bits)
- * for the product with the value codes.  Scales must be at least 2^-64 in magnitude (pdq_kv_append's are).
+ *   y, lse and the workspace overlap nothing else that the call reads or writes.
+ * The page scales of visible keys must be 2^-64 or more (pdq_kv_append's are, or NaN: rows
+ * that see such a page are NaN).  A value scale's logarithm enters the weights: with
+ * one that is negative the rows that see its page are NaN, with one of 0 its keys
+ * do not count.
+ * Scores, the softmax's maximum and sum and both products are held in binary32.  The
+ * error of a row's scores counts a few 2^-24 of the largest |z|, |ln S_v| and 1 among
+ * its visible keys, dim 2^-24 at most of the largest sum of |scale S_k q code| over a
+ * key's channels, and with a cap up to 2^-20 softcap.  For the product with the value
+ * codes a weight times its value scale is rounded to binary16: by 2^-11 of itself, or
+ * where that is less than 2^-18 of the row's largest, by 2^-29 of the largest.  y is
+ * rounded to dt.
+ * One kernel serves a call, by the batch's average of rows: a batch that mixes
+ * sequences of one new row with a prompt's chunk is faster as two calls on the same
+ * buffers, cu_q of the second beginning behind the first's rows.
  */
 size_t pdq_kv_attention_workspace(int64_t tokens, int64_t batch, int64_t hq, int64_t heads, int64_t dim);
 

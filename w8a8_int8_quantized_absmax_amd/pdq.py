@@ -745,7 +745,10 @@ def kv_attention(q, cache: KVCache, batch: KVBatch, scale: float | None = None, 
 
     scale: 1 / sqrt(dim) by default; softcap > 0: scores capped by softcap *
     tanh(z / softcap); window > 0: the last window keys; alibi_slopes float32 [hq]:
-    a bias by distance; prefix_len int32 [batch]: tokens that every row sees."""
+    slope * (key - row) added, the signed distance (keys ahead of a row, which only
+    prefix_len shows, gain by a positive slope); prefix_len int32 [batch]: tokens that
+    every row sees.  A batch that mixes single rows with a prompt's chunk is faster as
+    two calls, the second's cu_q beginning behind the first's rows."""
     index = cache.index
     if batch.index != index:
         raise ValueError("the cache and the batch must be on one device")
