@@ -34,7 +34,11 @@ __device__ __forceinline__ Units units_of(const AttentionArgs& a, int s) {
     return u;
 }
 
-// Workgroups of the few-row kernel that the chip holds at once, one range each.
+// Workgroups of the few-row kernel that the chip holds at once, one range each: as many as a
+// compute unit's registers hold without spilling.  With 128 channels two against three and four, joins included: 32
+// sequences up to 4096 keys 43 us against 53 and 68, one of 131071 51 against 58 and 99, 96 up to 16384 354 against 355
+// and 516.  With 256 channels a lane takes 394 registers; held to the 256 of two workgroups it spills, and 24 sequences of
+// up to five rows and 6011 keys take 66 us instead of 51.
 constexpr int resident(int D, int NQ) { return D == 256 ? 1 : D == 128 ? 2 : NQ == 1 ? 4 : 2; }
 constexpr int ways(int D, int R) { return 256 * resident(D, R / 16); }
 
@@ -122,13 +126,11 @@ __device__ __forceinline__ void write_row(const AttentionArgs& a, int64_t row, i
 // written out.
 //
 // Bound by the cache's bytes, 2 D a key and head, at long contexts (one read at
-// the card's best, 6.2 TB/s): 96 sequences up to 16384 keys (1.93 GB) 344 us, 5.6
+// the card's best, 6.2 TB/s): 96 sequences up to 16384 keys (1.93 GB) 341 us, 5.7
 // TB/s; one of 131071 (268 MB) 52 us, 5.2 TB/s, of which some 5 us are its begin:
 // lengths, range, page, codes, one after the other.  32 sequences up to 4096 (139
 // MB) 38 us, 3.7 TB/s: beside the begin, the 1.5 segments of a workgroup.  The
-// equal ranges are what ragged lengths need; three workgroups a compute unit
-// instead of two with 128 channels: 48.0 against 48.3 us there, 61.5 against 60.0 for
-// the one long sequence; four: 64 and 93.  K straight into the operand layout
+// equal ranges are what ragged lengths need.  K straight into the operand layout
 // keeps LDS out of the loop; converting the codes takes 160 of some 250 vector
 // instructions a tile, 22% of the time at most.
 template <int DT, int D, int NQ>
@@ -503,7 +505,7 @@ __global__ __launch_bounds__(256, resident(D, NQ)) void k_attention_few(Attentio
 
 // Joins the partial results of a segment that was cut: one workgroup for each
 // (row tile of a sequence, head; row), D / 8 threads for each of 2048 / D parts
-// at a time.  All latency: 4.7 us for 32 x 4096 and for 1 x 131071 keys.
+// at a time.  All latency: 4.7 us for 32 x 4096 and for 1 x 131071 keys, 6.4 for 24 x 6011 with 256 channels.
 template <int DT, int D, int R>
 __global__ __launch_bounds__(256) void k_attention_join(AttentionArgs a) {
     constexpr int NP = 2048 / D;  // parts taken at once
@@ -562,9 +564,14 @@ __global__ __launch_bounds__(256) void k_attention_join(AttentionArgs a) {
 }
 
 // 16-row tiles of the few-row kernel for a batch: enough for the rows that a
-// sequence has on average; 0: the prompt kernel.  Measured on 8 sequences of 4000
-// keys, 128 channels: 32 rows 31 us against 73 of the prompt kernel, 64 rows 43
-// against 38; with 256 channels 64 rows 51 against 70.
+// sequence has on average; 0: the prompt kernel.  8 sequences of 4000 keys, this kernel
+// against the prompt kernel, us (8 key/value heads; with 256 channels 8 and 2):
+//   rows    64 channels   128 channels   256, 8 heads   256, 2 heads
+//   24      25 / 25       29 / 34        54 / 62        30 / 47
+//   32      28 / 26       31 / 34        56 / 62        32 / 48
+//   48      35 / 29       40 / 36        82 / 65        36 / 51
+//   64      37 / 30       42 / 37        84 / 68        37 / 54
+// With 256 channels the limit of 64 is that of few heads and sequences; with many, 32 would be the better one.
 int row_tiles(int64_t tokens, int64_t batch, int hq, int hkv, int dim) {
     const int64_t rows = (tokens * (hq / hkv) + batch - 1) / batch;
     return rows <= 16 ? 1 : rows <= (dim == 256 ? 64 : 32) ? 2 : 0;

@@ -61,7 +61,10 @@ __device__ __forceinline__ int lanes_sum(int v) {
 // c(k).  Workgroups start in the order of their numbers, round the compute units:
 // prompts of uneven lengths then share them evenly (9 prompts of 347 to 1531
 // rows, 12 heads of 64: the busiest unit has 48 steps of 64 keys, 69 sequence by
-// sequence, of 35 on average; 52.6 us, 73).
+// sequence, of 35 on average; 53 us, 72).  Used up to five times the workgroups that fit,
+// with / without it, us: 3.2 times (40 prompts, 64 channels) 64 / 73, 3.3 (7 prompts, 128 channels) 96 / 103, 3.7 (8, 256
+// channels) 150 / 171; beyond, 7.1 (64 channels) 179 / 186, 7.4 (128) 210 / 213, 13 (128) 358 / 357, 16 (256) 474 / 484, 25
+// (128) 637 / 633: there the many tiles even out by themselves.
 __device__ __forceinline__ bool heaviest_first(const AttentionArgs& a, int rows, int group, int rank, int& s, int64_t& tile) {
     const int lane = threadIdx.x & 63;
     const int mine = lane < a.b.batch ? (int)(((int64_t)kv_seq(a.b, lane).n * group + rows - 1) / rows) : 0;
@@ -101,13 +104,13 @@ __device__ __forceinline__ bool heaviest_first(const AttentionArgs& a, int rows,
 // for 40%.  They overlap badly: beside a wave that issues matrix instructions back to
 // back, another wave's binary32 additions and multiply-adds hardly advance (57 in
 // 33000 cycles; exponentials and packed binary16 do, where the first leaves it a few
-// cycles between), so the two waves of a SIMD add their matrix and vector time.  Tried and slower: the two waves of a SIMD held half a step
-// apart by a second barrier (620 us), 64 rows a wave (790), 32 keys a step with
-// three waves a SIMD (609), four-wave workgroups, two a compute unit (590).
+// cycles between), so the two waves of a SIMD add their matrix and vector time.  Tried and slower, each
+// on a form of 580 to 607 us: the two waves of a SIMD held half a step apart by a second barrier (620 us),
+// 64 rows a wave (790), 32 keys a step with three waves a SIMD (609), four-wave workgroups, two a compute unit (590).
 template <int DT, int D, bool CAP, bool BIAS>
 __global__ __launch_bounds__(64 * waves(D), per_simd(D)) void k_attention_prompt(AttentionArgs a, int64_t items, int splits) {
     constexpr int KU = kKeys / 32, NU = kKeys / 16, NW = waves(D), kRows = tile_rows(D), NC = D / 16, NT = D / 32;
-    // operands on their way from LDS while one is multiplied, where registers allow (8192 tokens: 593 us without, 579 with)
+    // operands on their way from LDS while one is multiplied, where registers allow (8192 tokens: 577 to 587 us without, 563 with)
     constexpr int kAhead = D == 128 ? 8 : 0;
     constexpr int KB = kKeys * D / (64 * NW), VD = kKeys * D / (512 * NW);  // bytes of K, channels of V that a thread brings
     __shared__ KeyStage<D> ks[2];
@@ -514,8 +517,14 @@ int attention_prompt_most_splits(int64_t tokens, int64_t batch, int hq, int hkv,
 
 // Parts of the keys that each tile of rows is cut into: the fewest microseconds
 // of rounds of workgroups, each some 6 and 2 a step, and of the join, some 4 and
-// 0.4 a part (measured with 128 channels: 110 rows x 2 heads of a group over 4842
-// keys 34 / 31 / 36 us in 8 / 16 / 32 parts).  keys: what the table can name.
+// 0.4 a part.  keys: what the table can name; a window that hides most of them is not
+// known here, so windowed chunks are cut more than they need (700 rows, window 128: 31 us, 17 uncut).
+// The constants are those of 128 channels and serve 64 and 256 too.  us in 8 / 16 / 32 parts and in the rule's:
+//                                  64 channels            128                    256
+//   110 tokens, 4842 keys, 1 head  25 / 24 / 31, 19: 23   37 / 31 / 38, 19: 31   50 / 39 / 44, 19: 38
+//   512 tokens, 2000 keys, 1 head  19 / 22 / 33, 11: 19   26 / 30 / 42, 11: 27   35 / 38 / 56, 11: 35
+//   130 tokens, 16000 keys, 8 (4)  69 / 58 / 66, 18: 55   83 / 97 / 104, 10: 72  122 / 134 / 136, 12: 92
+// (key/value heads, each with two query heads, in the last row with four).
 int attention_prompt_splits(int64_t tokens, int64_t batch, int hq, int hkv, int dim, int64_t keys) {
     const int most = attention_prompt_most_splits(tokens, batch, hq, hkv, dim);
     const int64_t n = tiles(tokens, batch, hq, hkv, dim), steps = (keys + kKeys - 1) / kKeys;
