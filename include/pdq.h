@@ -599,6 +599,156 @@ pdq_status pdq_kv_attention(const void* q, pdq_dtype dt, int64_t tokens, int64_t
                             int64_t window, const float* slopes, const int32_t* prefix, void* y, int64_t ldy,
                             float* lse, void* workspace, size_t workspace_bytes, void* stream);
 
+/*
+ * 8-bit floating-point (FP8) linear layers with a scale for each block of 128.
+ *
+ * Codes are e4m3 values (the OCP format: 448 the largest magnitude, no infinity).
+ * A block's scale S is a power of two in the e8m0 format (byte b: 2^(b - 127), 255:
+ * NaN), of weights also any binary32 value:
+ *   activations  one S for each row and group of 128 K values (the last group of a
+ *                row may be shorter); weights one for each block of 128 output
+ *                channels x 128 K values (the last ones of either may be smaller)
+ *   S            the smallest power of two with C <= 448 S, C the largest magnitude
+ *                of the group or block, at least 2^-127; 1 if C == 0; NaN if a value
+ *                is not finite (its codes are 0: what is made of it is NaN)
+ *   code         e4m3(x / S), rounded to nearest even.  The division is exact: the
+ *                code is off by half a step of e4m3 (2^-4 relative from 2^-6 up,
+ *                2^-10 absolute below) and by nothing else.
+ *   product      y[m, n] = sum over groups g of S_x[m, g] S_w[n / 128, g] sum_{k in g}
+ *                xq[m, k] wq[n, k] [+ bias[n]], sums in binary32 (in an order of the
+ *                kernel's own, the same on every call), rounded once to y's type.  A
+ *                power-of-two S_w enters the matrix instruction; a binary32 one
+ *                multiplies the group's sum.  The matrix unit aligns the products of eight
+ *                neighbouring K values to the largest of their exponents and keeps 13 bits
+ *                behind it: each loses less than 2^-13 of the eight's largest magnitude (some
+ *                2^-14 of y's size over many outputs).
+ * An FP8 matrix is packed as an INT8 one is (pdq_quantize_weight), with K padded to a
+ * multiple of 128: pdq_fp8_bytes(rows, K) bytes, rows and K values beyond the matrix
+ * 0.  Scales of a row (of a weight's 128 rows) are followed by padding up to
+ * pdq_fp8_scale_pitch(K) = 4 ceil(K / 512) of them.  K, alignment and the sizes'
+ * limits as above.  A call on `count` matrices takes them one behind the other.
+ */
+typedef enum {
+    PDQ_E8M0 = 0,      /* a power of two, one byte */
+    PDQ_SCALE_F32 = 1, /* binary32                 */
+    PDQ_SCALE_MIN_ENUM_ = -0x7fffffff - 1,
+    PDQ_SCALE_MAX_ENUM_ = 0x7fffffff
+} pdq_scale_type;
+
+size_t pdq_fp8_bytes(int64_t rows, int64_t K);
+int64_t pdq_fp8_scale_pitch(int64_t K);
+
+/*
+ * Weights, once:
+ *   w        [N, K] of w_dt, row pitch ldw; `count` of them, `stride` elements apart
+ *            (a multiple of 16 bytes, and at least (N - 1) ldw + K)
+ *   wq       count * pdq_fp8_bytes(N, K) bytes out
+ *   w_scale  e8m0 out [count, ceil(N / 128), pdq_fp8_scale_pitch(K)]
+ * pdq_pack_weight_fp8 takes codes and scales that are there already (a checkpoint's):
+ *   codes    e4m3 [count, N, K], contiguous
+ *   scale    [count, ceil(N / 128), ceil(K / 128)] of scale_t, contiguous; w_scale likewise
+ *            of scale_t
+ */
+pdq_status pdq_quantize_weight_fp8(const void* w, pdq_dtype w_dt, int64_t count, int64_t N, int64_t K, int64_t ldw,
+                                   int64_t stride, uint8_t* wq, uint8_t* w_scale, void* stream);
+pdq_status pdq_pack_weight_fp8(const uint8_t* codes, const void* scale, pdq_scale_type scale_t, int64_t count,
+                               int64_t N, int64_t K, uint8_t* wq, void* w_scale, void* stream);
+
+/*
+ * Linear layer: pdq_quantize_fp8, then pdq_gemm_fp8.
+ *   x        [M, K] of x_dt, row pitch ldx
+ *   xq       packed codes out, pdq_fp8_bytes(M, K) bytes, 16-byte aligned
+ *   x_scale  e8m0 out [M, pdq_fp8_scale_pitch(K)], 4-byte aligned
+ *   wq, w_scale (16-byte aligned), scale_t  one matrix of pdq_quantize_weight_fp8 or pdq_pack_weight_fp8
+ *   bias     [N] float or NULL
+ *   y        [M, N] of y_dt (BF16 or F16) out, row pitch ldy >= N
+ */
+pdq_status pdq_quantize_fp8(const void* x, pdq_dtype x_dt, int64_t M, int64_t K, int64_t ldx, uint8_t* xq,
+                            uint8_t* x_scale, void* stream);
+pdq_status pdq_gemm_fp8(const uint8_t* xq, const uint8_t* x_scale, int64_t M, int64_t K, const uint8_t* wq,
+                        const void* w_scale, pdq_scale_type scale_t, const float* bias, int64_t N, void* y,
+                        pdq_dtype y_dt, int64_t ldy, void* stream);
+pdq_status pdq_linear_fp8(const void* x, pdq_dtype x_dt, int64_t M, int64_t K, int64_t ldx, const uint8_t* wq,
+                          const void* w_scale, pdq_scale_type scale_t, const float* bias, int64_t N, uint8_t* xq,
+                          uint8_t* x_scale, void* y, pdq_dtype y_dt, int64_t ldy, void* stream);
+
+/*
+ * Routing of tokens to experts.
+ *   logits   [tokens, experts] of dt, row pitch ldl >= experts (elements), any alignment of
+ *            its type; experts 1 .. 512, tokens * k at most 2^30
+ *   rule     (host struct) score: of a logit z, softmax over the row or 1 / (1 + exp(-z));
+ *            k experts a token, 1 .. min(experts, 32);
+ *            groups: equal runs of consecutive experts (1 .. 64, a divisor of experts), of
+ *            which the best top_groups stay, by the sum of their group_score (1 or 2) largest
+ *            choice values; renormalize != 0: a token's weights are divided by their sum;
+ *            scale: then multiplied by it (finite)
+ *   bias     [experts] float or NULL: added to the scores for the choice alone
+ *   choice   the k largest values of score + bias, formed in binary64; without a bias the
+ *            logits themselves order the experts (and the scores the groups).  Equal values go
+ *            to the lower index, of experts and of groups.
+ *   ids      int32 [tokens, k] out, in descending order of their values; -1 where there is
+ *            none: a logit (or value) of -INF is never chosen
+ *   weights  float [tokens, k] out: the chosen scores, renormalized, scaled; 0 at an id of -1
+ *            and where the sum to divide by is 0.  A row that holds a NaN ranks it below
+ *            every number and has NaN weights; logits of +INF share a softmax's weight.
+ *   offsets, rows   int32 [experts + 1], [tokens * k] out: the tokens of each expert,
+ *            rows[offsets[e]] .. rows[offsets[e + 1] - 1], as token * k + slot, ascending;
+ *            -1 from offsets[experts] on
+ *   workspace  device scratch of at least pdq_route_workspace(tokens, experts) bytes, 256-byte
+ *            aligned; as pdq_kv_attention's
+ */
+enum { PDQ_SOFTMAX = 0, PDQ_SIGMOID = 1 };
+
+typedef struct pdq_route_rule {
+    int32_t score, k, groups, top_groups, group_score, renormalize;
+    float scale;
+} pdq_route_rule;
+
+size_t pdq_route_workspace(int64_t tokens, int64_t experts);
+
+pdq_status pdq_route_experts(const void* logits, pdq_dtype dt, int64_t tokens, int64_t experts, int64_t ldl,
+                             const float* bias, const pdq_route_rule* rule, int32_t* ids, float* weights,
+                             int32_t* offsets, int32_t* rows, void* workspace, size_t workspace_bytes, void* stream);
+
+/*
+ * The experts' layer: y[t] = sum over a token's slots j of
+ *   weights[t, j] * Down_e h,  h = silu(Gate_e x[t]) * (Up_e x[t]),  e = ids[t, j],
+ * x and h coded in FP8 as above, products, h and the sum over the slots (in their order) in
+ * binary32, silu as in pdq_silu_mul_quantize_per_token; y rounded once.
+ *   x        [tokens, hidden] of dt (BF16 or F16), row pitch ldx
+ *   routing  (host struct of device pointers) as pdq_route_experts leaves it.  What the arrays
+ *            hold cannot be refused: an entry that is not a row or an expert of the call is passed
+ *            over, and a slot whose id names an expert but whose row is not sorted is undefined.
+ *   experts  (host struct of device pointers) gate_up: 2 * experts matrices [inner, hidden],
+ *            gate then up of each expert; down: experts matrices [hidden, inner]; their scales
+ *            all of scale_t.  hidden and inner as K above.
+ *   y        [tokens, hidden] of dt out, row pitch ldy (a multiple of 4), 8-byte aligned
+ *   workspace  device scratch of at least pdq_experts_fp8_workspace bytes, 256-byte aligned; as
+ *            pdq_kv_attention's
+ */
+typedef struct pdq_routing {
+    const int32_t* ids;
+    const float* weights;
+    const int32_t* offsets;
+    const int32_t* rows;
+    int64_t tokens, experts, k;
+} pdq_routing;
+
+typedef struct pdq_experts {
+    const uint8_t* gate_up;
+    const void* gate_up_scale;
+    const uint8_t* down;
+    const void* down_scale;
+    pdq_scale_type scale_t;
+    int64_t experts, hidden, inner;
+} pdq_experts;
+
+size_t pdq_experts_fp8_workspace(int64_t tokens, int64_t k, int64_t experts, int64_t hidden, int64_t inner);
+
+pdq_status pdq_experts_fp8(const void* x, pdq_dtype dt, int64_t ldx, const pdq_routing* routing,
+                           const pdq_experts* experts, void* y, int64_t ldy, void* workspace, size_t workspace_bytes,
+                           void* stream);
+
 #ifdef __cplusplus
 }
 #endif

@@ -1,0 +1,141 @@
+// Device-side helpers of the 8-bit floating-point products (gfx950): codes are
+// e4m3 values (OCP: 448 the largest, no infinity), scales of activation groups
+// powers of two in the e8m0 format (byte b stands for 2^(b - 127), 255 for NaN).
+#pragma once
+
+#include "pdq_device.h"
+#include "pdq_kernels.h"
+
+namespace pdq {
+
+typedef int v8i __attribute__((ext_vector_type(8)));
+typedef float v4f __attribute__((ext_vector_type(4)));
+
+// K values of one scale: of a row's group and, with as many rows, of a weight's block.
+constexpr int kGroup = 128;
+
+// The packed operand is the INT8 one (pdq_device.h: 1 KB blocks of 16 rows x
+// 64 K values) with K padded to whole groups, so that a group of 16 rows is two
+// blocks that follow each other: 2 KB, one fragment of a 16x16x128 product.
+constexpr int kGroupBytes = 2 * kWBlock;
+__host__ __device__ __forceinline__ int64_t fp8_groups(int64_t K) { return (K + kGroup - 1) / kGroup; }
+// Groups in a row of scales: a multiple of 4, so that four scales are one aligned load.
+__host__ __device__ __forceinline__ int64_t fp8_scale_pitch(int64_t K) { return (fp8_groups(K) + 3) / 4 * 4; }
+
+// The e8m0 byte of a group whose largest magnitude has the bits `top` (the
+// maximum of the magnitudes' bits, so that infinities and NaN win): the smallest
+// power of two S with |x| <= 448 S.  448 = 1.75 * 2^8, so that S = 2^(E - 8), E
+// the magnitude's exponent, or twice that if its mantissa is above 1.75;
+// 2^-127, the format's smallest, where that is below it; 1 for zeros.
+__device__ __forceinline__ uint32_t fp8_scale_byte(uint32_t top) {
+    const int e = (int)(top >> 23) - 8 + ((top & 0x7fffffu) > 0x600000u ? 1 : 0);
+    const uint32_t b = (uint32_t)max(e, 0);
+    return top == 0 ? 127u : top >= 0x7f800000u ? 255u : b;
+}
+
+// 1 / S as binary32, exact: 2^(127 - b) for b <= 247 (E <= 254 above); 0 for NaN,
+// whose codes are zeros.
+__device__ __forceinline__ float fp8_inverse(uint32_t b) { return b == 255u ? 0.0f : __uint_as_float((254u - b) << 23); }
+
+// x / S of a group without NaN scale; a group with one holds infinities or NaN,
+// whose product with 0 is not 0.
+__device__ __forceinline__ float fp8_scaled(float x, float inv) { return inv == 0.0f ? 0.0f : x * inv; }
+
+// Four codes, rounded to nearest even (v_cvt_pk_fp8_f32; |v| <= 448).
+__device__ __forceinline__ uint32_t fp8_pack4(float a, float b, float c, float d) {
+    int r = __builtin_amdgcn_cvt_pk_fp8_f32(a, b, 0, false);
+    r = __builtin_amdgcn_cvt_pk_fp8_f32(c, d, r, true);
+    return (uint32_t)r;
+}
+
+// Maximum over the 16 lanes of a row of lanes, by lane permutations.
+template <int kCtrl>
+__device__ __forceinline__ uint32_t dpp_u32(uint32_t v) {
+    return (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, kCtrl, 0xf, 0xf, false);
+}
+__device__ __forceinline__ uint32_t row16_max(uint32_t v) {
+    v = max(v, dpp_u32<0xB1>(v));   // quad_perm [1, 0, 3, 2]
+    v = max(v, dpp_u32<0x4E>(v));   // quad_perm [2, 3, 0, 1]
+    v = max(v, dpp_u32<0x141>(v));  // row_half_mirror
+    return max(v, dpp_u32<0x140>(v));  // row_mirror
+}
+
+__device__ __forceinline__ uint32_t magnitude(float x) { return __float_as_uint(x) & 0x7fffffffu; }
+
+// A lane's 32 bytes of a fragment of 16 rows x 128 K values: row lane % 16, the
+// chunk lane / 16 of each of the two blocks.  The order of K values within a
+// group is the same for both operands of a product, so that any will do.
+__device__ __forceinline__ v8i fp8_fragment(const uint8_t* group, int lane) {
+    const uint8_t* p = group + wpack_pos(lane & 15, lane >> 4);
+    const v4i lo = *reinterpret_cast<const v4i*>(p);
+    const v4i hi = *reinterpret_cast<const v4i*>(p + kWBlock);
+    return v8i{lo[0], lo[1], lo[2], lo[3], hi[0], hi[1], hi[2], hi[3]};
+}
+
+// c += 2^(sw - 127) 2^(sx - 127) W X^T for fragments of 16 weight rows and 16
+// activation rows: lane l's scale byte is its own row's (l % 16); all 128
+// products of an output share a scale.  Output r of lane l: weight row
+// 4 (l / 16) + r, activation row l % 16.
+__device__ __forceinline__ v4f fp8_mfma16(v8i w, v8i x, v4f c, int sw, int sx) {
+    return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(w, x, c, 0, 0, 0, sw, 0, sx);
+}
+
+// A product's result, for every lane, here: the compiler may otherwise move the
+// instruction into a branch that only some lanes take, and with it the writes of
+// its scale operands, which the lanes outside then lack.
+__device__ __forceinline__ void fp8_settle(v4f& v) { asm volatile("" : "+v"(v)); }
+
+// A tile of kRows sorted rows, all of one expert: the `index`-th of all, in the
+// order of the experts.
+struct Fp8Tile {
+    int expert;  // -1: there is no such tile
+    int first;   // its first sorted row
+    int rows;    // 1 .. kRows
+    int block;   // its first block of 16 rows
+};
+
+// Every lane of the wavefront takes part and gets the same answer.  What the
+// offsets hold cannot be checked on the host: they are clamped to rows that are
+// there, and a tile's blocks may exceed what well-formed offsets give, which the
+// caller's grid bounds (a tile of 16 rows is block `index`).
+template <int kRows>
+__device__ __forceinline__ Fp8Tile fp8_tile(const Fp8Sorted& s, int index, int lane) {
+    int tiles0 = 0, blocks0 = 0;
+    for (int e0 = 0; e0 < s.experts; e0 += 64) {
+        const int e = min(e0 + lane, s.experts);
+        const int lo = min(max(s.offsets[e], 0), s.total);
+        const int hi = min(max(s.offsets[min(e + 1, s.experts)], lo), s.total);
+        const int count = hi - lo, blocks = (count + 15) / 16, tiles = (count + kRows - 1) / kRows;
+        int bsum = blocks, tsum = tiles;  // inclusive sums over the lanes
+#pragma unroll
+        for (int d = 1; d < 64; d <<= 1) {
+            const int b = __shfl_up(bsum, d), t = kRows == 16 ? 0 : __shfl_up(tsum, d);
+            if (lane >= d) {
+                bsum += b;
+                tsum += t;
+            }
+        }
+        if (kRows == 16) tsum = bsum;
+        const uint64_t past = __ballot(tiles0 + tsum > index);
+        if (past) {
+            const int l = __builtin_ctzll(past);
+            const int at = index - tiles0 - (__builtin_amdgcn_readlane(tsum, l) - __builtin_amdgcn_readlane(tiles, l));
+            const int n = __builtin_amdgcn_readlane(count, l);
+            return Fp8Tile{e0 + l, __builtin_amdgcn_readlane(lo, l) + at * kRows, min(n - at * kRows, kRows),
+                           blocks0 + __builtin_amdgcn_readlane(bsum, l) - __builtin_amdgcn_readlane(blocks, l) +
+                               at * (kRows / 16)};
+        }
+        tiles0 += __builtin_amdgcn_readlane(tsum, 63);
+        blocks0 += __builtin_amdgcn_readlane(bsum, 63);
+    }
+    return Fp8Tile{-1, 0, 0, 0};
+}
+
+// The token and slot of row r of a tile, -1 where there is none (or the entry is not a row of the call).
+__device__ __forceinline__ int fp8_sorted_row(const Fp8Sorted& s, const Fp8Tile& t, int r) {
+    if (t.expert < 0 || r >= t.rows) return -1;
+    const int flat = s.rows[t.first + r];
+    return (uint32_t)flat < (uint32_t)s.total ? flat : -1;
+}
+
+}  // namespace pdq

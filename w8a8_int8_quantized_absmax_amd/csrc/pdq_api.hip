@@ -8,6 +8,7 @@
 #include <mutex>
 
 #include "pdq.h"
+#include "fp8_device.h"
 #include "pdq_device.h"
 #include "pdq_kernels.h"
 
@@ -878,6 +879,267 @@ pdq_status pdq_kv_attention(const void* q, pdq_dtype dt, int64_t tokens, int64_t
     if (attention_threads(a) > kMaxThreads) return PDQ_ERR_SHAPE;
     if (tokens == 0 || a.b.batch == 0) return PDQ_OK;
     launch_attention(a, dt, static_cast<hipStream_t>(stream));
+    return launched();
+}
+
+}  // extern "C"
+
+namespace {
+
+constexpr int64_t kMaxExperts = 512, kMaxChoices = 32, kMaxSorted = int64_t(1) << 30;
+
+bool scale_ok(int t) { return t == PDQ_E8M0 || t == PDQ_SCALE_F32; }
+
+// count matrices of N x K: the sizes' limits, of one of them and of all.
+pdq_status check_stack(int64_t count, int64_t N, int64_t K) {
+    PDQ_TRY(check_mk(N, K, K));
+    if (count < 0 || count > kMaxRows) return PDQ_ERR_SHAPE;
+    const int64_t padded = (N + 127) / 128 * 128 * (fp8_groups(K) * 128);
+    if (count > 0 && padded > kMaxValues / count) return PDQ_ERR_SHAPE;
+    return PDQ_OK;
+}
+
+pdq_status check_fp8_gemm(int64_t M, int64_t K, const uint8_t* wq, const void* w_scale, pdq_scale_type scale_t,
+                          const float* bias, int64_t N, const uint8_t* xq, const uint8_t* x_scale, const void* y,
+                          pdq_dtype y_dt, int64_t ldy) {
+    if (y_dt != PDQ_BF16 && y_dt != PDQ_F16) return PDQ_ERR_DTYPE;
+    if (!scale_ok(scale_t)) return PDQ_ERR_DTYPE;
+    PDQ_TRY(check_mk(M, K, K));
+    PDQ_TRY(check_stack(1, N, K));
+    if (M * N > kMaxOutputs || ldy < N) return PDQ_ERR_SHAPE;
+    if (N > 0 && (!wq || !w_scale)) return PDQ_ERR_NULL;
+    if (M > 0 && (!xq || !x_scale)) return PDQ_ERR_NULL;
+    if (M > 0 && N > 0 && !y) return PDQ_ERR_NULL;
+    if (!aligned(wq, 16) || !aligned(xq, 16) || !aligned(w_scale, 16) || !aligned(x_scale, 4) || !aligned(bias, 4) ||
+        !aligned(y, 2))
+        return PDQ_ERR_ALIGN;
+    return PDQ_OK;
+}
+
+Fp8GemmArgs fp8_gemm_args(int64_t M, int64_t K, const uint8_t* wq, const void* w_scale, pdq_scale_type scale_t,
+                          const float* bias, int64_t N, const uint8_t* xq, const uint8_t* x_scale, void* y, int64_t ldy) {
+    Fp8GemmArgs a{};
+    a.x = xq;
+    a.xs = x_scale;
+    a.w = wq;
+    a.ws = w_scale;
+    a.ws_f32 = scale_t == PDQ_SCALE_F32;
+    a.M = (int)M;
+    a.N = (int)N;
+    a.groups = (int)fp8_groups(K);
+    a.pitch = (int)fp8_scale_pitch(K);
+    a.bias = bias;
+    a.y = y;
+    a.ldy = ldy;
+    return a;
+}
+
+// The parts of the experts' layer's workspace, in bytes.
+struct ExpertsSpace {
+    size_t x, xs, h, hs, partial;
+    size_t all() const { return x + xs + h + hs + partial; }
+};
+ExpertsSpace experts_space(int64_t tokens, int64_t k, int64_t experts, int64_t hidden, int64_t inner) {
+    const int64_t rows = 16 * fp8_blocks(tokens * k, experts);
+    return ExpertsSpace{align256((size_t)(rows * fp8_groups(hidden) * kGroup)), align256((size_t)(rows * fp8_scale_pitch(hidden))),
+                        align256((size_t)(rows * fp8_groups(inner) * kGroup)), align256((size_t)(rows * fp8_scale_pitch(inner))),
+                        align256((size_t)(tokens * k * hidden * 4))};
+}
+bool experts_sizes_ok(int64_t tokens, int64_t k, int64_t experts, int64_t hidden, int64_t inner) {
+    if (tokens < 0 || tokens > kMaxRows || experts < 1 || experts > kMaxExperts || k < 1 || k > std::min(experts, kMaxChoices))
+        return false;
+    if (tokens * k > kMaxSorted) return false;
+    if (hidden < 16 || hidden > kMaxK || hidden % 16 != 0 || inner < 16 || inner > kMaxK || inner % 16 != 0) return false;
+    return tokens * k <= kMaxValues / std::max(hidden, inner);
+}
+
+}  // namespace
+
+extern "C" {
+
+size_t pdq_fp8_bytes(int64_t rows, int64_t K) {
+    if (rows < 0 || K < 0) return 0;
+    return (size_t)((rows + kWGroup - 1) / kWGroup) * (size_t)fp8_groups(K) * kGroupBytes;
+}
+
+int64_t pdq_fp8_scale_pitch(int64_t K) { return K < 0 ? 0 : fp8_scale_pitch(K); }
+
+pdq_status pdq_quantize_weight_fp8(const void* w, pdq_dtype w_dt, int64_t count, int64_t N, int64_t K, int64_t ldw,
+                                   int64_t stride, uint8_t* wq, uint8_t* w_scale, void* stream) {
+    if (!dtype_ok(w_dt)) return PDQ_ERR_DTYPE;
+    PDQ_TRY(check_stack(count, N, K));
+    if (ldw < K || ldw > kMaxValues) return PDQ_ERR_SHAPE;
+    if (count > 1 && N > 0 && (stride < (N - 1) * ldw + K || stride > kMaxValues)) return PDQ_ERR_SHAPE;
+    if (count > 0 && N > 0 && (!w || !wq || !w_scale)) return PDQ_ERR_NULL;
+    const int eb = elem_bytes(w_dt);
+    if (!aligned(w, 16) || (ldw * eb) % 16 != 0 || (count > 1 && (stride * eb) % 16 != 0) || !aligned(wq, 16))
+        return PDQ_ERR_ALIGN;
+    if (count == 0 || N == 0) return PDQ_OK;
+    launch_fp8_weight(Fp8WeightArgs{w, count, N, K, ldw, stride, wq, w_scale}, w_dt, static_cast<hipStream_t>(stream));
+    return launched();
+}
+
+pdq_status pdq_pack_weight_fp8(const uint8_t* codes, const void* scale, pdq_scale_type scale_t, int64_t count,
+                               int64_t N, int64_t K, uint8_t* wq, void* w_scale, void* stream) {
+    if (!scale_ok(scale_t)) return PDQ_ERR_DTYPE;
+    PDQ_TRY(check_stack(count, N, K));
+    if (count > 0 && N > 0 && (!codes || !scale || !wq || !w_scale)) return PDQ_ERR_NULL;
+    const uintptr_t es = scale_t == PDQ_SCALE_F32 ? 4 : 1;
+    if (!aligned(codes, 16) || !aligned(wq, 16) || !aligned(scale, es) || !aligned(w_scale, es)) return PDQ_ERR_ALIGN;
+    if (count == 0 || N == 0) return PDQ_OK;
+    launch_fp8_pack(Fp8PackArgs{codes, scale, count, N, K, scale_t == PDQ_SCALE_F32, wq, w_scale},
+                    static_cast<hipStream_t>(stream));
+    return launched();
+}
+
+pdq_status pdq_quantize_fp8(const void* x, pdq_dtype x_dt, int64_t M, int64_t K, int64_t ldx, uint8_t* xq,
+                            uint8_t* x_scale, void* stream) {
+    if (!dtype_ok(x_dt)) return PDQ_ERR_DTYPE;
+    PDQ_TRY(check_operand(x, elem_bytes(x_dt), M, K, ldx));
+    if (M > 0 && (!xq || !x_scale)) return PDQ_ERR_NULL;
+    if (!aligned(xq, 16) || !aligned(x_scale, 4)) return PDQ_ERR_ALIGN;
+    if (M == 0) return PDQ_OK;
+    Fp8QuantArgs a{};
+    a.x = x;
+    a.ldx = ldx;
+    a.M = M;
+    a.K = (int)K;
+    a.groups = (int)fp8_groups(K);
+    a.pitch = (int)fp8_scale_pitch(K);
+    a.q = xq;
+    a.scale = x_scale;
+    launch_fp8_quant(a, x_dt, (M + 15) / 16, static_cast<hipStream_t>(stream));
+    return launched();
+}
+
+pdq_status pdq_gemm_fp8(const uint8_t* xq, const uint8_t* x_scale, int64_t M, int64_t K, const uint8_t* wq,
+                        const void* w_scale, pdq_scale_type scale_t, const float* bias, int64_t N, void* y,
+                        pdq_dtype y_dt, int64_t ldy, void* stream) {
+    PDQ_TRY(check_fp8_gemm(M, K, wq, w_scale, scale_t, bias, N, xq, x_scale, y, y_dt, ldy));
+    if (M == 0 || N == 0) return PDQ_OK;
+    launch_fp8_rows(fp8_gemm_args(M, K, wq, w_scale, scale_t, bias, N, xq, x_scale, y, ldy), y_dt,
+                    static_cast<hipStream_t>(stream));
+    return launched();
+}
+
+pdq_status pdq_linear_fp8(const void* x, pdq_dtype x_dt, int64_t M, int64_t K, int64_t ldx, const uint8_t* wq,
+                          const void* w_scale, pdq_scale_type scale_t, const float* bias, int64_t N, uint8_t* xq,
+                          uint8_t* x_scale, void* y, pdq_dtype y_dt, int64_t ldy, void* stream) {
+    if (!dtype_ok(x_dt)) return PDQ_ERR_DTYPE;
+    PDQ_TRY(check_operand(x, elem_bytes(x_dt), M, K, ldx));
+    PDQ_TRY(check_fp8_gemm(M, K, wq, w_scale, scale_t, bias, N, xq, x_scale, y, y_dt, ldy));
+    PDQ_TRY(pdq_quantize_fp8(x, x_dt, M, K, ldx, xq, x_scale, stream));
+    return pdq_gemm_fp8(xq, x_scale, M, K, wq, w_scale, scale_t, bias, N, y, y_dt, ldy, stream);
+}
+
+size_t pdq_route_workspace(int64_t tokens, int64_t experts) {
+    if (tokens < 1 || tokens > kMaxRows || experts < 1 || experts > kMaxExperts) return 0;
+    return align256((size_t)route_blocks(tokens) * (size_t)experts * 4);
+}
+
+pdq_status pdq_route_experts(const void* logits, pdq_dtype dt, int64_t tokens, int64_t experts, int64_t ldl,
+                             const float* bias, const pdq_route_rule* rule, int32_t* ids, float* weights,
+                             int32_t* offsets, int32_t* rows, void* workspace, size_t workspace_bytes, void* stream) {
+    if (!dtype_ok(dt)) return PDQ_ERR_DTYPE;
+    if (!rule) return PDQ_ERR_NULL;
+    if (tokens < 0 || tokens > kMaxRows || experts < 1 || experts > kMaxExperts || ldl < experts || ldl > kMaxValues)
+        return PDQ_ERR_SHAPE;
+    if (rule->k < 1 || rule->k > std::min(experts, kMaxChoices) || tokens * rule->k > kMaxSorted) return PDQ_ERR_SHAPE;
+    if (rule->groups < 1 || rule->groups > 64 || experts % rule->groups != 0 || rule->top_groups < 1 ||
+        rule->top_groups > rule->groups)
+        return PDQ_ERR_SHAPE;
+    if ((rule->score != PDQ_SOFTMAX && rule->score != PDQ_SIGMOID) || rule->group_score < 1 || rule->group_score > 2 ||
+        !isfinite(rule->scale))
+        return PDQ_ERR_UNSUPPORTED;
+    if (!offsets || (tokens > 0 && (!logits || !ids || !weights || !rows))) return PDQ_ERR_NULL;
+    if (!aligned(logits, elem_bytes(dt)) || !aligned(bias, 4) || !aligned(ids, 4) || !aligned(weights, 4) ||
+        !aligned(offsets, 4) || !aligned(rows, 4))
+        return PDQ_ERR_ALIGN;
+    if (tokens > 0 && (!workspace || workspace_bytes < pdq_route_workspace(tokens, experts))) return PDQ_ERR_WORKSPACE;
+    if (!aligned(workspace, 256)) return PDQ_ERR_ALIGN;
+    RouteArgs a{};
+    a.logits = logits;
+    a.ldl = ldl;
+    a.bias = bias;
+    a.tokens = (int)tokens;
+    a.experts = (int)experts;
+    a.k = rule->k;
+    a.sigmoid = rule->score == PDQ_SIGMOID;
+    a.renormalize = rule->renormalize != 0;
+    a.groups = rule->groups;
+    a.top_groups = rule->top_groups;
+    a.group_score = rule->group_score;
+    a.scale = rule->scale;
+    a.ids = ids;
+    a.weights = weights;
+    a.offsets = offsets;
+    a.rows = rows;
+    a.hist = static_cast<int32_t*>(workspace);
+    launch_route(a, dt, static_cast<hipStream_t>(stream));
+    return launched();
+}
+
+size_t pdq_experts_fp8_workspace(int64_t tokens, int64_t k, int64_t experts, int64_t hidden, int64_t inner) {
+    if (tokens < 1 || !experts_sizes_ok(tokens, k, experts, hidden, inner)) return 0;
+    return experts_space(tokens, k, experts, hidden, inner).all();
+}
+
+pdq_status pdq_experts_fp8(const void* x, pdq_dtype dt, int64_t ldx, const pdq_routing* routing,
+                           const pdq_experts* experts, void* y, int64_t ldy, void* workspace, size_t workspace_bytes,
+                           void* stream) {
+    if (dt != PDQ_BF16 && dt != PDQ_F16) return PDQ_ERR_DTYPE;
+    if (!routing || !experts) return PDQ_ERR_NULL;
+    if (!scale_ok(experts->scale_t)) return PDQ_ERR_DTYPE;
+    const int64_t tokens = routing->tokens, k = routing->k, E = experts->experts, H = experts->hidden, I = experts->inner;
+    if (routing->experts != E || !experts_sizes_ok(tokens, k, E, H, I)) return PDQ_ERR_SHAPE;
+    PDQ_TRY(check_stack(2 * E, I, H));
+    PDQ_TRY(check_stack(E, H, I));
+    PDQ_TRY(check_operand(x, 2, tokens, H, ldx));
+    if (ldy < H || ldy > kMaxValues) return PDQ_ERR_SHAPE;
+    const int64_t blocks = fp8_blocks(tokens * k, E);
+    if (blocks * std::max(fp8_groups(I), (H + 63) / 64) * 256 > kMaxThreads) return PDQ_ERR_SHAPE;
+    if (!experts->gate_up || !experts->gate_up_scale || !experts->down || !experts->down_scale) return PDQ_ERR_NULL;
+    if (!routing->offsets || (tokens > 0 && (!routing->ids || !routing->weights || !routing->rows || !y))) return PDQ_ERR_NULL;
+    if (!aligned(experts->gate_up, 16) || !aligned(experts->down, 16) || !aligned(experts->gate_up_scale, 16) ||
+        !aligned(experts->down_scale, 16) || !aligned(routing->ids, 4) || !aligned(routing->weights, 4) ||
+        !aligned(routing->offsets, 4) || !aligned(routing->rows, 4) || !aligned(y, 8) || ldy % 4 != 0)
+        return PDQ_ERR_ALIGN;
+    const ExpertsSpace space = experts_space(tokens, k, E, H, I);
+    if (tokens > 0 && (!workspace || workspace_bytes < space.all())) return PDQ_ERR_WORKSPACE;
+    if (!aligned(workspace, 256)) return PDQ_ERR_ALIGN;
+    if (tokens == 0) return PDQ_OK;
+    uint8_t* ws = static_cast<uint8_t*>(workspace);
+    Fp8ExpertsArgs a{};
+    a.sorted = Fp8Sorted{routing->offsets, routing->rows, (int)E, (int)k, (int)(tokens * k)};
+    Fp8QuantArgs q{};
+    q.x = x;
+    q.ldx = ldx;
+    q.M = tokens;
+    q.K = (int)H;
+    q.groups = (int)fp8_groups(H);
+    q.pitch = (int)fp8_scale_pitch(H);
+    q.q = ws;
+    q.scale = ws + space.x;
+    q.sorted = a.sorted;
+    a.x = q.q;
+    a.xs = q.scale;
+    a.h = ws + space.x + space.xs;
+    a.hs = a.h + space.h;
+    a.partial = reinterpret_cast<float*>(a.hs + space.hs);
+    a.gate_up = experts->gate_up;
+    a.gate_up_s = experts->gate_up_scale;
+    a.down = experts->down;
+    a.down_s = experts->down_scale;
+    a.ws_f32 = experts->scale_t == PDQ_SCALE_F32;
+    a.hidden = (int)H;
+    a.inner = (int)I;
+    a.ids = routing->ids;
+    a.weights = routing->weights;
+    a.y = y;
+    a.ldy = ldy;
+    a.tokens = tokens;
+    launch_fp8_quant(q, dt, blocks, static_cast<hipStream_t>(stream));
+    launch_fp8_experts(a, dt, static_cast<hipStream_t>(stream));
     return launched();
 }
 

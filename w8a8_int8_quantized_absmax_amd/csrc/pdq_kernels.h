@@ -196,4 +196,102 @@ size_t attention_workspace(int64_t tokens, int64_t batch, int hq, int hkv, int d
 int64_t attention_threads(const AttentionArgs& a);  // of its largest launch
 void launch_attention(const AttentionArgs& a, int dt, hipStream_t st);
 
+// fp8_quant.hip, fp8_rows.hip, route.hip, experts.hip --------------------
+// Rows sorted by expert (route.hip): expert e's are rows[offsets[e]] ..
+// rows[offsets[e + 1] - 1], each a token and slot (token * k + slot).  The
+// products take them in blocks of 16 rows, each expert's from a block of its own.
+struct Fp8Sorted {
+    const int32_t* offsets;  // [experts + 1]; null: the rows as they are
+    const int32_t* rows;     // [total]
+    int experts, k, total;   // total = tokens * k
+};
+// Activations -> codes and scales: M rows as they are, or (sorted) the token of
+// each sorted row.
+struct Fp8QuantArgs {
+    const void* x;
+    int64_t ldx, M;
+    int K, groups, pitch;  // pitch: bytes of a row of scales
+    uint8_t* q;
+    uint8_t* scale;
+    Fp8Sorted sorted;
+};
+void launch_fp8_quant(const Fp8QuantArgs& a, int dt, int64_t blocks, hipStream_t st);
+
+// count matrices of N x K weights, `stride` elements apart -> codes and block scales (e8m0).
+struct Fp8WeightArgs {
+    const void* w;
+    int64_t count, N, K, ldw, stride;
+    uint8_t* q;
+    uint8_t* scale;
+};
+void launch_fp8_weight(const Fp8WeightArgs& a, int dt, hipStream_t st);
+
+// The same of codes [count, N, K] and scales [count, N / 128, K / 128] that are there already.
+struct Fp8PackArgs {
+    const uint8_t* codes;
+    const void* scale;
+    int64_t count, N, K;
+    bool f32;  // scales binary32, else e8m0
+    uint8_t* q;
+    void* scale_out;
+};
+void launch_fp8_pack(const Fp8PackArgs& a, hipStream_t st);
+
+// y[m, n] = sum_g S_x[m, g] S_w[n / 128, g] sum_{k in g} xq[m, k] wq[n, k] (+ bias[n]).
+struct Fp8GemmArgs {
+    const uint8_t* x;  // packed codes
+    const uint8_t* xs;
+    const uint8_t* w;
+    const void* ws;
+    bool ws_f32;
+    int M, N, groups, pitch;  // pitch: groups in a row of either operand's scales
+    const float* bias;
+    void* y;
+    int64_t ldy;
+};
+void launch_fp8_rows(const Fp8GemmArgs& a, int out_dt, hipStream_t st);
+
+// The experts' layer: h = silu(gate) * up of each sorted row, coded; then down,
+// weighted, a row of partial for each token and slot; then their sum.
+struct Fp8ExpertsArgs {
+    Fp8Sorted sorted;
+    const uint8_t* x;  // packed codes of the sorted rows, in blocks
+    const uint8_t* xs;
+    const uint8_t* gate_up;  // gate, then up, of each expert
+    const void* gate_up_s;
+    const uint8_t* down;
+    const void* down_s;
+    bool ws_f32;
+    int hidden, inner;
+    uint8_t* h;  // packed codes of h
+    uint8_t* hs;
+    const int32_t* ids;
+    const float* weights;
+    float* partial;  // [total, hidden]
+    void* y;
+    int64_t ldy, tokens;
+};
+// The most blocks of 16 rows that `total` rows of `experts` experts take.
+inline int64_t fp8_blocks(int64_t total, int64_t experts) {
+    return (total + 15 * (total < experts ? total : experts)) / 16;
+}
+void launch_fp8_experts(const Fp8ExpertsArgs& a, int out_dt, hipStream_t st);
+
+struct RouteArgs {
+    const void* logits;
+    int64_t ldl;
+    const float* bias;
+    int tokens, experts, k;
+    bool sigmoid, renormalize;
+    int groups, top_groups, group_score;
+    float scale;
+    int32_t* ids;
+    float* weights;
+    int32_t* offsets;
+    int32_t* rows;
+    int32_t* hist;  // [route_blocks(tokens), experts]
+};
+int route_blocks(int64_t tokens);
+void launch_route(const RouteArgs& a, int dt, hipStream_t st);
+
 }  // namespace pdq

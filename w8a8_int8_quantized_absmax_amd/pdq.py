@@ -76,6 +76,20 @@ SIGNATURES = {
     "pdq_kv_attention_workspace": (_sz, [_i64, _i64, _i64, _i64, _i64]),
     "pdq_kv_attention": (ctypes.c_int, [_vp, ctypes.c_int, _i64, _i64, _i64, _vp, _vp, _f32, _f32, _i64, _vp, _vp,
                                         _vp, _i64, _vp, _vp, _sz, _vp]),
+    "pdq_fp8_bytes": (_sz, [_i64, _i64]),
+    "pdq_fp8_scale_pitch": (_i64, [_i64]),
+    "pdq_quantize_weight_fp8": (ctypes.c_int, [_vp, ctypes.c_int, _i64, _i64, _i64, _i64, _i64, _vp, _vp, _vp]),
+    "pdq_pack_weight_fp8": (ctypes.c_int, [_vp, _vp, ctypes.c_int, _i64, _i64, _i64, _vp, _vp, _vp]),
+    "pdq_quantize_fp8": (ctypes.c_int, [_vp, ctypes.c_int, _i64, _i64, _i64, _vp, _vp, _vp]),
+    "pdq_gemm_fp8": (ctypes.c_int, [_vp, _vp, _i64, _i64, _vp, _vp, ctypes.c_int, _vp, _i64, _vp, ctypes.c_int, _i64,
+                                    _vp]),
+    "pdq_linear_fp8": (ctypes.c_int, [_vp, ctypes.c_int, _i64, _i64, _i64, _vp, _vp, ctypes.c_int, _vp, _i64, _vp, _vp,
+                                      _vp, ctypes.c_int, _i64, _vp]),
+    "pdq_route_workspace": (_sz, [_i64, _i64]),
+    "pdq_route_experts": (ctypes.c_int, [_vp, ctypes.c_int, _i64, _i64, _i64, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _sz,
+                                         _vp]),
+    "pdq_experts_fp8_workspace": (_sz, [_i64, _i64, _i64, _i64, _i64]),
+    "pdq_experts_fp8": (ctypes.c_int, [_vp, ctypes.c_int, _i64, _vp, _vp, _vp, _i64, _vp, _sz, _vp]),
 }
 
 _lib = None
@@ -792,3 +806,339 @@ def kv_attention(q, cache: KVCache, batch: KVBatch, scale: float | None = None, 
              prefix_len.data_ptr() if prefix_len is not None else None, y.data_ptr(), ldy,
              lse.data_ptr() if lse is not None else None, workspace.data_ptr() if size else None, size)
     return dict(y=y, lse=lse)
+
+
+# ---- 8-bit floating-point products, routing and experts -------------------
+
+E8M0, SCALE_F32 = 0, 1
+_SCORES = {"softmax": 0, "sigmoid": 1}
+
+
+def fp8_bytes(rows: int, k: int) -> int:
+    """Bytes of the packed FP8 codes of a [rows, k] matrix (include/pdq.h)."""
+    return int(lib().pdq_fp8_bytes(rows, k))
+
+
+@functools.lru_cache(maxsize=4096)
+def _fp8_sizes(rows: int, k: int):
+    """Bytes of packed codes, scales in a row of them."""
+    return int(lib().pdq_fp8_bytes(rows, k)), int(lib().pdq_fp8_scale_pitch(k))
+
+
+def _fp8_unpack(data: torch.Tensor, count: int, n: int, k: int) -> torch.Tensor:
+    """Packed codes -> [count, n, k] e4m3 on their device."""
+    size, kp = fp8_bytes(n, k), (k + 127) // 128 * 128
+    out = torch.empty((count, n, kp), dtype=torch.int8, device=data.device)
+    for i in range(count):
+        unpack_int8(data[i * size:(i + 1) * size].view(torch.int8), n, kp, out=out[i])
+    return out[..., :k].contiguous().view(torch.float8_e4m3fn)
+
+
+class WeightFP8:
+    """FP8 weights with a scale for each block of 128 x 128 (include/pdq.h): one [n, k]
+    matrix, or a stack of them with the leading dimensions `lead`.
+
+    data: packed codes, uint8; scale: e8m0 (torch.float8_e8m0fnu) or float32, [*lead,
+    ceil(n / 128), pitch].  quantize_weight_fp8 and pack_weight_fp8 make them."""
+
+    __slots__ = ("data", "scale", "lead", "n", "k", "scale_type", "device", "index")
+
+    def __init__(self, data: torch.Tensor, scale: torch.Tensor, n: int, k: int):
+        if scale.dtype not in (torch.float8_e8m0fnu, torch.float32):
+            raise ValueError(f"scale: unsupported dtype {scale.dtype}")
+        _check_dense(scale, "scale", scale.dtype)
+        _check_dense(data, "data", torch.uint8)
+        size, pitch = _fp8_sizes(n, k)
+        if scale.dim() < 2 or scale.shape[-1] != pitch or scale.shape[-2] != (n + 127) // 128:
+            raise ValueError(f"scale of shape {tuple(scale.shape)} given for {n} x {k} weights")
+        count = scale.numel() // max(1, scale.shape[-1] * scale.shape[-2])
+        if data.numel() < count * size:
+            raise ValueError(f"data holds {data.numel()} bytes, {count} packed {n} x {k} weights need {count * size}")
+        if data.device != scale.device:
+            raise ValueError("the weight's tensors must be on one device")
+        self.data, self.scale, self.n, self.k, self.lead = data, scale, int(n), int(k), tuple(scale.shape[:-2])
+        self.scale_type = SCALE_F32 if scale.dtype == torch.float32 else E8M0
+        self.device, self.index = data.device, data.get_device()
+
+    @property
+    def shape(self):
+        return (*self.lead, self.n, self.k)
+
+    def codes(self) -> torch.Tensor:
+        """The e4m3 codes [*lead, n, k], row-major."""
+        count = 1
+        for d in self.lead:
+            count *= d
+        return _fp8_unpack(self.data, count, self.n, self.k).view(self.shape)
+
+    def scales(self) -> torch.Tensor:
+        """The block scales [*lead, ceil(n / 128), ceil(k / 128)], float32."""
+        return self.scale.float()[..., :(self.k + 127) // 128]
+
+
+class CodesFP8:
+    """FP8 activation codes of a [rows, k] matrix, packed, and their groups' e8m0 scales."""
+
+    __slots__ = ("data", "scale", "rows", "k")
+
+    def __init__(self, data: torch.Tensor, scale: torch.Tensor, rows: int, k: int):
+        size, pitch = _fp8_sizes(rows, k)
+        _check_dense(data, "data", torch.uint8)
+        _check_dense(scale, "scale", torch.float8_e8m0fnu, (rows, pitch))
+        if data.numel() < size or data.device != scale.device:
+            raise ValueError(f"packed {rows} x {k} codes are {size} bytes, on their scales' device")
+        self.data, self.scale, self.rows, self.k = data, scale, int(rows), int(k)
+
+    @property
+    def shape(self):
+        return (self.rows, self.k)
+
+    def codes(self) -> torch.Tensor:
+        """The e4m3 codes [rows, k], row-major."""
+        return _fp8_unpack(self.data, 1, self.rows, self.k)[0]
+
+    def values(self) -> torch.Tensor:
+        """What the codes and scales stand for, float32 [rows, k]."""
+        return self.codes().float() * self.scale.float().repeat_interleave(128, 1)[:, :self.k]
+
+
+def _stack_shape(t, name):
+    if not t.is_cuda:
+        raise ValueError(f"{name} must be a device tensor")
+    if t.dim() < 2:
+        raise ValueError(f"{name} must be [..., n, k]")
+    count = 1
+    for d in t.shape[:-2]:
+        count *= d
+    return count, t.shape[-2], t.shape[-1]
+
+
+def quantize_weight_fp8(w: torch.Tensor) -> WeightFP8:
+    """Weights [..., n, k] of f32, bf16 or f16 -> FP8 with a power of two as scale for each block
+    of 128 x 128."""
+    count, n, k = _stack_shape(w, "w")
+    if w.dtype not in _DT:
+        raise ValueError(f"w: unsupported dtype {w.dtype}")
+    if not w.is_contiguous() and not (w.dim() == 2 and w.stride(1) == 1):
+        raise ValueError("w must be contiguous, or 2-D with unit stride in the last dimension")
+    size, pitch = _fp8_sizes(n, k)
+    data = torch.empty(count * size, dtype=torch.uint8, device=w.device)
+    scale = torch.empty((*w.shape[:-2], (n + 127) // 128, pitch), dtype=torch.float8_e8m0fnu, device=w.device)
+    ld = _ld(w) if w.dim() == 2 else k
+    _kv_call("pdq_quantize_weight_fp8", w.get_device(), w.data_ptr(), _DT[w.dtype], count, n, k, ld, n * k, data.data_ptr(),
+             scale.data_ptr())
+    return WeightFP8(data, scale, n, k)
+
+
+def pack_weight_fp8(codes: torch.Tensor, scale: torch.Tensor) -> WeightFP8:
+    """Codes [..., n, k] (torch.float8_e4m3fn) and block scales [..., ceil(n / 128), ceil(k / 128)]
+    (float32 or torch.float8_e8m0fnu), as a checkpoint holds them -> the packed weight."""
+    count, n, k = _stack_shape(codes, "codes")
+    _check_dense(codes, "codes", torch.float8_e4m3fn)
+    if scale.dtype not in (torch.float8_e8m0fnu, torch.float32):
+        raise ValueError(f"scale: unsupported dtype {scale.dtype}")
+    _check_dense(scale, "scale", scale.dtype, (*codes.shape[:-2], (n + 127) // 128, (k + 127) // 128))
+    if scale.device != codes.device:
+        raise ValueError("codes and scale must be on one device")
+    size, pitch = _fp8_sizes(n, k)
+    data = torch.empty(count * size, dtype=torch.uint8, device=codes.device)
+    out = torch.empty((*codes.shape[:-2], (n + 127) // 128, pitch), dtype=scale.dtype, device=codes.device)
+    _kv_call("pdq_pack_weight_fp8", codes.get_device(), codes.data_ptr(), scale.data_ptr(),
+             SCALE_F32 if scale.dtype == torch.float32 else E8M0, count, n, k, data.data_ptr(), out.data_ptr())
+    return WeightFP8(data, out, n, k)
+
+
+def quantize_fp8(x: torch.Tensor) -> CodesFP8:
+    """Activations [m, k] -> FP8 codes with a power of two as scale for each row and group of 128."""
+    _check_mat(x, "x")
+    m, k = x.shape
+    size, pitch = _fp8_sizes(m, k)
+    data = torch.empty(size, dtype=torch.uint8, device=x.device)
+    scale = torch.empty((m, pitch), dtype=torch.float8_e8m0fnu, device=x.device)
+    _kv_call("pdq_quantize_fp8", x.get_device(), x.data_ptr(), _DT[x.dtype], m, k, _ld(x), data.data_ptr(), scale.data_ptr())
+    return CodesFP8(data, scale, m, k)
+
+
+def _fp8_operands(w, k, index, bias, m, out, dtype, like):
+    if not isinstance(w, WeightFP8) or w.lead:
+        raise ValueError("w must be one FP8 weight (a WeightFP8 without leading dimensions)")
+    if w.k != k or w.index != index:
+        raise ValueError(f"a [{w.n}, {w.k}] weight on device {w.index} does not fit activations of {k} on device {index}")
+    if bias is not None:
+        _check_dense(bias, "bias", torch.float32, (w.n,))
+        if bias.get_device() != index:
+            raise ValueError("bias must be on the weight's device")
+    if out is None:
+        if dtype not in _HALF:
+            raise ValueError(f"unsupported output dtype {dtype}")
+        return like.new_empty((m, w.n), dtype=dtype)
+    _check_mat(out, "out", _HALF)
+    if tuple(out.shape) != (m, w.n) or out.get_device() != index:
+        raise ValueError(f"out must be [{m}, {w.n}] on the weight's device")
+    return out
+
+
+def linear_fp8(x, w: WeightFP8, bias=None, out=None, dtype=None):
+    """y = x W^T (+ bias) on FP8 codes -> dict(y, xq): x [m, k] f32, bf16 or f16, coded within the call.
+
+    y is f16 for f16 x, else bf16, or of `dtype`; xq: x's codes, for other weights (gemm_fp8)."""
+    _check_mat(x, "x")
+    m, k = x.shape
+    index = x.get_device()
+    y = _fp8_operands(w, k, index, bias, m, out,
+                      dtype or (torch.float16 if x.dtype == torch.float16 else torch.bfloat16), x)
+    size, pitch = _fp8_sizes(m, k)
+    data = x.new_empty(size, dtype=torch.uint8)
+    scale = x.new_empty((m, pitch), dtype=torch.float8_e8m0fnu)
+    _kv_call("pdq_linear_fp8", index, x.data_ptr(), _DT[x.dtype], m, k, _ld(x), w.data.data_ptr(), w.scale.data_ptr(),
+             w.scale_type, bias.data_ptr() if bias is not None else None, w.n, data.data_ptr(), scale.data_ptr(),
+             y.data_ptr(), _DT[y.dtype], _ld(y))
+    return dict(y=y, xq=CodesFP8(data, scale, m, k))
+
+
+def gemm_fp8(xq: CodesFP8, w: WeightFP8, bias=None, out=None, dtype=torch.bfloat16):
+    """The product of linear_fp8 on codes that are there already -> dict(y)."""
+    if not isinstance(xq, CodesFP8):
+        raise ValueError("xq must be FP8 activation codes (a CodesFP8 object)")
+    m, k = xq.shape
+    index = xq.data.get_device()
+    y = _fp8_operands(w, k, index, bias, m, out, dtype, xq.data)
+    _kv_call("pdq_gemm_fp8", index, xq.data.data_ptr(), xq.scale.data_ptr(), m, k, w.data.data_ptr(), w.scale.data_ptr(),
+             w.scale_type, bias.data_ptr() if bias is not None else None, w.n, y.data_ptr(), _DT[y.dtype], _ld(y))
+    return dict(y=y)
+
+
+class _RouteRuleC(ctypes.Structure):
+    _fields_ = [("score", _i32), ("k", _i32), ("groups", _i32), ("top_groups", _i32), ("group_score", _i32),
+                ("renormalize", _i32), ("scale", _f32)]
+
+
+class _RoutingC(ctypes.Structure):
+    _fields_ = [("ids", _vp), ("weights", _vp), ("offsets", _vp), ("rows", _vp), ("tokens", _i64), ("experts", _i64),
+                ("k", _i64)]
+
+
+class _ExpertsC(ctypes.Structure):
+    _fields_ = [("gate_up", _vp), ("gate_up_scale", _vp), ("down", _vp), ("down_scale", _vp), ("scale_t", ctypes.c_int),
+                ("experts", _i64), ("hidden", _i64), ("inner", _i64)]
+
+
+class Routing:
+    """The experts of each token (include/pdq.h, pdq_route_experts): ids int32 and weights float32
+    [tokens, k]; the rows token * k + slot sorted by expert: offsets int32 [experts + 1], rows int32
+    [tokens * k]."""
+
+    __slots__ = ("ids", "weights", "offsets", "rows", "tokens", "experts", "k", "index", "_c", "_ref")
+
+    def __init__(self, ids: torch.Tensor, weights: torch.Tensor, offsets: torch.Tensor, rows: torch.Tensor):
+        if ids.dim() != 2 or offsets.dim() != 1 or offsets.shape[0] < 2:
+            raise ValueError("ids must be [tokens, k], offsets [experts + 1]")
+        tokens, k = ids.shape
+        _check_dense(ids, "ids", torch.int32)
+        _check_dense(weights, "weights", torch.float32, (tokens, k))
+        _check_dense(offsets, "offsets", torch.int32)
+        _check_dense(rows, "rows", torch.int32, (tokens * k,))
+        if not ids.device == weights.device == offsets.device == rows.device:
+            raise ValueError("the routing's tensors must be on one device")
+        self._take(ids, weights, offsets, rows, tokens, offsets.shape[0] - 1, k, ids.get_device())
+
+    def _take(self, ids, weights, offsets, rows, tokens, experts, k, index):
+        self.ids, self.weights, self.offsets, self.rows = ids, weights, offsets, rows
+        self.tokens, self.experts, self.k, self.index = tokens, experts, k, index
+        self._c = _RoutingC(ids.data_ptr(), weights.data_ptr(), offsets.data_ptr(), rows.data_ptr(), tokens, experts, k)
+        self._ref = ctypes.byref(self._c)
+
+
+@functools.lru_cache(maxsize=4096)
+def route_workspace_bytes(tokens: int, experts: int) -> int:
+    return int(lib().pdq_route_workspace(tokens, experts))
+
+
+@functools.lru_cache(maxsize=256)
+def _route_rule(score, k, groups, top_groups, group_score, renormalize, scale):
+    c = _RouteRuleC(_SCORES[score], k, groups, top_groups, group_score, 1 if renormalize else 0, scale)
+    return c, ctypes.byref(c)
+
+
+def route_experts(logits, k: int, score: str = "softmax", bias=None, groups: int = 1, top_groups: int = 1,
+                  group_score: int = 1, renormalize: bool = True, scale: float = 1.0, workspace=None) -> Routing:
+    """The k experts of each token from the router's logits [tokens, experts] (f32, bf16 or f16), and
+    the tokens sorted by expert.
+
+    score: "softmax" or "sigmoid"; bias float32 [experts]: added for the choice alone; groups,
+    top_groups, group_score: only the best top_groups of `groups` runs of experts take part, by the sum
+    of their group_score largest; renormalize: a token's weights sum to 1, times scale."""
+    _check_mat(logits, "logits")
+    tokens, experts = logits.shape
+    index = logits.get_device()
+    if score not in _SCORES:
+        raise ValueError(f"score must be one of {sorted(_SCORES)}")
+    if bias is not None:
+        _check_dense(bias, "bias", torch.float32, (experts,))
+        if bias.get_device() != index:
+            raise ValueError("bias must be on logits' device")
+    if not 1 <= k <= experts:
+        raise ValueError(f"k = {k} of {experts} experts")
+    rule = _route_rule(score, int(k), int(groups), int(top_groups), int(group_score), bool(renormalize), float(scale))
+    ids = logits.new_empty((tokens, k), dtype=torch.int32)
+    weights = logits.new_empty((tokens, k), dtype=torch.float32)
+    offsets = logits.new_empty(experts + 1, dtype=torch.int32)
+    rows = logits.new_empty(tokens * k, dtype=torch.int32)
+    size = route_workspace_bytes(tokens, experts)
+    workspace, size = _workspace(workspace, size, logits, index)
+    _kv_call("pdq_route_experts", index, logits.data_ptr(), _DT[logits.dtype], tokens, experts, _ld(logits),
+             bias.data_ptr() if bias is not None else None, rule[1], ids.data_ptr(), weights.data_ptr(),
+             offsets.data_ptr(), rows.data_ptr(), workspace.data_ptr() if size else None, size)
+    r = Routing.__new__(Routing)
+    r._take(ids, weights, offsets, rows, tokens, experts, k, index)
+    return r
+
+
+def _workspace(workspace, size, like, index):
+    """The caller's workspace, or a new one."""
+    if workspace is None:
+        return (like.new_empty(size, dtype=torch.uint8) if size else None), size
+    _check_dense(workspace, "workspace", torch.uint8)
+    if workspace.get_device() != index:
+        raise ValueError("the workspace must be on the call's device")
+    return workspace, workspace.numel()
+
+
+@functools.lru_cache(maxsize=4096)
+def experts_fp8_workspace_bytes(tokens: int, k: int, experts: int, hidden: int, inner: int) -> int:
+    return int(lib().pdq_experts_fp8_workspace(tokens, k, experts, hidden, inner))
+
+
+def experts_fp8(x, routing: Routing, gate_up: WeightFP8, down: WeightFP8, out=None, workspace=None):
+    """The experts' layer -> dict(y of x's shape and dtype): each token's chosen gated MLPs on FP8
+    weights, weighted and summed.
+
+    x: [tokens, hidden] bf16 or f16; gate_up: a WeightFP8 [experts, 2, inner, hidden]; down:
+    [experts, hidden, inner], both with scales of one type."""
+    _check_mat(x, "x", _HALF)
+    tokens, hidden = x.shape
+    index = x.get_device()
+    experts, inner = routing.experts, gate_up.n
+    if gate_up.lead != (experts, 2) or down.lead != (experts,) or gate_up.k != hidden or down.n != hidden or down.k != inner:
+        raise ValueError(f"weights of shapes {gate_up.shape} and {down.shape} given, [{experts}, 2, inner, {hidden}] and "
+                         f"[{experts}, {hidden}, inner] needed")
+    if gate_up.scale_type != down.scale_type:
+        raise ValueError("the weights' scales must be of one type")
+    if routing.tokens != tokens:
+        raise ValueError(f"the routing of {routing.tokens} tokens given for {tokens}")
+    if not index == routing.index == gate_up.index == down.index:
+        raise ValueError("x, the routing and the weights must be on one device")
+    if out is None:
+        y = x.new_empty((tokens, hidden))
+    else:
+        y = out
+        _check_mat(y, "out", (x.dtype,))
+        if y.shape != x.shape or y.get_device() != index:
+            raise ValueError("out must have x's shape and device")
+    size = experts_fp8_workspace_bytes(tokens, routing.k, experts, hidden, inner)
+    workspace, size = _workspace(workspace, size, x, index)
+    c = _ExpertsC(gate_up.data.data_ptr(), gate_up.scale.data_ptr(), down.data.data_ptr(), down.scale.data_ptr(),
+                  gate_up.scale_type, experts, hidden, inner)
+    _kv_call("pdq_experts_fp8", index, x.data_ptr(), _DT[x.dtype], _ld(x), routing._ref, ctypes.byref(c), y.data_ptr(),
+             _ld(y), workspace.data_ptr() if size else None, size)
+    return dict(y=y)
