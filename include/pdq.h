@@ -622,7 +622,9 @@ pdq_status pdq_kv_attention(const void* q, pdq_dtype dt, int64_t tokens, int64_t
  *                neighbouring K values to the largest of their exponents and keeps 13 bits
  *                behind it: each loses less than 2^-13 of the eight's largest magnitude (some
  *                2^-14 of y's size over many outputs).
- * An FP8 matrix is packed as an INT8 one is (pdq_quantize_weight), with K padded to a
+ * An FP8 matrix is packed in blocks of 16 rows x 64 K values, block (g, s) the 1024
+ * bytes at (g * 2 ceil(K / 128) + s) * 1024, in it the 16-byte chunk c (K values 64 s +
+ * 16 c ..) of row r at c * 256 + r * 16 (not the INT8 order), with K padded to a
  * multiple of 128: pdq_fp8_bytes(rows, K) bytes, rows and K values beyond the matrix
  * 0.  Scales of a row (of a weight's 128 rows) are followed by padding up to
  * pdq_fp8_scale_pitch(K) = 4 ceil(K / 512) of them.  K, alignment and the sizes'

@@ -6,7 +6,6 @@ import torch
 import oracle.fp8_oracle as FO
 from fp8_cases import DT, check_linear, randn, values, weight
 from guards import SENTINEL, gapped
-from packing import pack
 from w8a8_int8_quantized_absmax_amd import pdq
 
 pytestmark = pytest.mark.gpu
@@ -17,11 +16,11 @@ def bits(t):
 
 
 def image(codes):
-    """The packed image of code bits [rows, k], K padded to whole groups."""
+    """The packed image of code bits [rows, k]: blocks of 16 rows x 64 K values, by chunk of 16, then row."""
     rows, k = codes.shape
-    full = np.zeros((rows, -(-k // 128) * 128), np.int8)
-    full[:, :k] = codes.view(np.int8)
-    return pack(full).view(np.uint8)
+    full = np.zeros((-(-rows // 16) * 16, -(-k // 128) * 128), np.uint8)
+    full[:rows, :k] = codes
+    return full.reshape(-1, 16, full.shape[1] // 64, 4, 16).transpose(0, 2, 3, 1, 4).reshape(-1)
 
 
 def raw_quantize(x):

@@ -9,12 +9,6 @@ namespace pdq {
 
 namespace {
 
-__device__ __forceinline__ float silu_mul(float g, float u) {
-    const float e = __builtin_amdgcn_exp2f(-fabsf(g) * 1.4426950408889634f);
-    const float r = __builtin_amdgcn_rcpf(1.0f + e);
-    return (g * (g >= 0.0f ? r : e * r)) * u;
-}
-
 template <bool F32S>
 struct BlockScale {
     float f;
@@ -87,7 +81,7 @@ __global__ __launch_bounds__(256) void k_fp8_gate_up(Fp8ExpertsArgs a) {
     for (int j = 0; j < 2; ++j)
 #pragma unroll
         for (int r = 0; r < 4; ++r) {
-            h[j][r] = (int)blockIdx.y * 8 + 2 * wave + j < ngroups ? silu_mul(acc[0][j][r], acc[1][j][r]) : 0.0f;
+            h[j][r] = (int)blockIdx.y * 8 + 2 * wave + j < ngroups ? fp8_silu_mul(acc[0][j][r], acc[1][j][r]) : 0.0f;
             top = max(top, magnitude(h[j][r]));
         }
     top = max(top, (uint32_t)__shfl_xor((int)top, 16));
@@ -103,7 +97,7 @@ __global__ __launch_bounds__(256) void k_fp8_gate_up(Fp8ExpertsArgs a) {
         const int c = 2 * wave + j;  // chunk of 16 channels in the group
 #pragma unroll
         for (int r = 0; r < 4; ++r) h[j][r] = fp8_scaled(h[j][r], inv);
-        *reinterpret_cast<uint32_t*>(hb + (c >> 2) * kWBlock + wpack_pos(row, c & 3) + 4 * (lane >> 4)) =
+        *reinterpret_cast<uint32_t*>(hb + (c >> 2) * kWBlock + fp8_pos(row, c & 3) + 4 * (lane >> 4)) =
             fp8_pack4(h[j][0], h[j][1], h[j][2], h[j][3]);
     }
     if (threadIdx.x < 16) a.hs[((int64_t)blockIdx.x * 16 + row) * fp8_scale_pitch(a.inner) + blockIdx.y] = (uint8_t)b;
@@ -154,6 +148,37 @@ __global__ __launch_bounds__(256) void k_fp8_combine(Fp8ExpertsArgs a) {
 
 template <bool F32S>
 void launch_products(const Fp8ExpertsArgs& a, hipStream_t st) {
+    // Rows of a tile by the average rows of an expert: a tile that is not full costs as much as a
+    // full one.  Below 24 one block of 16 rows at a time.
+    const int64_t each = a.sorted.total / a.sorted.experts;
+    const int rows = each >= 200 ? 256 : each >= 64 ? 128 : each >= 24 ? 64 : 0;
+    if (!F32S && rows > 0) {
+        Fp8TileArgs t{};
+        t.x = a.x;
+        t.xs = a.xs;
+        t.w = a.gate_up;
+        t.ws = static_cast<const uint8_t*>(a.gate_up_s);
+        t.N = a.inner;
+        t.groups = (int)fp8_groups(a.hidden);
+        t.pitch = (int)fp8_scale_pitch(a.hidden);
+        t.sorted = a.sorted;
+        t.h = a.h;
+        t.hs = a.hs;
+        t.h_pitch = (int)fp8_scale_pitch(a.inner);
+        launch_fp8_expert_tiles(t, true, rows, st);
+        t.x = a.h;
+        t.xs = a.hs;
+        t.w = a.down;
+        t.ws = static_cast<const uint8_t*>(a.down_s);
+        t.N = a.hidden;
+        t.groups = (int)fp8_groups(a.inner);
+        t.pitch = (int)fp8_scale_pitch(a.inner);
+        t.y = a.partial;
+        t.ldy = a.hidden;
+        t.weights = a.weights;
+        launch_fp8_expert_tiles(t, false, rows, st);
+        return;
+    }
     const uint32_t blocks = (uint32_t)fp8_blocks(a.sorted.total, a.sorted.experts);
     hipLaunchKernelGGL((k_fp8_gate_up<F32S>), dim3(blocks, (uint32_t)fp8_groups(a.inner)), dim3(256), 0, st, a);
     hipLaunchKernelGGL((k_fp8_down<F32S>), dim3(blocks, (a.hidden + 63) / 64), dim3(256), 0, st, a);

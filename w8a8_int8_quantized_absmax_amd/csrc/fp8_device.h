@@ -14,9 +14,13 @@ typedef float v4f __attribute__((ext_vector_type(4)));
 // K values of one scale: of a row's group and, with as many rows, of a weight's block.
 constexpr int kGroup = 128;
 
-// The packed operand is the INT8 one (pdq_device.h: 1 KB blocks of 16 rows x
-// 64 K values) with K padded to whole groups, so that a group of 16 rows is two
-// blocks that follow each other: 2 KB, one fragment of a 16x16x128 product.
+// The packed operand: blocks of 16 rows x 64 K values as the INT8 one's (pdq_device.h), two blocks
+// that follow each other for a group: 2 KB, one fragment of a 16x16x128 product.  Within a block
+// the 16-byte chunks go by chunk, then row, so that lane l's, row l % 16 and chunk l / 16, is the
+// l-th: 1 KB by 64 lanes in order, from memory as from LDS, free of bank conflicts.  (In the
+// INT8 order, rows of 64 bytes with their chunks turned, these reads count as many conflict
+// clocks as clocks.)
+__host__ __device__ __forceinline__ int fp8_pos(int r, int c) { return c * 256 + r * 16; }
 constexpr int kGroupBytes = 2 * kWBlock;
 __host__ __device__ __forceinline__ int64_t fp8_groups(int64_t K) { return (K + kGroup - 1) / kGroup; }
 // Groups in a row of scales: a multiple of 4, so that four scales are one aligned load.
@@ -66,7 +70,7 @@ __device__ __forceinline__ uint32_t magnitude(float x) { return __float_as_uint(
 // chunk lane / 16 of each of the two blocks.  The order of K values within a
 // group is the same for both operands of a product, so that any will do.
 __device__ __forceinline__ v8i fp8_fragment(const uint8_t* group, int lane) {
-    const uint8_t* p = group + wpack_pos(lane & 15, lane >> 4);
+    const uint8_t* p = group + 16 * lane;
     const v4i lo = *reinterpret_cast<const v4i*>(p);
     const v4i hi = *reinterpret_cast<const v4i*>(p + kWBlock);
     return v8i{lo[0], lo[1], lo[2], lo[3], hi[0], hi[1], hi[2], hi[3]};
@@ -129,6 +133,26 @@ __device__ __forceinline__ Fp8Tile fp8_tile(const Fp8Sorted& s, int index, int l
         blocks0 += __builtin_amdgcn_readlane(bsum, 63);
     }
     return Fp8Tile{-1, 0, 0, 0};
+}
+
+// How many tiles of kRows sorted rows there are.
+template <int kRows>
+__device__ __forceinline__ int fp8_tiles(const Fp8Sorted& s, int lane) {
+    int n = 0;
+    for (int e0 = 0; e0 < s.experts; e0 += 64) {
+        const int e = min(e0 + lane, s.experts);
+        const int lo = min(max(s.offsets[e], 0), s.total);
+        const int hi = min(max(s.offsets[min(e + 1, s.experts)], lo), s.total);
+        n += (hi - lo + kRows - 1) / kRows;
+    }
+    return __builtin_amdgcn_readfirstlane(wave_sum(n));
+}
+
+// silu(g) * u: e = 2^(-|g| log2 e) and 1 / (1 + e) by the hardware's exp2 and reciprocal.
+__device__ __forceinline__ float fp8_silu_mul(float g, float u) {
+    const float e = __builtin_amdgcn_exp2f(-fabsf(g) * 1.4426950408889634f);
+    const float r = __builtin_amdgcn_rcpf(1.0f + e);
+    return (g * (g >= 0.0f ? r : e * r)) * u;
 }
 
 // The token and slot of row r of a tile, -1 where there is none (or the entry is not a row of the call).

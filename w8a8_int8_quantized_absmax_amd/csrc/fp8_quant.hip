@@ -16,13 +16,14 @@ namespace pdq {
 
 namespace {
 
-// A workgroup codes 16 rows x 4 groups (2 blocks of packed codes a group, one
-// dword of scales a row): wavefront w the rows 4 w .. 4 w + 3, 16 lanes a row,
-// 8 values a lane and group, the row's maximum by lane permutations within its
-// 16 lanes.  A wavefront's loads are 4 rows x 256 bytes, its stores of a group
-// 4 rows x 64 bytes in each of the two blocks: whole lines both.
+// A workgroup codes 16 rows x 4 groups (8 KB of packed codes, one dword of scales a
+// row): wavefront w the rows 4 w .. 4 w + 3, 16 lanes a row, 8 values a lane and
+// group, the row's maximum by lane permutations within its 16 lanes.  A wavefront's
+// loads are 4 rows x 256 bytes; the codes take their places in LDS and leave as one
+// contiguous run.
 template <int DT>
 __global__ __launch_bounds__(256) void k_fp8_quant(Fp8QuantArgs a) {
+    __shared__ __attribute__((aligned(16))) uint8_t image[4 * kGroupBytes];
     const int lane = threadIdx.x & 63, r = threadIdx.x >> 4;  // row of the 16-row block
     const int gpieces = (a.groups + 3) / 4;
     const int64_t block = blockIdx.x / gpieces;
@@ -57,13 +58,20 @@ __global__ __launch_bounds__(256) void k_fp8_quant(Fp8QuantArgs a) {
 #pragma unroll
         for (int j = 0; j < 8; ++j) v[j] = fp8_scaled(v[j], inv);
         const int c16 = c8 >> 1;
-        uint8_t* blk = a.q + (block * a.groups + g0 + i) * kGroupBytes + (c16 >> 2) * kWBlock;
-        *reinterpret_cast<uint2*>(blk + wpack_pos(r, c16 & 3) + 8 * (c8 & 1)) =
+        *reinterpret_cast<uint2*>(image + i * kGroupBytes + (c16 >> 2) * kWBlock + fp8_pos(r, c16 & 3) + 8 * (c8 & 1)) =
             make_uint2(fp8_pack4(v[0], v[1], v[2], v[3]), fp8_pack4(v[4], v[5], v[6], v[7]));
         scales |= b << (8 * i);
     }
     if (c8 == 0 && (a.sorted.offsets || row < a.M))
         *reinterpret_cast<uint32_t*>(a.scale + row * a.pitch + g0) = scales;
+    __syncthreads();
+    uint4* out = reinterpret_cast<uint4*>(a.q + (block * a.groups + g0) * kGroupBytes);
+    const int chunks = min(a.groups - g0, 4) * (kGroupBytes / 16);
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+        const int c = threadIdx.x + 256 * i;
+        if (c < chunks) out[c] = reinterpret_cast<const uint4*>(image)[c];
+    }
 }
 
 // One block of 128 x 128 weights a workgroup: its values stay in registers (8
@@ -109,7 +117,7 @@ __global__ __launch_bounds__(256) void k_fp8_weight(Fp8WeightArgs a) {
         for (int j = 0; j < 8; ++j) v[j] = fp8_scaled(v[j], inv);
         const int c16 = c8 >> 1;
         uint8_t* blk = a.q + ((mat * ngroups + g16) * groups + g) * kGroupBytes + (c16 >> 2) * kWBlock;
-        *reinterpret_cast<uint2*>(blk + wpack_pos(r16, c16 & 3) + 8 * (c8 & 1)) =
+        *reinterpret_cast<uint2*>(blk + fp8_pos(r16, c16 & 3) + 8 * (c8 & 1)) =
             make_uint2(fp8_pack4(v[0], v[1], v[2], v[3]), fp8_pack4(v[4], v[5], v[6], v[7]));
     }
     // the row's padding up to the pitch: scales of 1
@@ -124,7 +132,7 @@ __global__ __launch_bounds__(256) void k_fp8_pack(Fp8PackArgs a, int64_t chunks)
     if (t >= chunks) return;
     const int64_t groups = fp8_groups(a.K), ngroups = (a.N + 15) / 16;
     // t: the chunk in the packed image, blocks of 64 chunks
-    const int in = (int)(t & 63), r = in >> 2, c = (in & 3) ^ ((r >> 2) & 3);
+    const int in = (int)(t & 63), r = in & 15, c = in >> 4;
     const int64_t blk = t >> 6, kt = blk % (2 * groups), g16 = blk / (2 * groups) % ngroups, mat = blk / (2 * groups * ngroups);
     const int64_t n = g16 * 16 + r, k = kt * kWTileK + c * 16;
     uint4 v = make_uint4(0, 0, 0, 0);

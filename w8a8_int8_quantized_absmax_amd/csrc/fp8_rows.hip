@@ -33,7 +33,7 @@ __global__ __launch_bounds__(256) void k_fp8_rows(Fp8GemmArgs a) {
     const uint8_t* wp[NG];
     const uint8_t* xp[MB];
     const uint8_t* xsp[MB];
-    const int off = wpack_pos(lane & 15, lane >> 4);
+    const int off = 16 * lane;
 #pragma unroll
     for (int i = 0; i < NG; ++i) wp[i] = a.w + (int64_t)min(n0 / 16 + i, lastw) * G * kGroupBytes + off;
 #pragma unroll

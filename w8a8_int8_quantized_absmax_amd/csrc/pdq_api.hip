@@ -1017,6 +1017,23 @@ pdq_status pdq_gemm_fp8(const uint8_t* xq, const uint8_t* x_scale, int64_t M, in
                         pdq_dtype y_dt, int64_t ldy, void* stream) {
     PDQ_TRY(check_fp8_gemm(M, K, wq, w_scale, scale_t, bias, N, xq, x_scale, y, y_dt, ldy));
     if (M == 0 || N == 0) return PDQ_OK;
+    const int trows = M > 1024 ? 256 : M > 64 ? 128 : 0;
+    if (scale_t == PDQ_E8M0 && trows > 0) {
+        Fp8TileArgs t{};
+        t.x = xq;
+        t.xs = x_scale;
+        t.w = wq;
+        t.ws = static_cast<const uint8_t*>(w_scale);
+        t.M = (int)M;
+        t.N = (int)N;
+        t.groups = (int)fp8_groups(K);
+        t.pitch = (int)fp8_scale_pitch(K);
+        t.bias = bias;
+        t.y = y;
+        t.ldy = ldy;
+        launch_fp8_tiles(t, y_dt, trows, static_cast<hipStream_t>(stream));
+        return launched();
+    }
     launch_fp8_rows(fp8_gemm_args(M, K, wq, w_scale, scale_t, bias, N, xq, x_scale, y, ldy), y_dt,
                     static_cast<hipStream_t>(stream));
     return launched();

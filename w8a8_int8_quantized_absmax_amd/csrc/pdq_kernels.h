@@ -271,6 +271,25 @@ struct Fp8ExpertsArgs {
     void* y;
     int64_t ldy, tokens;
 };
+// The tiled products with e8m0 scales, gemm_fp8.hip: dense, or (sorted) of the experts' layer.
+struct Fp8TileArgs {
+    const uint8_t* x;  // packed codes
+    const uint8_t* xs;
+    const uint8_t* w;
+    const uint8_t* ws;
+    int M, N, groups, pitch;  // N: weight rows of one matrix
+    const float* bias;
+    void* y;  // dense: 16 bits; down: binary32 [total, ldy]
+    int64_t ldy;
+    Fp8Sorted sorted;
+    const float* weights;  // down
+    uint8_t* h;            // gate and up: codes and scales out
+    uint8_t* hs;
+    int h_pitch;
+};
+void launch_fp8_tiles(const Fp8TileArgs& a, int out_dt, int rows, hipStream_t st);
+void launch_fp8_expert_tiles(const Fp8TileArgs& a, bool gate_up, int rows, hipStream_t st);
+
 // The most blocks of 16 rows that `total` rows of `experts` experts take.
 inline int64_t fp8_blocks(int64_t total, int64_t experts) {
     return (total + 15 * (total < experts ? total : experts)) / 16;

@@ -826,12 +826,10 @@ def _fp8_sizes(rows: int, k: int):
 
 
 def _fp8_unpack(data: torch.Tensor, count: int, n: int, k: int) -> torch.Tensor:
-    """Packed codes -> [count, n, k] e4m3 on their device."""
-    size, kp = fp8_bytes(n, k), (k + 127) // 128 * 128
-    out = torch.empty((count, n, kp), dtype=torch.int8, device=data.device)
-    for i in range(count):
-        unpack_int8(data[i * size:(i + 1) * size].view(torch.int8), n, kp, out=out[i])
-    return out[..., :k].contiguous().view(torch.float8_e4m3fn)
+    """Packed codes (include/pdq.h) -> [count, n, k] e4m3 on their device."""
+    blocks = data[:count * fp8_bytes(n, k)].view(count, (n + 15) // 16, (k + 127) // 128 * 2, 4, 16, 16)
+    rows = blocks.permute(0, 1, 4, 2, 3, 5).reshape(count, (n + 15) // 16 * 16, -1)
+    return rows[:, :n, :k].contiguous().view(torch.float8_e4m3fn)
 
 
 class WeightFP8:
