@@ -30,6 +30,10 @@ HIPCC_FLAGS = [
     "-Wno-unused-function",
 ]
 
+# flags of one source: results of matrix instructions in vector registers, where its kernels' other
+# instructions read them (accumulation registers would cost a copy a value)
+FILE_FLAGS = {"gemm_fp8_f32.hip": ["-mllvm", "-amdgpu-mfma-vgpr-form=1"]}
+
 
 def _quiet(text: str) -> str:
     return "\n".join(line for line in text.splitlines()
@@ -54,7 +58,7 @@ def build(verbose: bool = False) -> str:
 
     def compile_one(src):
         obj = os.path.join(objdir, os.path.basename(src)[:-4] + ".o")
-        cmd = [cc, *HIPCC_FLAGS, "-c", "-I", INCLUDE, "-I", CSRC, src, "-o", obj]
+        cmd = [cc, *HIPCC_FLAGS, *FILE_FLAGS.get(os.path.basename(src), []), "-c", "-I", INCLUDE, "-I", CSRC, src, "-o", obj]
         if verbose:
             print(" ".join(cmd), flush=True)
         res = subprocess.run(cmd, capture_output=True, text=True)

@@ -151,13 +151,14 @@ void launch_products(const Fp8ExpertsArgs& a, hipStream_t st) {
     // Rows of a tile by the average rows of an expert: a tile that is not full costs as much as a
     // full one.  Below 24 one block of 16 rows at a time.
     const int64_t each = a.sorted.total / a.sorted.experts;
-    const int rows = each >= 200 ? 256 : each >= 64 ? 128 : each >= 24 ? 64 : 0;
-    if (!F32S && rows > 0) {
+    const int rows = each >= 200 ? (F32S ? 192 : 256) : each >= 64 ? 128 : each >= 24 ? 64 : 0;
+    if (rows > 0) {
         Fp8TileArgs t{};
         t.x = a.x;
         t.xs = a.xs;
         t.w = a.gate_up;
-        t.ws = static_cast<const uint8_t*>(a.gate_up_s);
+        t.ws = a.gate_up_s;
+        t.ws_f32 = F32S;
         t.N = a.inner;
         t.groups = (int)fp8_groups(a.hidden);
         t.pitch = (int)fp8_scale_pitch(a.hidden);
@@ -169,7 +170,7 @@ void launch_products(const Fp8ExpertsArgs& a, hipStream_t st) {
         t.x = a.h;
         t.xs = a.hs;
         t.w = a.down;
-        t.ws = static_cast<const uint8_t*>(a.down_s);
+        t.ws = a.down_s;
         t.N = a.hidden;
         t.groups = (int)fp8_groups(a.inner);
         t.pitch = (int)fp8_scale_pitch(a.inner);

@@ -7,16 +7,6 @@
 
 namespace pdq {
 
-// A value at an address that is the same in every lane, of memory that the kernel
-// does not write: through the scalar cache, so that waiting for it does not wait
-// for the vector loads in flight.
-template <typename T>
-__device__ __forceinline__ T uniform_load(const T* p) {
-    const uint64_t u = reinterpret_cast<uint64_t>(p);
-    const uint32_t lo = __builtin_amdgcn_readfirstlane((int)u), hi = __builtin_amdgcn_readfirstlane((int)(u >> 32));
-    return *reinterpret_cast<const __attribute__((address_space(4))) T*>((uint64_t)hi << 32 | lo);
-}
-
 template <bool Uniform, typename T>
 __device__ __forceinline__ T load_as(const T* p) {
     if constexpr (Uniform) return uniform_load(p);

@@ -1017,13 +1017,14 @@ pdq_status pdq_gemm_fp8(const uint8_t* xq, const uint8_t* x_scale, int64_t M, in
                         pdq_dtype y_dt, int64_t ldy, void* stream) {
     PDQ_TRY(check_fp8_gemm(M, K, wq, w_scale, scale_t, bias, N, xq, x_scale, y, y_dt, ldy));
     if (M == 0 || N == 0) return PDQ_OK;
-    const int trows = M > 1024 ? 256 : M > 64 ? 128 : 0;
-    if (scale_t == PDQ_E8M0 && trows > 0) {
+    const int trows = M > 1024 ? (scale_t == PDQ_E8M0 ? 256 : 192) : M > 64 ? 128 : 0;
+    if (trows > 0) {
         Fp8TileArgs t{};
         t.x = xq;
         t.xs = x_scale;
         t.w = wq;
-        t.ws = static_cast<const uint8_t*>(w_scale);
+        t.ws = w_scale;
+        t.ws_f32 = scale_t == PDQ_SCALE_F32;
         t.M = (int)M;
         t.N = (int)N;
         t.groups = (int)fp8_groups(K);

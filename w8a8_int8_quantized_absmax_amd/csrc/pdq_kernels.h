@@ -271,12 +271,13 @@ struct Fp8ExpertsArgs {
     void* y;
     int64_t ldy, tokens;
 };
-// The tiled products with e8m0 scales, gemm_fp8.hip: dense, or (sorted) of the experts' layer.
+// The tiled products, gemm_fp8.hip: dense, or (sorted) of the experts' layer.
 struct Fp8TileArgs {
     const uint8_t* x;  // packed codes
     const uint8_t* xs;
     const uint8_t* w;
-    const uint8_t* ws;
+    const void* ws;
+    bool ws_f32;
     int M, N, groups, pitch;  // N: weight rows of one matrix
     const float* bias;
     void* y;  // dense: 16 bits; down: binary32 [total, ldy]
@@ -287,7 +288,9 @@ struct Fp8TileArgs {
     uint8_t* hs;
     int h_pitch;
 };
+// rows of a tile: 256 (e8m0 scales), 192 (binary32 scales), 128, of the experts also 64
 void launch_fp8_tiles(const Fp8TileArgs& a, int out_dt, int rows, hipStream_t st);
+void launch_fp8_tiles_f32(const Fp8TileArgs& a, int epi, int out_dt, int rows, uint32_t tiles, hipStream_t st);
 void launch_fp8_expert_tiles(const Fp8TileArgs& a, bool gate_up, int rows, hipStream_t st);
 
 // The most blocks of 16 rows that `total` rows of `experts` experts take.
