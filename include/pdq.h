@@ -657,22 +657,30 @@ pdq_status pdq_pack_weight_fp8(const uint8_t* codes, const void* scale, pdq_scal
                                int64_t N, int64_t K, uint8_t* wq, void* w_scale, void* stream);
 
 /*
- * Linear layer: pdq_quantize_fp8, then pdq_gemm_fp8.
+ * Linear layer: pdq_quantize_fp8, then pdq_gemm_fp8 (one launch for few values: to about the same
+ * result, the order of its sums is another).  The parts, for callers that feed several weights.
  *   x        [M, K] of x_dt, row pitch ldx
  *   xq       packed codes out, pdq_fp8_bytes(M, K) bytes, 16-byte aligned
  *   x_scale  e8m0 out [M, pdq_fp8_scale_pitch(K)], 4-byte aligned
  *   wq, w_scale (16-byte aligned), scale_t  one matrix of pdq_quantize_weight_fp8 or pdq_pack_weight_fp8
  *   bias     [N] float or NULL
  *   y        [M, N] of y_dt (BF16 or F16) out, row pitch ldy >= N
+ *   workspace  device scratch of at least pdq_linear_fp8_workspace(M, K) bytes (0 for few
+ *            values: NULL then), 256-byte aligned; its contents on entry do not matter and nothing
+ *            in it carries over; calls that overlap in time need one each
  */
 pdq_status pdq_quantize_fp8(const void* x, pdq_dtype x_dt, int64_t M, int64_t K, int64_t ldx, uint8_t* xq,
                             uint8_t* x_scale, void* stream);
 pdq_status pdq_gemm_fp8(const uint8_t* xq, const uint8_t* x_scale, int64_t M, int64_t K, const uint8_t* wq,
                         const void* w_scale, pdq_scale_type scale_t, const float* bias, int64_t N, void* y,
                         pdq_dtype y_dt, int64_t ldy, void* stream);
+/* The kernel that pdq_gemm_fp8 runs: the activation rows of a tile (64 < .. <= 256) of the tiled kernel, or 0: the one
+ * for few rows, which streams the weight.  A performance choice.  -1 for sizes that are refused. */
+int pdq_gemm_fp8_tile(int64_t M, int64_t N, int64_t K, pdq_scale_type scale_t);
+size_t pdq_linear_fp8_workspace(int64_t M, int64_t K);
 pdq_status pdq_linear_fp8(const void* x, pdq_dtype x_dt, int64_t M, int64_t K, int64_t ldx, const uint8_t* wq,
-                          const void* w_scale, pdq_scale_type scale_t, const float* bias, int64_t N, uint8_t* xq,
-                          uint8_t* x_scale, void* y, pdq_dtype y_dt, int64_t ldy, void* stream);
+                          const void* w_scale, pdq_scale_type scale_t, const float* bias, int64_t N, void* y,
+                          pdq_dtype y_dt, int64_t ldy, void* workspace, size_t workspace_bytes, void* stream);
 
 /*
  * Routing of tokens to experts.

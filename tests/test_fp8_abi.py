@@ -51,18 +51,26 @@ def test_pack_weight(L):
 
 
 def test_linear(L):
-    def f(x=P, dt=1, m=4, k=64, ld=64, wq=P, ws=P, st=0, b=None, n=16, xq=P, xs=P, y=P, ydt=1, ldy=16):
-        return L.pdq_linear_fp8(x, dt, m, k, ld, wq, ws, st, b, n, xq, xs, y, ydt, ldy, None)
+    def f(x=P, dt=1, m=400, k=64, ld=64, wq=P, ws=P, st=0, b=None, n=16, y=P, ydt=1, ldy=16, work=P, size=1 << 20):
+        return L.pdq_linear_fp8(x, dt, m, k, ld, wq, ws, st, b, n, y, ydt, ldy, work, size, None)
     assert f(dt=3) == DTYPE and f(ydt=0) == DTYPE and f(st=7) == DTYPE
     assert f(k=40, ld=40) == SHAPE and f(k=0) == SHAPE and f(ld=32) == SHAPE and f(ldy=15) == SHAPE and f(n=-1) == SHAPE
     assert f(m=(1 << 21) + 1) == SHAPE and f(k=65552, ld=65552) == SHAPE
-    for a in ("x", "wq", "ws", "xq", "xs", "y"):
+    for a in ("x", "wq", "ws", "y"):
         assert f(**{a: None}) == NULL
-    for a, by in (("x", 8), ("wq", 8), ("ws", 8), ("xq", 8), ("xs", 2), ("y", 1), ("b", 0)):
-        if by:
-            assert f(**{a: P + by}) == ALIGN
-    assert f(b=P + 2) == ALIGN and f(ld=68) == ALIGN
-    assert f(m=0) == OK
+    for a, by in (("x", 8), ("wq", 8), ("ws", 8), ("y", 1), ("b", 2), ("work", 64)):
+        assert f(**{a: P + by}) == ALIGN
+    assert f(ld=68) == ALIGN
+    assert f(work=None) == WS and f(size=100) == WS
+    assert f(m=0) == OK and f(n=0) == OK
+    assert L.pdq_linear_fp8_workspace(400, 64) >= L.pdq_fp8_bytes(400, 64) + 400 * L.pdq_fp8_scale_pitch(64)
+    assert [L.pdq_linear_fp8_workspace(m, k) for m, k in ((1, 4096), (0, 64), (-1, 64), (4, 60))] == [0] * 4
+
+
+def test_gemm_tile(L):
+    f = L.pdq_gemm_fp8_tile
+    assert f(0, 8, 64, 0) == -1 and f(8, 0, 64, 0) == -1 and f(8, 8, 0, 0) == -1 and f(8, 8, 64, 5) == -1
+    assert f(64, 28672, 4096, 0) == 0 and f(8192, 8192, 4096, 0) == 256 and f(8192, 8192, 4096, 1) in (128, 192)
 
 
 def test_gemm_and_quantize(L):
@@ -70,6 +78,9 @@ def test_gemm_and_quantize(L):
     assert L.pdq_gemm_fp8(P, P, 4, 64, P, P, 0, None, 0, P, 1, 16, None) == OK
     assert L.pdq_gemm_fp8(P, P, 4, 63, P, P, 0, None, 16, P, 1, 16, None) == SHAPE
     assert L.pdq_gemm_fp8(None, P, 4, 64, P, P, 0, None, 16, P, 1, 16, None) == NULL
+    assert L.pdq_gemm_fp8(P, None, 4, 64, P, P, 0, None, 16, P, 1, 16, None) == NULL
+    assert L.pdq_gemm_fp8(P + 8, P, 4, 64, P, P, 0, None, 16, P, 1, 16, None) == ALIGN
+    assert L.pdq_gemm_fp8(P, P + 2, 4, 64, P, P, 0, None, 16, P, 1, 16, None) == ALIGN
     assert L.pdq_quantize_fp8(P, 1, 0, 64, 64, P, P, None) == OK
     assert L.pdq_quantize_fp8(P, 1, 4, 64, 64, None, P, None) == NULL
     assert L.pdq_quantize_fp8(P, 1, 4, 64, 64, P + 8, P, None) == ALIGN

@@ -117,9 +117,41 @@ def test_linear(m, n, k, dt, scales, bias):
     check()
     y64, size, aligned = FO.linear(values(x), wq, ws, None if b is None else values(b))
     check_linear(r["y"], y64, size, aligned, k)
-    assert np.array_equal(r["xq"].values().cpu().double().numpy(), FO.values(values(x)))
-    again = pdq.gemm_fp8(r["xq"], w, bias=None if b is None else b.cuda(), dtype=y.dtype)["y"]
-    assert torch.equal(again, y)  # the same on every call, and by the parts
+    bias_d = None if b is None else b.cuda()
+    ws = torch.full((pdq.linear_fp8_workspace_bytes(m, k) + 256,), 0xFF, dtype=torch.uint8, device="cuda")
+    assert torch.equal(pdq.linear_fp8(x.cuda(), w, bias=bias_d, workspace=ws)["y"], y)  # the same on every call
+    parts, check = gapped(m, n, y.dtype)
+    xq = pdq.quantize_fp8(x.cuda())
+    pdq.gemm_fp8(xq, w, bias=bias_d, out=parts)
+    check()
+    check_linear(parts, y64, size, aligned, k)
+    assert torch.equal(parts, pdq.gemm_fp8(xq, w, bias=bias_d, dtype=y.dtype)["y"])
+
+
+@pytest.mark.parametrize("m,n,k,scales,tile", [
+    (1, 8210, 144, "pow2", 0), (3, 16400, 272, "f32", 0), (13, 8200, 1424, "pow2", 0), (20, 8210, 144, "f32", 0), (40, 11000, 144, "pow2", 0),
+    (64, 6200, 272, "f32", 0), (520, 4100, 400, "pow2", 128), (1030, 4100, 144, "f32", 128), (2039, 8190, 400, "pow2", 256),
+    (1529, 8190, 400, "f32", 192), (4097, 300, 1040, "pow2", None), (2047, 8150, 912, "pow2", 256), (1500, 8150, 912, "f32", 192)])
+def test_linear_wide(m, n, k, scales, tile):
+    # every kernel of the rule; an odd last group for the tiled ones; some rows against the oracle
+    x = randn(m + n, m, k).bfloat16()
+    w, wq, ws = weight(n + k, (), n, k, scales)
+    if tile is not None:
+        assert pdq.gemm_fp8_tile(m, n, k, w.scale_type) == tile
+    y, check = gapped(m, n, torch.bfloat16)
+    pdq.linear_fp8(x.cuda(), w, out=y)
+    check()
+    rows = np.unique(np.concatenate([np.arange(0, m, max(1, m // 7)), [m - 1]]))
+    cols = np.unique(np.concatenate([np.arange(0, n, 97), np.arange(max(0, n - 40), n)]))
+    y64, size, aligned = FO.linear(values(x[rows]), wq, ws)
+    pick = np.ix_(np.arange(len(rows)), cols)
+    check_linear(y[torch.from_numpy(rows).cuda()][:, torch.from_numpy(cols).cuda()], y64[pick], size[pick], aligned[pick], k)
+    # and all of them against the same codes in binary32 (whose own error is far below the roundings')
+    q = pdq.quantize_fp8(x.cuda()).values()
+    scale = w.scales().repeat_interleave(128, 0)[:n].repeat_interleave(128, 1)[:, :k]
+    full = q @ (w.codes().float() * scale).T
+    assert float((y.float() - full).norm() / full.norm()) <= 2.0 ** -8 + 2.0 ** -12
+    assert bool(((y.float() - full).abs() <= 2.0 ** -8 * full.abs() + 2.0 ** -9 * full.abs().max()).all())
 
 
 @pytest.mark.parametrize("m", [1, 40, 300])

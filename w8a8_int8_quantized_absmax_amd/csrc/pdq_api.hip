@@ -934,6 +934,27 @@ Fp8GemmArgs fp8_gemm_args(int64_t M, int64_t K, const uint8_t* wq, const void* w
     return a;
 }
 
+// Rows of a tile of the tiled kernel for an FP8 product, 0: the kernel for few rows.  The estimates are in
+// microseconds for G groups, from times measured on MI355X with 64 .. 1024 rows, N 1024 .. 28672 and K
+// 1408 .. 14336; they are within a quarter of those.  A round of up to 256 tiles takes as long however many
+// tiles it holds; the other kernel's time goes with its workgroups (64 rows x 32 or 64 channels).  E.g.
+// K = 4096 (few rows / 128 / 256 rows a tile): 128 x 28672 48 / 38 / 43, 512 x 28672 148 / 68 / 53,
+// 256 x 4096 14.7 / 30.5 / 42, 1024 x 4096 38 / 29 / 42; 1024 x 14336 -> 4096 106 / 107 / 142.
+int fp8_tile_rows(int64_t M, int64_t N, int64_t G, bool f32) {
+    if (M <= 64) return 0;
+    auto rounds = [&](int64_t rows) {
+        return (double)((((M + rows - 1) / rows) * ((N + 255) / 256) + 255) / 256);
+    };
+    const int width = fp8_rows_width(M, N);
+    const double groups = (double)(((M + 63) / 64) * ((N + 16 * width - 1) / (16 * width)));
+    const double few = 3.5 + G * std::max(1.0, groups / 256) * (width == 4 ? 0.29 : width == 2 ? 0.22 : 0.16);
+    const int large = f32 ? 192 : 256;
+    const double t128 = rounds(128) * (f32 ? 3 + 1.05 * G : 1.5 + 0.95 * G);
+    const double tl = rounds(large) * (f32 ? 6 + 1.35 * G : 4 + 1.4 * G);
+    if (few <= std::min(t128, tl)) return 0;
+    return tl < t128 ? large : 128;
+}
+
 // The parts of the experts' layer's workspace, in bytes.
 struct ExpertsSpace {
     size_t x, xs, h, hs, partial;
@@ -1012,12 +1033,17 @@ pdq_status pdq_quantize_fp8(const void* x, pdq_dtype x_dt, int64_t M, int64_t K,
     return launched();
 }
 
+int pdq_gemm_fp8_tile(int64_t M, int64_t N, int64_t K, pdq_scale_type scale_t) {
+    if (M < 1 || N < 1 || K < 1 || M > kMaxRows || N > kMaxRows || K > kMaxK || !scale_ok(scale_t)) return -1;
+    return fp8_tile_rows(M, N, fp8_groups(K), scale_t == PDQ_SCALE_F32);
+}
+
 pdq_status pdq_gemm_fp8(const uint8_t* xq, const uint8_t* x_scale, int64_t M, int64_t K, const uint8_t* wq,
                         const void* w_scale, pdq_scale_type scale_t, const float* bias, int64_t N, void* y,
                         pdq_dtype y_dt, int64_t ldy, void* stream) {
     PDQ_TRY(check_fp8_gemm(M, K, wq, w_scale, scale_t, bias, N, xq, x_scale, y, y_dt, ldy));
     if (M == 0 || N == 0) return PDQ_OK;
-    const int trows = M > 1024 ? (scale_t == PDQ_E8M0 ? 256 : 192) : M > 64 ? 128 : 0;
+    const int trows = fp8_tile_rows(M, N, fp8_groups(K), scale_t == PDQ_SCALE_F32);
     if (trows > 0) {
         Fp8TileArgs t{};
         t.x = xq;
@@ -1040,14 +1066,36 @@ pdq_status pdq_gemm_fp8(const uint8_t* xq, const uint8_t* x_scale, int64_t M, in
     return launched();
 }
 
+size_t pdq_linear_fp8_workspace(int64_t M, int64_t K) {
+    if (M < 1 || M > kMaxRows || K < 16 || K > kMaxK || K % 16 != 0 || M * K > kMaxValues || fp8_fusable(M, K)) return 0;
+    return align256(pdq_fp8_bytes(M, K)) + align256((size_t)(M * fp8_scale_pitch(K)));
+}
+
 pdq_status pdq_linear_fp8(const void* x, pdq_dtype x_dt, int64_t M, int64_t K, int64_t ldx, const uint8_t* wq,
-                          const void* w_scale, pdq_scale_type scale_t, const float* bias, int64_t N, uint8_t* xq,
-                          uint8_t* x_scale, void* y, pdq_dtype y_dt, int64_t ldy, void* stream) {
+                          const void* w_scale, pdq_scale_type scale_t, const float* bias, int64_t N, void* y,
+                          pdq_dtype y_dt, int64_t ldy, void* workspace, size_t workspace_bytes, void* stream) {
     if (!dtype_ok(x_dt)) return PDQ_ERR_DTYPE;
     PDQ_TRY(check_operand(x, elem_bytes(x_dt), M, K, ldx));
-    PDQ_TRY(check_fp8_gemm(M, K, wq, w_scale, scale_t, bias, N, xq, x_scale, y, y_dt, ldy));
-    PDQ_TRY(pdq_quantize_fp8(x, x_dt, M, K, ldx, xq, x_scale, stream));
-    return pdq_gemm_fp8(xq, x_scale, M, K, wq, w_scale, scale_t, bias, N, y, y_dt, ldy, stream);
+    // (the codes' addresses are checked as the workspace's)
+    const uint8_t* some = reinterpret_cast<const uint8_t*>(16);
+    PDQ_TRY(check_fp8_gemm(M, K, wq, w_scale, scale_t, bias, N, some, some, y, y_dt, ldy));
+    const size_t need = pdq_linear_fp8_workspace(M, K);
+    if (need > 0 && (!workspace || workspace_bytes < need)) return PDQ_ERR_WORKSPACE;
+    if (!aligned(workspace, 256)) return PDQ_ERR_ALIGN;
+    if (M == 0 || N == 0) return PDQ_OK;
+    if (need == 0) {  // one launch
+        Fp8GemmArgs a = fp8_gemm_args(M, K, wq, w_scale, scale_t, bias, N, nullptr, nullptr, y, ldy);
+        a.raw = x;
+        a.raw_dt = x_dt;
+        a.K = (int)K;
+        a.ldx = ldx;
+        launch_fp8_rows(a, y_dt, static_cast<hipStream_t>(stream));
+        return launched();
+    }
+    uint8_t* xq = static_cast<uint8_t*>(workspace);
+    uint8_t* xs = xq + align256(pdq_fp8_bytes(M, K));
+    PDQ_TRY(pdq_quantize_fp8(x, x_dt, M, K, ldx, xq, xs, stream));
+    return pdq_gemm_fp8(xq, xs, M, K, wq, w_scale, scale_t, bias, N, y, y_dt, ldy, stream);
 }
 
 size_t pdq_route_workspace(int64_t tokens, int64_t experts) {

@@ -248,8 +248,13 @@ struct Fp8GemmArgs {
     const float* bias;
     void* y;
     int64_t ldy;
+    const void* raw;  // activations not coded yet, instead of x and xs (fp8_fusable): [M, K], pitch ldx
+    int raw_dt, K;
+    int64_t ldx;
 };
+bool fp8_fusable(int64_t M, int64_t K);
 void launch_fp8_rows(const Fp8GemmArgs& a, int out_dt, hipStream_t st);
+int fp8_rows_width(int64_t M, int64_t N);
 
 // The experts' layer: h = silu(gate) * up of each sorted row, coded; then down,
 // weighted, a row of partial for each token and slot; then their sum.

@@ -83,8 +83,10 @@ SIGNATURES = {
     "pdq_quantize_fp8": (ctypes.c_int, [_vp, ctypes.c_int, _i64, _i64, _i64, _vp, _vp, _vp]),
     "pdq_gemm_fp8": (ctypes.c_int, [_vp, _vp, _i64, _i64, _vp, _vp, ctypes.c_int, _vp, _i64, _vp, ctypes.c_int, _i64,
                                     _vp]),
-    "pdq_linear_fp8": (ctypes.c_int, [_vp, ctypes.c_int, _i64, _i64, _i64, _vp, _vp, ctypes.c_int, _vp, _i64, _vp, _vp,
-                                      _vp, ctypes.c_int, _i64, _vp]),
+    "pdq_gemm_fp8_tile": (ctypes.c_int, [_i64, _i64, _i64, ctypes.c_int]),
+    "pdq_linear_fp8_workspace": (_sz, [_i64, _i64]),
+    "pdq_linear_fp8": (ctypes.c_int, [_vp, ctypes.c_int, _i64, _i64, _i64, _vp, _vp, ctypes.c_int, _vp, _i64, _vp,
+                                      ctypes.c_int, _i64, _vp, _sz, _vp]),
     "pdq_route_workspace": (_sz, [_i64, _i64]),
     "pdq_route_experts": (ctypes.c_int, [_vp, ctypes.c_int, _i64, _i64, _i64, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _sz,
                                          _vp]),
@@ -839,7 +841,7 @@ class WeightFP8:
     data: packed codes, uint8; scale: e8m0 (torch.float8_e8m0fnu) or float32, [*lead,
     ceil(n / 128), pitch].  quantize_weight_fp8 and pack_weight_fp8 make them."""
 
-    __slots__ = ("data", "scale", "lead", "n", "k", "scale_type", "device", "index")
+    __slots__ = ("data", "scale", "lead", "n", "k", "scale_type", "device", "index", "at", "scale_at")
 
     def __init__(self, data: torch.Tensor, scale: torch.Tensor, n: int, k: int):
         if scale.dtype not in (torch.float8_e8m0fnu, torch.float32):
@@ -857,6 +859,7 @@ class WeightFP8:
         self.data, self.scale, self.n, self.k, self.lead = data, scale, int(n), int(k), tuple(scale.shape[:-2])
         self.scale_type = SCALE_F32 if scale.dtype == torch.float32 else E8M0
         self.device, self.index = data.device, data.get_device()
+        self.at, self.scale_at = data.data_ptr(), scale.data_ptr()
 
     @property
     def shape(self):
@@ -875,21 +878,35 @@ class WeightFP8:
 
 
 class CodesFP8:
-    """FP8 activation codes of a [rows, k] matrix, packed, and their groups' e8m0 scales."""
+    """FP8 activation codes of a [rows, k] matrix, packed, and their groups' e8m0 scales behind them,
+    in one buffer (16-byte aligned)."""
 
-    __slots__ = ("data", "scale", "rows", "k")
+    __slots__ = ("buffer", "rows", "k", "size", "pitch", "index")
 
-    def __init__(self, data: torch.Tensor, scale: torch.Tensor, rows: int, k: int):
+    def __init__(self, buffer: torch.Tensor, rows: int, k: int):
         size, pitch = _fp8_sizes(rows, k)
-        _check_dense(data, "data", torch.uint8)
-        _check_dense(scale, "scale", torch.float8_e8m0fnu, (rows, pitch))
-        if data.numel() < size or data.device != scale.device:
-            raise ValueError(f"packed {rows} x {k} codes are {size} bytes, on their scales' device")
-        self.data, self.scale, self.rows, self.k = data, scale, int(rows), int(k)
+        if not buffer.is_cuda or not buffer.is_contiguous() or buffer.nbytes < size + rows * pitch:
+            raise ValueError(f"packed {rows} x {k} codes with their scales need a contiguous device tensor of "
+                             f"{size + rows * pitch} bytes")
+        self._take(buffer, rows, k, size, pitch, buffer.get_device())
+
+    def _take(self, buffer, rows, k, size, pitch, index):
+        self.buffer, self.rows, self.k, self.size, self.pitch, self.index = buffer, rows, k, size, pitch, index
 
     @property
     def shape(self):
         return (self.rows, self.k)
+
+    @property
+    def data(self) -> torch.Tensor:
+        """The packed codes, uint8."""
+        return self.buffer.view(-1).view(torch.uint8)[:self.size]
+
+    @property
+    def scale(self) -> torch.Tensor:
+        """The groups' scales [rows, pitch], torch.float8_e8m0fnu."""
+        flat = self.buffer.view(-1).view(torch.uint8)[self.size:self.size + self.rows * self.pitch]
+        return flat.view(torch.float8_e8m0fnu).view(self.rows, self.pitch)
 
     def codes(self) -> torch.Tensor:
         """The e4m3 codes [rows, k], row-major."""
@@ -898,6 +915,14 @@ class CodesFP8:
     def values(self) -> torch.Tensor:
         """What the codes and scales stand for, float32 [rows, k]."""
         return self.codes().float() * self.scale.float().repeat_interleave(128, 1)[:, :self.k]
+
+
+def _codes_fp8(like, m, k, index):
+    """New codes of a [m, k] matrix, in like's dtype (a new tensor of another one costs the host more)."""
+    size, pitch = _fp8_sizes(m, k)
+    c = CodesFP8.__new__(CodesFP8)
+    c._take(like.new_empty((size + m * pitch + 3) // like.element_size() + 1), m, k, size, pitch, index)
+    return c
 
 
 def _stack_shape(t, name):
@@ -950,15 +975,16 @@ def quantize_fp8(x: torch.Tensor) -> CodesFP8:
     """Activations [m, k] -> FP8 codes with a power of two as scale for each row and group of 128."""
     _check_mat(x, "x")
     m, k = x.shape
-    size, pitch = _fp8_sizes(m, k)
-    data = torch.empty(size, dtype=torch.uint8, device=x.device)
-    scale = torch.empty((m, pitch), dtype=torch.float8_e8m0fnu, device=x.device)
-    _kv_call("pdq_quantize_fp8", x.get_device(), x.data_ptr(), _DT[x.dtype], m, k, _ld(x), data.data_ptr(), scale.data_ptr())
-    return CodesFP8(data, scale, m, k)
+    index = x.get_device()
+    q = _codes_fp8(x, m, k, index)
+    at = q.buffer.data_ptr()
+    _kv_call("pdq_quantize_fp8", index, x.data_ptr(), _DT[x.dtype], m, k, _ld(x), at, at + q.size)
+    return q
 
 
 def _fp8_operands(w, k, index, bias, m, out, dtype, like):
-    if not isinstance(w, WeightFP8) or w.lead:
+    """The checks that linear_fp8 and gemm_fp8 share -> y, its row pitch."""
+    if type(w) is not WeightFP8 or w.lead:
         raise ValueError("w must be one FP8 weight (a WeightFP8 without leading dimensions)")
     if w.k != k or w.index != index:
         raise ValueError(f"a [{w.n}, {w.k}] weight on device {w.index} does not fit activations of {k} on device {index}")
@@ -967,43 +993,55 @@ def _fp8_operands(w, k, index, bias, m, out, dtype, like):
         if bias.get_device() != index:
             raise ValueError("bias must be on the weight's device")
     if out is None:
+        if dtype is like.dtype and dtype in _HALF:
+            return like.new_empty((m, w.n)), w.n
         if dtype not in _HALF:
             raise ValueError(f"unsupported output dtype {dtype}")
-        return like.new_empty((m, w.n), dtype=dtype)
+        return like.new_empty((m, w.n), dtype=dtype), w.n
     _check_mat(out, "out", _HALF)
     if tuple(out.shape) != (m, w.n) or out.get_device() != index:
         raise ValueError(f"out must be [{m}, {w.n}] on the weight's device")
-    return out
+    return out, _ld(out)
 
 
-def linear_fp8(x, w: WeightFP8, bias=None, out=None, dtype=None):
-    """y = x W^T (+ bias) on FP8 codes -> dict(y, xq): x [m, k] f32, bf16 or f16, coded within the call.
+@functools.lru_cache(maxsize=4096)
+def linear_fp8_workspace_bytes(m: int, k: int) -> int:
+    return int(lib().pdq_linear_fp8_workspace(m, k))
 
-    y is f16 for f16 x, else bf16, or of `dtype`; xq: x's codes, for other weights (gemm_fp8)."""
+
+def linear_fp8(x, w: WeightFP8, bias=None, out=None, dtype=None, workspace=None):
+    """y = x W^T (+ bias) on FP8 codes -> dict(y): x [m, k] f32, bf16 or f16, coded within the call.
+    (quantize_fp8 and gemm_fp8: codes for several weights.)
+
+    y is f16 for f16 x, else bf16, or of `dtype`."""
     _check_mat(x, "x")
     m, k = x.shape
-    index = x.get_device()
-    y = _fp8_operands(w, k, index, bias, m, out,
-                      dtype or (torch.float16 if x.dtype == torch.float16 else torch.bfloat16), x)
-    size, pitch = _fp8_sizes(m, k)
-    data = x.new_empty(size, dtype=torch.uint8)
-    scale = x.new_empty((m, pitch), dtype=torch.float8_e8m0fnu)
-    _kv_call("pdq_linear_fp8", index, x.data_ptr(), _DT[x.dtype], m, k, _ld(x), w.data.data_ptr(), w.scale.data_ptr(),
-             w.scale_type, bias.data_ptr() if bias is not None else None, w.n, data.data_ptr(), scale.data_ptr(),
-             y.data_ptr(), _DT[y.dtype], _ld(y))
-    return dict(y=y, xq=CodesFP8(data, scale, m, k))
+    index, kind = x.get_device(), x.dtype
+    y, ldy = _fp8_operands(w, k, index, bias, m, out, dtype or (torch.bfloat16 if kind is torch.float32 else kind), x)
+    size, at = linear_fp8_workspace_bytes(m, k), None
+    if size or workspace is not None:
+        workspace, size = _workspace(workspace, size, x, index)
+        at = workspace.data_ptr()
+    _kv_call("pdq_linear_fp8", index, x.data_ptr(), _DT[kind], m, k, _ld(x), w.at, w.scale_at, w.scale_type,
+             bias.data_ptr() if bias is not None else None, w.n, y.data_ptr(), _DT[y.dtype], ldy, at, size)
+    return {"y": y}
 
 
 def gemm_fp8(xq: CodesFP8, w: WeightFP8, bias=None, out=None, dtype=torch.bfloat16):
     """The product of linear_fp8 on codes that are there already -> dict(y)."""
-    if not isinstance(xq, CodesFP8):
+    if type(xq) is not CodesFP8:
         raise ValueError("xq must be FP8 activation codes (a CodesFP8 object)")
-    m, k = xq.shape
-    index = xq.data.get_device()
-    y = _fp8_operands(w, k, index, bias, m, out, dtype, xq.data)
-    _kv_call("pdq_gemm_fp8", index, xq.data.data_ptr(), xq.scale.data_ptr(), m, k, w.data.data_ptr(), w.scale.data_ptr(),
-             w.scale_type, bias.data_ptr() if bias is not None else None, w.n, y.data_ptr(), _DT[y.dtype], _ld(y))
-    return dict(y=y)
+    m, k, index = xq.rows, xq.k, xq.index
+    y, ldy = _fp8_operands(w, k, index, bias, m, out, dtype, xq.buffer)
+    at = xq.buffer.data_ptr()
+    _kv_call("pdq_gemm_fp8", index, at, at + xq.size, m, k, w.at, w.scale_at, w.scale_type,
+             bias.data_ptr() if bias is not None else None, w.n, y.data_ptr(), _DT[y.dtype], ldy)
+    return {"y": y}
+
+
+def gemm_fp8_tile(m: int, n: int, k: int, scale_type: int = E8M0) -> int:
+    """Rows of a tile where gemm_fp8 runs the tiled kernel, 0 where it runs the one for few rows."""
+    return int(lib().pdq_gemm_fp8_tile(m, n, k, scale_type))
 
 
 class _RouteRuleC(ctypes.Structure):
@@ -1026,7 +1064,7 @@ class Routing:
     [tokens, k]; the rows token * k + slot sorted by expert: offsets int32 [experts + 1], rows int32
     [tokens * k]."""
 
-    __slots__ = ("ids", "weights", "offsets", "rows", "tokens", "experts", "k", "index", "_c", "_ref")
+    __slots__ = ("_tensors", "_buffer", "tokens", "experts", "k", "index", "_c", "_ref")
 
     def __init__(self, ids: torch.Tensor, weights: torch.Tensor, offsets: torch.Tensor, rows: torch.Tensor):
         if ids.dim() != 2 or offsets.dim() != 1 or offsets.shape[0] < 2:
@@ -1038,13 +1076,34 @@ class Routing:
         _check_dense(rows, "rows", torch.int32, (tokens * k,))
         if not ids.device == weights.device == offsets.device == rows.device:
             raise ValueError("the routing's tensors must be on one device")
-        self._take(ids, weights, offsets, rows, tokens, offsets.shape[0] - 1, k, ids.get_device())
-
-    def _take(self, ids, weights, offsets, rows, tokens, experts, k, index):
-        self.ids, self.weights, self.offsets, self.rows = ids, weights, offsets, rows
-        self.tokens, self.experts, self.k, self.index = tokens, experts, k, index
-        self._c = _RoutingC(ids.data_ptr(), weights.data_ptr(), offsets.data_ptr(), rows.data_ptr(), tokens, experts, k)
+        self._tensors, self._buffer = (ids, weights, offsets, rows), None
+        self.tokens, self.experts, self.k, self.index = tokens, offsets.shape[0] - 1, k, ids.get_device()
+        self._c = _RoutingC(*(t.data_ptr() for t in self._tensors), tokens, self.experts, k)
         self._ref = ctypes.byref(self._c)
+
+    def _all(self):
+        if self._tensors is None:  # parts of route_experts' one buffer, as tensors when they are asked for
+            n, e = self.tokens * self.k, self.experts + 1
+            ids, weights, rows, offsets = self._buffer[:3 * n + e].split((n, n, n, e))
+            self._tensors = (ids.view(self.tokens, self.k), weights.view(torch.float32).view(self.tokens, self.k),
+                             offsets, rows)
+        return self._tensors
+
+    @property
+    def ids(self) -> torch.Tensor:
+        return self._all()[0]
+
+    @property
+    def weights(self) -> torch.Tensor:
+        return self._all()[1]
+
+    @property
+    def offsets(self) -> torch.Tensor:
+        return self._all()[2]
+
+    @property
+    def rows(self) -> torch.Tensor:
+        return self._all()[3]
 
 
 @functools.lru_cache(maxsize=4096)
@@ -1054,6 +1113,8 @@ def route_workspace_bytes(tokens: int, experts: int) -> int:
 
 @functools.lru_cache(maxsize=256)
 def _route_rule(score, k, groups, top_groups, group_score, renormalize, scale):
+    if score not in _SCORES:
+        raise ValueError(f"score must be one of {sorted(_SCORES)}")
     c = _RouteRuleC(_SCORES[score], k, groups, top_groups, group_score, 1 if renormalize else 0, scale)
     return c, ctypes.byref(c)
 
@@ -1068,34 +1129,40 @@ def route_experts(logits, k: int, score: str = "softmax", bias=None, groups: int
     of their group_score largest; renormalize: a token's weights sum to 1, times scale."""
     _check_mat(logits, "logits")
     tokens, experts = logits.shape
-    index = logits.get_device()
-    if score not in _SCORES:
-        raise ValueError(f"score must be one of {sorted(_SCORES)}")
+    index, kind = logits.get_device(), logits.dtype
     if bias is not None:
         _check_dense(bias, "bias", torch.float32, (experts,))
         if bias.get_device() != index:
             raise ValueError("bias must be on logits' device")
     if not 1 <= k <= experts:
         raise ValueError(f"k = {k} of {experts} experts")
-    rule = _route_rule(score, int(k), int(groups), int(top_groups), int(group_score), bool(renormalize), float(scale))
-    ids = logits.new_empty((tokens, k), dtype=torch.int32)
-    weights = logits.new_empty((tokens, k), dtype=torch.float32)
-    offsets = logits.new_empty(experts + 1, dtype=torch.int32)
-    rows = logits.new_empty(tokens * k, dtype=torch.int32)
+    rule = _route_rule(score, k, groups, top_groups, group_score, renormalize, scale)
+    n = tokens * k
+    used = (3 * n + experts + 1 + 63) // 64 * 64
     size = route_workspace_bytes(tokens, experts)
-    workspace, size = _workspace(workspace, size, logits, index)
-    _kv_call("pdq_route_experts", index, logits.data_ptr(), _DT[logits.dtype], tokens, experts, _ld(logits),
-             bias.data_ptr() if bias is not None else None, rule[1], ids.data_ptr(), weights.data_ptr(),
-             offsets.data_ptr(), rows.data_ptr(), workspace.data_ptr() if size else None, size)
+    if workspace is None:  # behind the outputs, in one buffer
+        buffer = logits.new_empty(used + size // 4, dtype=torch.int32)
+        at = buffer.data_ptr()
+        ws = at + 4 * used
+    else:
+        workspace, size = _workspace(workspace, size, logits, index)
+        buffer = logits.new_empty(used, dtype=torch.int32)
+        at = buffer.data_ptr()
+        ws = workspace.data_ptr()
+    offsets = at + 12 * n
+    _kv_call("pdq_route_experts", index, logits.data_ptr(), _DT[kind], tokens, experts, _ld(logits),
+             bias.data_ptr() if bias is not None else None, rule[1], at, at + 4 * n, offsets, at + 8 * n, ws, size)
     r = Routing.__new__(Routing)
-    r._take(ids, weights, offsets, rows, tokens, experts, k, index)
+    r._tensors, r._buffer, r.tokens, r.experts, r.k, r.index = None, buffer, tokens, experts, k, index
+    r._c = _RoutingC(at, at + 4 * n, offsets, at + 8 * n, tokens, experts, k)
+    r._ref = ctypes.byref(r._c)
     return r
 
 
 def _workspace(workspace, size, like, index):
     """The caller's workspace, or a new one."""
     if workspace is None:
-        return (like.new_empty(size, dtype=torch.uint8) if size else None), size
+        return (like.new_empty(size // like.element_size()) if size else None), size
     _check_dense(workspace, "workspace", torch.uint8)
     if workspace.get_device() != index:
         raise ValueError("the workspace must be on the call's device")
@@ -1135,8 +1202,7 @@ def experts_fp8(x, routing: Routing, gate_up: WeightFP8, down: WeightFP8, out=No
             raise ValueError("out must have x's shape and device")
     size = experts_fp8_workspace_bytes(tokens, routing.k, experts, hidden, inner)
     workspace, size = _workspace(workspace, size, x, index)
-    c = _ExpertsC(gate_up.data.data_ptr(), gate_up.scale.data_ptr(), down.data.data_ptr(), down.scale.data_ptr(),
-                  gate_up.scale_type, experts, hidden, inner)
+    c = _ExpertsC(gate_up.at, gate_up.scale_at, down.at, down.scale_at, gate_up.scale_type, experts, hidden, inner)
     _kv_call("pdq_experts_fp8", index, x.data_ptr(), _DT[x.dtype], _ld(x), routing._ref, ctypes.byref(c), y.data_ptr(),
              _ld(y), workspace.data_ptr() if size else None, size)
-    return dict(y=y)
+    return {"y": y}
