@@ -1100,7 +1100,7 @@ pdq_status pdq_linear_fp8(const void* x, pdq_dtype x_dt, int64_t M, int64_t K, i
 
 size_t pdq_route_workspace(int64_t tokens, int64_t experts) {
     if (tokens < 1 || tokens > kMaxRows || experts < 1 || experts > kMaxExperts) return 0;
-    return align256((size_t)route_blocks(tokens) * (size_t)experts * 4);
+    return align256(route_space(tokens, experts));
 }
 
 pdq_status pdq_route_experts(const void* logits, pdq_dtype dt, int64_t tokens, int64_t experts, int64_t ldl,

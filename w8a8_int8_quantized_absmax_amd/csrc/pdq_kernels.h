@@ -316,9 +316,9 @@ struct RouteArgs {
     float* weights;
     int32_t* offsets;
     int32_t* rows;
-    int32_t* hist;  // [route_blocks(tokens), experts]
+    int32_t* hist;  // route_space(tokens, experts) bytes
 };
-int route_blocks(int64_t tokens);
+size_t route_space(int64_t tokens, int64_t experts);
 void launch_route(const RouteArgs& a, int dt, hipStream_t st);
 
 }  // namespace pdq

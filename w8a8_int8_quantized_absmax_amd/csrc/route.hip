@@ -1,11 +1,14 @@
 // Routing to experts (gfx950): scores of the router's logits, groups, the largest k,
 // their weights; and the rows (token and slot) sorted by expert.
 //
-// Latency and not bytes: a wavefront a token, the scores in its registers, and the
-// largest found k times over.  What decides a choice is binary64: a score next to
-// another's would else be ordered by its last rounding.  Counting is by workgroup
-// (LDS atomics on whole numbers, whose order changes nothing), the places by sums
-// over the workgroups before, so that the order is the tokens' own.
+// Latency and not bytes.  A token is taken by 16 lanes (64 where there are more than 256
+// experts), its logits in their registers, and the largest is found k times over: maxima
+// within 16 lanes are four lane permutations, no LDS.  What decides a choice is binary64: a
+// score next to another's would else be ordered by its last rounding; scores that decide
+// nothing are formed for the chosen experts alone.
+// Counting is by workgroup (LDS atomics on whole numbers, whose order changes nothing), the
+// places by sums over the workgroups before, so that the order is the tokens' own: two
+// launches, one where a workgroup takes all tokens.
 
 #include <algorithm>
 
@@ -15,7 +18,7 @@ namespace pdq {
 
 namespace {
 
-constexpr int kThreads = 512, kWaves = kThreads / 64;
+constexpr int kThreads = 512, kWaves = kThreads / 64, kMost = 512;  // experts
 
 // Whole numbers in the order of the doubles; NaN 1 (below every number), 0 is kept for "not to be chosen".
 __device__ __forceinline__ uint64_t order_key(double v) {
@@ -24,13 +27,55 @@ __device__ __forceinline__ uint64_t order_key(double v) {
     return u >> 63 ? ~u : u | (uint64_t(1) << 63);
 }
 
-__device__ __forceinline__ uint64_t wave_max_u64(uint64_t v) {
-#pragma unroll
-    for (int d = 32; d >= 1; d >>= 1) {
-        const uint64_t o = __shfl_xor((unsigned long long)v, d);
-        v = o > v ? o : v;
+template <int kCtrl>
+__device__ __forceinline__ uint64_t dpp_u64(uint64_t v) {
+    return (uint64_t)dpp_u32<kCtrl>((uint32_t)(v >> 32)) << 32 | dpp_u32<kCtrl>((uint32_t)v);
+}
+
+// f over the L lanes of a token, the same in each of them.
+template <int L, typename F>
+__device__ __forceinline__ uint64_t reduce_u64(uint64_t v, F f) {
+    v = f(v, dpp_u64<0xB1>(v));   // quad_perm [1, 0, 3, 2]
+    v = f(v, dpp_u64<0x4E>(v));   // quad_perm [2, 3, 0, 1]
+    v = f(v, dpp_u64<0x141>(v));  // row_half_mirror
+    v = f(v, dpp_u64<0x140>(v));  // row_mirror
+    if constexpr (L == 64) {
+        v = f(v, (uint64_t)__shfl_xor((unsigned long long)v, 16));
+        v = f(v, (uint64_t)__shfl_xor((unsigned long long)v, 32));
     }
     return v;
+}
+
+template <int L>
+__device__ __forceinline__ double sum_of(double v) {
+    return __longlong_as_double((long long)reduce_u64<L>((uint64_t)__double_as_longlong(v), [](uint64_t a, uint64_t b) {
+        return (uint64_t)__double_as_longlong(__longlong_as_double((long long)a) + __longlong_as_double((long long)b));
+    }));
+}
+
+template <int L>
+__device__ __forceinline__ uint64_t max_of(uint64_t v) {
+    return reduce_u64<L>(v, [](uint64_t a, uint64_t b) { return a > b ? a : b; });
+}
+
+template <int L>
+__device__ __forceinline__ uint32_t min_of(uint32_t v) {
+    v = min(v, dpp_u32<0xB1>(v));
+    v = min(v, dpp_u32<0x4E>(v));
+    v = min(v, dpp_u32<0x141>(v));
+    v = min(v, dpp_u32<0x140>(v));
+    if constexpr (L == 64) {
+        v = min(v, (uint32_t)__shfl_xor((int)v, 16));
+        v = min(v, (uint32_t)__shfl_xor((int)v, 32));
+    }
+    return v;
+}
+
+// Whether a lane of the token says so.
+template <int L>
+__device__ __forceinline__ bool any_of(bool v) {
+    const uint64_t all = __ballot(v);
+    return L == 64 ? all != 0 : (all >> (threadIdx.x & 48) & 0xffff) != 0;
 }
 
 template <int DT>
@@ -40,190 +85,109 @@ __device__ __forceinline__ float logit(const void* row, int e) {
     else return f16_to_f32(static_cast<const uint16_t*>(row)[e]);
 }
 
-// VPL: experts a lane (lane + 64 j).
-template <int DT, int VPL>
-__global__ __launch_bounds__(kThreads) void k_route(RouteArgs a, int per) {
-    __shared__ int hist[64 * VPL];
-    __shared__ double cs[kWaves][64 * VPL];
-    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-    for (int e = threadIdx.x; e < a.experts; e += kThreads) hist[e] = 0;
-    __syncthreads();
-    const int t0 = blockIdx.x * per, t1 = min(t0 + per, a.tokens);
-    const int size = a.experts / a.groups;
-    for (int t = t0 + wave; t < t1; t += kWaves) {
-        const char* row = static_cast<const char*>(a.logits) + t * a.ldl * Elem<DT>::bytes;
-        double x[VPL], p[VPL];
-        uint64_t key[VPL];
-        bool nan = false;
-        double top = -INFINITY;
-#pragma unroll
-        for (int j = 0; j < VPL; ++j) {
-            const int e = lane + 64 * j;
-            x[j] = e < a.experts ? (double)logit<DT>(row, e) : -INFINITY;
-            nan |= x[j] != x[j];
-            top = x[j] > top ? x[j] : top;
-        }
-        nan = __any(nan);
-        if (a.sigmoid) {
-#pragma unroll
-            for (int j = 0; j < VPL; ++j) p[j] = 1.0 / (1.0 + exp(-x[j]));
-        } else {
-#pragma unroll
-            for (int d = 32; d >= 1; d >>= 1) {
-                const double o = __shfl_xor(top, d);
-                top = o > top ? o : top;
-            }
-            double sum = 0.0;
-#pragma unroll
-            for (int j = 0; j < VPL; ++j) {
-                p[j] = x[j] == top ? 1.0 : exp(x[j] - top);  // infinite logits share the weight
-                if (x[j] == -INFINITY) p[j] = 0.0;
-                sum += p[j];
-            }
-#pragma unroll
-            for (int d = 32; d >= 1; d >>= 1) sum += __shfl_xor(sum, d);
-#pragma unroll
-            for (int j = 0; j < VPL; ++j) p[j] = p[j] / sum;
-        }
-#pragma unroll
-        for (int j = 0; j < VPL; ++j) {
-            const int e = lane + 64 * j;
-            const double c = a.bias && e < a.experts ? p[j] + (double)a.bias[e] : x[j];
-            key[j] = x[j] == -INFINITY || c == -INFINITY ? 0 : order_key(c);
-            if (a.groups > 1) cs[wave][e] = key[j] < 2 ? -INFINITY : a.bias ? c : p[j];
-        }
-        if (a.groups > 1) {
-            __builtin_amdgcn_fence(__ATOMIC_SEQ_CST, "workgroup");
-            __builtin_amdgcn_wave_barrier();
-            uint64_t mine = 0;
-            if (lane < a.groups) {
-                double first = -INFINITY, second = -INFINITY;
-                for (int i = 0; i < size; ++i) {
-                    const double v = cs[wave][lane * size + i];
-                    if (v > first) {
-                        second = first;
-                        first = v;
-                    } else if (v > second) {
-                        second = v;
-                    }
-                }
-                if (first > -INFINITY)
-                    mine = order_key(a.group_score == 2 && second > -INFINITY ? first + second : first);
-            }
-            int rank = 0;
-            for (int h = 0; h < a.groups; ++h) {
-                const uint64_t o = __shfl((unsigned long long)mine, h);
-                rank += o > mine || (o == mine && h < lane);
-            }
-            const uint64_t kept = __ballot(lane < a.groups && rank < a.top_groups);
-            __builtin_amdgcn_wave_barrier();
-#pragma unroll
-            for (int j = 0; j < VPL; ++j)
-                if (!(kept >> min((lane + 64 * j) / size, 63) & 1)) key[j] = 0;
-        }
-        int id = -1;     // lane s: slot s
-        double w = 0.0, sum = 0.0;
-        for (int s = 0; s < a.k; ++s) {
-            uint64_t best = key[0];
-#pragma unroll
-            for (int j = 1; j < VPL; ++j) best = key[j] > best ? key[j] : best;
-            best = wave_max_u64(best);
-            if (best == 0) break;
-            int at = -1;
-            double pv = 0.0;
-#pragma unroll
-            for (int j = 0; j < VPL; ++j) {
-                const uint64_t eq = __ballot(key[j] == best);
-                if (at < 0 && eq) {
-                    const int l = __builtin_ctzll(eq);
-                    at = 64 * j + l;
-                    pv = __shfl(p[j], l);
-                    if (lane == l) key[j] = 0;
-                }
-            }
-            sum += pv;
-            if (lane == s) {
-                id = at;
-                w = pv;
-            }
-        }
-        if (lane < a.k) {
-            if (a.renormalize) w = sum > 0.0 ? w / sum : sum == 0.0 ? 0.0 : sum;
-            const int64_t flat = (int64_t)t * a.k + lane;
-            a.ids[flat] = id;
-            a.weights[flat] = id < 0 ? 0.0f : nan ? __builtin_nanf("") : (float)(w * (double)a.scale);
-            if (id >= 0) atomicAdd(&hist[id], 1);
-        }
-    }
-    __syncthreads();
-    for (int e = threadIdx.x; e < a.experts; e += kThreads) a.hist[(int64_t)blockIdx.x * a.experts + e] = hist[e];
+// exp(x - top); infinite logits share a softmax's weight.
+__device__ __forceinline__ double shifted_exp(float x, float top) {
+    return x == top ? 1.0 : exp((double)x - (double)top);
 }
 
-// The rows of the workgroup's tokens to their places: an expert's begin behind those
-// of the experts before it, a workgroup's behind those of the workgroups before it.
-__global__ __launch_bounds__(kThreads) void k_route_sort(RouteArgs a, int per) {
-    __shared__ int next[1024], wsum[kWaves], all;
-    __shared__ unsigned long long lanes[1024];
-    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-    int before_all = 0;
-    for (int e0 = 0; e0 < a.experts; e0 += kThreads) {
-        const int e = e0 + threadIdx.x;
-        int total = 0, before = 0;
-        if (e < a.experts)
-            for (int b = 0; a.tokens > 0 && b < (int)gridDim.x; ++b) {
-                const int n = a.hist[(int64_t)b * a.experts + e];
-                total += n;
-                before += b < (int)blockIdx.x ? n : 0;
-            }
-        int sum = total;
+__device__ __forceinline__ double sigmoid(float x) { return 1.0 / (1.0 + exp(-(double)x)); }
+
+struct SortSpace {
+    int total[kMost], next[kMost], wave_next[kWaves][kMost], sums[kWaves];
+    unsigned long long lanes[kWaves][kMost];
+};
+
+// The rows of the workgroup's tokens [t0, t1) to their places, by the whole workgroup: an expert's
+// begin behind those of the experts before it, a workgroup's behind those of the workgroups
+// before it.  hist: the blocks' counts, rows of `pitch`.
+__device__ void sort_rows(const RouteArgs& a, const int* hist, int pitch, int blocks, int block, int t0, int t1,
+                          SortSpace& s) {
+    const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+    s.total[tid] = 0;  // kThreads == kMost
+    s.next[tid] = 0;
 #pragma unroll
-        for (int d = 1; d < 64; d <<= 1) {
-            const int o = __shfl_up(sum, d);
-            if (lane >= d) sum += o;
-        }
-        if (lane == 63) wsum[wave] = sum;
-        __syncthreads();
-        int base = before_all;
-        for (int w = 0; w < kWaves; ++w) {
-            if (w < wave) base += wsum[w];
-            before_all += wsum[w];
-        }
-        if (e < a.experts) {
-            next[e] = base + sum - total + before;
-            lanes[e] = 0;
-            if (blockIdx.x == 0) {
-                a.offsets[e] = base + sum - total;
-                if (e == a.experts - 1) a.offsets[a.experts] = base + sum;
-            }
-        }
-        __syncthreads();
+    for (int w = 0; w < kWaves; ++w) {
+        s.wave_next[w][tid] = 0;
+        s.lanes[w][tid] = 0;
     }
-    if (threadIdx.x == 0) all = before_all;
     __syncthreads();
-    const int64_t total = (int64_t)a.tokens * a.k;
-    for (int64_t i = all + blockIdx.x * (int64_t)kThreads + threadIdx.x; i < total; i += (int64_t)gridDim.x * kThreads)
-        a.rows[i] = -1;
-    if (wave != 0) return;
-    const int64_t f0 = (int64_t)blockIdx.x * per * a.k, f1 = min(f0 + (int64_t)per * a.k, total);
-    for (int64_t f = f0; f < f1; f += 64) {  // in order, 64 rows at a time
-        const int id = f + lane < f1 ? a.ids[f + lane] : -1;
-        if (id >= 0) atomicOr(&lanes[id], 1ull << lane);
+    // counts: four experts a lane, the blocks dealt to the slices of lanes
+    const int quads = pitch / 4, slices = kThreads / quads, slice = tid / quads;
+    if (slice < slices) {
+        v4i total = v4i{}, before = v4i{};
+        const v4i* h = reinterpret_cast<const v4i*>(hist) + tid % quads;
+        for (int b = slice; b < blocks; b += slices) {
+            const v4i n = h[(int64_t)b * quads];
+            total += n;
+            if (b < block) before += n;
+        }
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const int e = tid % quads * 4 + i;
+            if (total[i]) atomicAdd(&s.total[e], total[i]);
+            if (before[i]) atomicAdd(&s.next[e], before[i]);
+        }
+    }
+    // the workgroup's own, by wavefront
+    const int64_t f0 = (int64_t)t0 * a.k, f1 = (int64_t)t1 * a.k;
+    const int64_t each = (f1 - f0 + 64 * kWaves - 1) / (64 * kWaves) * 64;  // rows of a wavefront
+    const int64_t w0 = min(f0 + wave * each, f1), w1 = min(w0 + each, f1);
+    for (int64_t f = w0 + lane; f < w1; f += 64) {
+        const int id = a.ids[f];
+        if (id >= 0) atomicAdd(&s.wave_next[wave][id], 1);
+    }
+    __syncthreads();
+    const int mine = s.total[tid];
+    int sum = mine;
+#pragma unroll
+    for (int d = 1; d < 64; d <<= 1) {
+        const int o = __shfl_up(sum, d);
+        if (lane >= d) sum += o;
+    }
+    if (lane == 63) s.sums[wave] = sum;
+    __syncthreads();
+    int base = 0, all = 0;
+#pragma unroll
+    for (int w = 0; w < kWaves; ++w) {
+        if (w < wave) base += s.sums[w];
+        all += s.sums[w];
+    }
+    const int first = base + sum - mine;
+    if (tid < a.experts) {
+        if (block == 0) {
+            a.offsets[tid] = first;
+            if (tid == a.experts - 1) a.offsets[a.experts] = all;
+        }
+        int at = first + s.next[tid];
+#pragma unroll
+        for (int w = 0; w < kWaves; ++w) {
+            const int n = s.wave_next[w][tid];
+            s.wave_next[w][tid] = at;
+            at += n;
+        }
+    }
+    __syncthreads();
+    const int64_t rows = (int64_t)a.tokens * a.k;
+    for (int64_t i = all + (int64_t)block * kThreads + tid; i < rows; i += (int64_t)blocks * kThreads) a.rows[i] = -1;
+    for (int64_t f = w0; f < w1; f += 64) {  // in order, 64 rows at a time
+        const int id = f + lane < w1 ? a.ids[f + lane] : -1;
+        if (id >= 0) atomicOr(&s.lanes[wave][id], 1ull << lane);
         __builtin_amdgcn_fence(__ATOMIC_SEQ_CST, "workgroup");
         __builtin_amdgcn_wave_barrier();
         unsigned long long same = 0;
-        int base = 0;
+        int at = 0;
         if (id >= 0) {
-            same = lanes[id];
-            base = next[id];
+            same = s.lanes[wave][id];
+            at = s.wave_next[wave][id];
         }
         __builtin_amdgcn_fence(__ATOMIC_SEQ_CST, "workgroup");
         __builtin_amdgcn_wave_barrier();
         if (id >= 0) {
             const int rank = __popcll(same & ((1ull << lane) - 1));
-            a.rows[base + rank] = (int)(f + lane);
+            a.rows[at + rank] = (int)(f + lane);
             if (rank == 0) {  // the first of its expert's
-                next[id] = base + __popcll(same);
-                lanes[id] = 0;
+                s.wave_next[wave][id] = at + __popcll(same);
+                s.lanes[wave][id] = 0;
             }
         }
         __builtin_amdgcn_fence(__ATOMIC_SEQ_CST, "workgroup");
@@ -231,34 +195,219 @@ __global__ __launch_bounds__(kThreads) void k_route_sort(RouteArgs a, int per) {
     }
 }
 
-// Tokens of a workgroup: 32, more where that would be more than 256 workgroups (each of
-// which reads every other's counts).
-int route_tokens(int64_t tokens) { return (int)std::max<int64_t>(32, (tokens + 255) / 256); }
+// L lanes a token, VPL experts a lane (lane + L j).  kAlone: the workgroup takes all tokens, and sorts
+// them too.
+template <int DT, int L, int VPL, bool kAlone>
+__global__ __launch_bounds__(kThreads) void k_route(RouteArgs a, int per, int pitch) {
+    constexpr int kTeams = kThreads / L, kSlots = L == 16 ? 2 : 1;  // at most 32 choices
+    __shared__ __attribute__((aligned(16))) int hist[kMost];
+    // the groups' scores; and, afterwards, what sorting needs
+    union Space {
+        double scores[kTeams][L * VPL];
+        SortSpace sort;
+        __device__ Space() {}
+    };
+    __shared__ Space space;
+    const int lane = threadIdx.x & 63, r = lane & (L - 1), team = threadIdx.x / L;
+    hist[threadIdx.x] = 0;
+    __syncthreads();
+    const int t0 = blockIdx.x * per, t1 = min(t0 + per, a.tokens);
+    const int size = a.experts / a.groups;
+    const bool every = a.bias || a.groups > 1;  // the scores of every expert take part in the choice
+    for (int t = t0 + team; t < t1; t += kTeams) {
+        const char* row = static_cast<const char*>(a.logits) + t * a.ldl * Elem<DT>::bytes;
+        float x[VPL];
+        bool nan = false;
+        float top = -INFINITY;
+#pragma unroll
+        for (int j = 0; j < VPL; ++j) {
+            const int e = r + L * j;
+            x[j] = e < a.experts ? logit<DT>(row, e) : -INFINITY;
+        }
+#pragma unroll
+        for (int j = 0; j < VPL; ++j) {
+            nan |= x[j] != x[j];
+            top = fmaxf(top, x[j]);
+        }
+        nan = any_of<L>(nan);
+        top = fmaxf(top, dpp_f32<0xB1>(top));
+        top = fmaxf(top, dpp_f32<0x4E>(top));
+        top = fmaxf(top, dpp_f32<0x141>(top));
+        top = fmaxf(top, dpp_f32<0x140>(top));
+        if constexpr (L == 64) {
+            top = fmaxf(top, __shfl_xor(top, 16));
+            top = fmaxf(top, __shfl_xor(top, 32));
+        }
+        uint64_t key[VPL];
+        double sum = 1.0;
+        if (every || (!a.sigmoid && !a.renormalize)) {
+            double p[VPL];
+            if (a.sigmoid) {
+#pragma unroll
+                for (int j = 0; j < VPL; ++j) p[j] = sigmoid(x[j]);
+            } else {
+                sum = 0.0;
+#pragma unroll
+                for (int j = 0; j < VPL; ++j) {
+                    p[j] = x[j] == -INFINITY ? 0.0 : shifted_exp(x[j], top);
+                    sum += p[j];
+                }
+                sum = sum_of<L>(sum);
+                if (every) {
+#pragma unroll
+                    for (int j = 0; j < VPL; ++j) p[j] = p[j] / sum;
+                }
+            }
+#pragma unroll
+            for (int j = 0; j < VPL; ++j) {
+                const int e = r + L * j;
+                const double c = a.bias && e < a.experts ? p[j] + (double)a.bias[e] : (double)x[j];
+                key[j] = x[j] == -INFINITY || c == -INFINITY ? 0 : order_key(c);
+                if (a.groups > 1) space.scores[team][e] = key[j] < 2 ? -INFINITY : a.bias ? c : p[j];
+            }
+        } else {
+#pragma unroll
+            for (int j = 0; j < VPL; ++j) key[j] = x[j] == -INFINITY ? 0 : order_key((double)x[j]);
+        }
+        if (a.groups > 1) {  // lane i's groups: i, i + L, ..; at most 64
+            __builtin_amdgcn_fence(__ATOMIC_SEQ_CST, "workgroup");
+            __builtin_amdgcn_wave_barrier();
+            uint64_t best[64 / L];
+            int rank[64 / L];
+#pragma unroll
+            for (int q = 0; q < 64 / L; ++q) {
+                const int g = r + L * q;
+                best[q] = 0;
+                rank[q] = 0;
+                if (g < a.groups) {
+                    double first = -INFINITY, second = -INFINITY;
+                    const double* v = space.scores[team] + g * size;
+#pragma unroll 4
+                    for (int i = 0; i < size; ++i) {
+                        second = fmax(second, fmin(first, v[i]));
+                        first = fmax(first, v[i]);
+                    }
+                    if (first > -INFINITY) best[q] = order_key(a.group_score == 2 && second > -INFINITY ? first + second : first);
+                }
+            }
+            for (int h = 0; h < a.groups; ++h) {
+                uint64_t o = 0;
+#pragma unroll
+                for (int q = 0; q < 64 / L; ++q)
+                    if (h / L == q) o = __shfl((unsigned long long)best[q], (lane & ~(L - 1)) + h % L);
+#pragma unroll
+                for (int q = 0; q < 64 / L; ++q) rank[q] += o > best[q] || (o == best[q] && h < r + L * q);
+            }
+            uint64_t kept = 0;
+#pragma unroll
+            for (int q = 0; q < 64 / L; ++q) {
+                const uint64_t b = __ballot(r + L * q < a.groups && rank[q] < a.top_groups);
+                kept |= (L == 64 ? b : b >> (lane & 48) & 0xffff) << (L * q & 63);
+            }
+            __builtin_amdgcn_wave_barrier();
+#pragma unroll
+            for (int j = 0; j < VPL; ++j)
+                if (!(kept >> min((r + L * j) / size, 63) & 1)) key[j] = 0;
+        }
+        int id[kSlots];
+#pragma unroll
+        for (int q = 0; q < kSlots; ++q) id[q] = -1;
+        for (int s = 0; s < a.k; ++s) {
+            uint64_t best = key[0];
+#pragma unroll
+            for (int j = 1; j < VPL; ++j) best = key[j] > best ? key[j] : best;
+            best = max_of<L>(best);
+            if (best == 0) break;  // (the same in a token's lanes)
+            uint32_t at = 0xffffffffu;
+#pragma unroll
+            for (int j = VPL - 1; j >= 0; --j)
+                if (key[j] == best) at = r + L * j;
+            at = min_of<L>(at);  // the lowest of equals
+#pragma unroll
+            for (int j = 0; j < VPL; ++j)
+                if (at == (uint32_t)(r + L * j)) key[j] = 0;
+#pragma unroll
+            for (int q = 0; q < kSlots; ++q)
+                if (s == r + L * q) id[q] = (int)at;
+        }
+        double p[kSlots], total = 0.0;
+#pragma unroll
+        for (int q = 0; q < kSlots; ++q) {
+            p[q] = 0.0;
+            if (id[q] >= 0) {
+                const float v = logit<DT>(row, id[q]);
+                p[q] = a.sigmoid ? sigmoid(v) : shifted_exp(v, top);
+            }
+            total += p[q];
+        }
+        if (a.renormalize) total = sum_of<L>(total);
+        else total = a.sigmoid ? 1.0 : sum;
+#pragma unroll
+        for (int q = 0; q < kSlots; ++q) {
+            if (r + L * q >= a.k) continue;
+            const int64_t flat = (int64_t)t * a.k + r + L * q;
+            a.ids[flat] = id[q];
+            // (a sum of 0: every score 0)
+            const double w = total == 0.0 ? 0.0 : p[q] / total * (double)a.scale;
+            a.weights[flat] = id[q] < 0 ? 0.0f : nan ? __builtin_nanf("") : (float)w;
+            if (id[q] >= 0) atomicAdd(&hist[id[q]], 1);
+        }
+    }
+    __syncthreads();
+    if constexpr (kAlone) {
+        sort_rows(a, hist, pitch, 1, 0, t0, t1, space.sort);
+    } else {
+        if ((int)threadIdx.x < pitch) a.hist[(int64_t)blockIdx.x * pitch + threadIdx.x] = hist[threadIdx.x];
+    }
+}
+
+__global__ __launch_bounds__(kThreads) void k_route_sort(RouteArgs a, int per, int pitch) {
+    __shared__ SortSpace space;
+    const int t0 = blockIdx.x * per;
+    sort_rows(a, a.hist, pitch, a.tokens ? gridDim.x : 0, blockIdx.x, min(t0, a.tokens), min(t0 + per, a.tokens), space);
+}
+
+// Tokens of a workgroup: 32 (16 lanes each), or as many as leave at most 256 workgroups, each of which
+// reads every other's counts.  Up to 64 tokens one workgroup does it all: its second round of
+// tokens takes less than another launch.
+int route_tokens(int64_t tokens) { return tokens <= 64 ? 64 : (int)std::max<int64_t>(32, (tokens + 255) / 256); }
+
+int hist_pitch(int experts) { return (experts + 3) / 4 * 4; }
+
+template <int DT, int L, int VPL>
+void launch_scores(const RouteArgs& a, int per, uint32_t blocks, hipStream_t st) {
+    const int pitch = hist_pitch(a.experts);
+    if (blocks == 1) hipLaunchKernelGGL((k_route<DT, L, VPL, true>), dim3(1), dim3(kThreads), 0, st, a, per, pitch);
+    else hipLaunchKernelGGL((k_route<DT, L, VPL, false>), dim3(blocks), dim3(kThreads), 0, st, a, per, pitch);
+}
 
 template <int DT>
 void launch_scores(const RouteArgs& a, int per, uint32_t blocks, hipStream_t st) {
-    const dim3 grid(blocks), block(kThreads);
-    if (a.experts <= 64) hipLaunchKernelGGL((k_route<DT, 1>), grid, block, 0, st, a, per);
-    else if (a.experts <= 128) hipLaunchKernelGGL((k_route<DT, 2>), grid, block, 0, st, a, per);
-    else if (a.experts <= 256) hipLaunchKernelGGL((k_route<DT, 4>), grid, block, 0, st, a, per);
-    else hipLaunchKernelGGL((k_route<DT, 8>), grid, block, 0, st, a, per);
+    if (a.experts <= 32) launch_scores<DT, 16, 2>(a, per, blocks, st);
+    else if (a.experts <= 64) launch_scores<DT, 16, 4>(a, per, blocks, st);
+    else if (a.experts <= 128) launch_scores<DT, 16, 8>(a, per, blocks, st);
+    else if (a.experts <= 192) launch_scores<DT, 16, 12>(a, per, blocks, st);
+    else if (a.experts <= 256) launch_scores<DT, 16, 16>(a, per, blocks, st);
+    else launch_scores<DT, 64, 8>(a, per, blocks, st);
 }
 
 }  // namespace
 
-int route_blocks(int64_t tokens) {
-    const int per = route_tokens(tokens);
-    return (int)((tokens + per - 1) / per);
+size_t route_space(int64_t tokens, int64_t experts) {
+    const int64_t per = route_tokens(tokens);
+    return (size_t)((tokens + per - 1) / per) * hist_pitch((int)experts) * 4;
 }
 
 void launch_route(const RouteArgs& a, int dt, hipStream_t st) {
     const int per = route_tokens(a.tokens);
-    const uint32_t blocks = (uint32_t)std::max(1, route_blocks(a.tokens));
-    if (a.tokens == 0) {  // no row: offsets alone
-    } else if (dt == kF32) launch_scores<kF32>(a, per, blocks, st);
-    else if (dt == kBF16) launch_scores<kBF16>(a, per, blocks, st);
-    else launch_scores<kF16>(a, per, blocks, st);
-    hipLaunchKernelGGL(k_route_sort, dim3(blocks), dim3(kThreads), 0, st, a, per);
+    const uint32_t blocks = (uint32_t)((a.tokens + per - 1) / per);
+    if (blocks > 0) {
+        if (dt == kF32) launch_scores<kF32>(a, per, blocks, st);
+        else if (dt == kBF16) launch_scores<kBF16>(a, per, blocks, st);
+        else launch_scores<kF16>(a, per, blocks, st);
+        if (blocks == 1) return;
+    }
+    hipLaunchKernelGGL(k_route_sort, dim3(std::max(1u, blocks)), dim3(kThreads), 0, st, a, per, hist_pitch(a.experts));
 }
 
 }  // namespace pdq
