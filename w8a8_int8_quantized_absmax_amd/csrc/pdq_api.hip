@@ -1125,6 +1125,7 @@ pdq_status pdq_route_experts(const void* logits, pdq_dtype dt, int64_t tokens, i
     if (!aligned(workspace, 256)) return PDQ_ERR_ALIGN;
     RouteArgs a{};
     a.logits = logits;
+    a.dt = dt;
     a.ldl = ldl;
     a.bias = bias;
     a.tokens = (int)tokens;
@@ -1141,7 +1142,7 @@ pdq_status pdq_route_experts(const void* logits, pdq_dtype dt, int64_t tokens, i
     a.offsets = offsets;
     a.rows = rows;
     a.hist = static_cast<int32_t*>(workspace);
-    launch_route(a, dt, static_cast<hipStream_t>(stream));
+    launch_route(a, static_cast<hipStream_t>(stream));
     return launched();
 }
 

@@ -306,6 +306,7 @@ void launch_fp8_experts(const Fp8ExpertsArgs& a, int out_dt, hipStream_t st);
 
 struct RouteArgs {
     const void* logits;
+    int dt;
     int64_t ldl;
     const float* bias;
     int tokens, experts, k;
@@ -319,6 +320,6 @@ struct RouteArgs {
     int32_t* hist;  // route_space(tokens, experts) bytes
 };
 size_t route_space(int64_t tokens, int64_t experts);
-void launch_route(const RouteArgs& a, int dt, hipStream_t st);
+void launch_route(const RouteArgs& a, hipStream_t st);
 
 }  // namespace pdq

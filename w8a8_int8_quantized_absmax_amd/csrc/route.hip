@@ -27,6 +27,13 @@ __device__ __forceinline__ uint64_t order_key(double v) {
     return u >> 63 ? ~u : u | (uint64_t(1) << 63);
 }
 
+// The same of binary32 values.
+__device__ __forceinline__ uint32_t order_key(float v) {
+    if (v != v) return 1;
+    const uint32_t u = __float_as_uint(v + 0.0f);
+    return u >> 31 ? ~u : u | 0x80000000u;
+}
+
 template <int kCtrl>
 __device__ __forceinline__ uint64_t dpp_u64(uint64_t v) {
     return (uint64_t)dpp_u32<kCtrl>((uint32_t)(v >> 32)) << 32 | dpp_u32<kCtrl>((uint32_t)v);
@@ -59,6 +66,16 @@ __device__ __forceinline__ uint64_t max_of(uint64_t v) {
 }
 
 template <int L>
+__device__ __forceinline__ uint32_t max_of(uint32_t v) {
+    v = row16_max(v);
+    if constexpr (L == 64) {
+        v = max(v, (uint32_t)__shfl_xor((int)v, 16));
+        v = max(v, (uint32_t)__shfl_xor((int)v, 32));
+    }
+    return v;
+}
+
+template <int L>
 __device__ __forceinline__ uint32_t min_of(uint32_t v) {
     v = min(v, dpp_u32<0xB1>(v));
     v = min(v, dpp_u32<0x4E>(v));
@@ -78,11 +95,11 @@ __device__ __forceinline__ bool any_of(bool v) {
     return L == 64 ? all != 0 : (all >> (threadIdx.x & 48) & 0xffff) != 0;
 }
 
-template <int DT>
-__device__ __forceinline__ float logit(const void* row, int e) {
-    if constexpr (DT == kF32) return static_cast<const float*>(row)[e];
-    else if constexpr (DT == kBF16) return bf16_to_f32(static_cast<const uint16_t*>(row)[e]);
-    else return f16_to_f32(static_cast<const uint16_t*>(row)[e]);
+__device__ __forceinline__ float logit(const RouteArgs& a, int64_t row, int e) {
+    const int64_t at = row + e;
+    if (a.dt == kF32) return static_cast<const float*>(a.logits)[at];
+    const uint32_t v = static_cast<const uint16_t*>(a.logits)[at];
+    return a.dt == kBF16 ? bf16_to_f32(v) : f16_to_f32(v);
 }
 
 // exp(x - top); infinite logits share a softmax's weight.
@@ -196,8 +213,8 @@ __device__ void sort_rows(const RouteArgs& a, const int* hist, int pitch, int bl
 }
 
 // L lanes a token, VPL experts a lane (lane + L j).  kAlone: the workgroup takes all tokens, and sorts
-// them too.
-template <int DT, int L, int VPL, bool kAlone>
+// them too.  Key: uint32_t where the logits order the experts, uint64_t where the biased scores do.
+template <typename Key, int L, int VPL, bool kAlone>
 __global__ __launch_bounds__(kThreads) void k_route(RouteArgs a, int per, int pitch) {
     constexpr int kTeams = kThreads / L, kSlots = L == 16 ? 2 : 1;  // at most 32 choices
     __shared__ __attribute__((aligned(16))) int hist[kMost];
@@ -213,16 +230,16 @@ __global__ __launch_bounds__(kThreads) void k_route(RouteArgs a, int per, int pi
     __syncthreads();
     const int t0 = blockIdx.x * per, t1 = min(t0 + per, a.tokens);
     const int size = a.experts / a.groups;
-    const bool every = a.bias || a.groups > 1;  // the scores of every expert take part in the choice
+    const bool every = sizeof(Key) == 8 || a.groups > 1;  // the scores of every expert take part in the choice
     for (int t = t0 + team; t < t1; t += kTeams) {
-        const char* row = static_cast<const char*>(a.logits) + t * a.ldl * Elem<DT>::bytes;
+        const int64_t row = t * a.ldl;
         float x[VPL];
         bool nan = false;
         float top = -INFINITY;
 #pragma unroll
         for (int j = 0; j < VPL; ++j) {
             const int e = r + L * j;
-            x[j] = e < a.experts ? logit<DT>(row, e) : -INFINITY;
+            x[j] = e < a.experts ? logit(a, row, e) : -INFINITY;
         }
 #pragma unroll
         for (int j = 0; j < VPL; ++j) {
@@ -238,7 +255,7 @@ __global__ __launch_bounds__(kThreads) void k_route(RouteArgs a, int per, int pi
             top = fmaxf(top, __shfl_xor(top, 16));
             top = fmaxf(top, __shfl_xor(top, 32));
         }
-        uint64_t key[VPL];
+        Key key[VPL];
         double sum = 1.0;
         if (every || (!a.sigmoid && !a.renormalize)) {
             double p[VPL];
@@ -261,13 +278,18 @@ __global__ __launch_bounds__(kThreads) void k_route(RouteArgs a, int per, int pi
 #pragma unroll
             for (int j = 0; j < VPL; ++j) {
                 const int e = r + L * j;
-                const double c = a.bias && e < a.experts ? p[j] + (double)a.bias[e] : (double)x[j];
-                key[j] = x[j] == -INFINITY || c == -INFINITY ? 0 : order_key(c);
-                if (a.groups > 1) space.scores[team][e] = key[j] < 2 ? -INFINITY : a.bias ? c : p[j];
+                double c = p[j];
+                if constexpr (sizeof(Key) == 8) {
+                    if (e < a.experts) c += (double)a.bias[e];
+                    key[j] = x[j] == -INFINITY || c == -INFINITY ? 0 : order_key(c);
+                } else {
+                    key[j] = x[j] == -INFINITY ? 0 : order_key(x[j]);
+                }
+                if (a.groups > 1) space.scores[team][e] = key[j] < 2 ? -INFINITY : c;
             }
         } else {
 #pragma unroll
-            for (int j = 0; j < VPL; ++j) key[j] = x[j] == -INFINITY ? 0 : order_key((double)x[j]);
+            for (int j = 0; j < VPL; ++j) key[j] = x[j] == -INFINITY ? 0 : order_key(x[j]);
         }
         if (a.groups > 1) {  // lane i's groups: i, i + L, ..; at most 64
             __builtin_amdgcn_fence(__ATOMIC_SEQ_CST, "workgroup");
@@ -313,9 +335,9 @@ __global__ __launch_bounds__(kThreads) void k_route(RouteArgs a, int per, int pi
 #pragma unroll
         for (int q = 0; q < kSlots; ++q) id[q] = -1;
         for (int s = 0; s < a.k; ++s) {
-            uint64_t best = key[0];
+            Key best = key[0];
 #pragma unroll
-            for (int j = 1; j < VPL; ++j) best = key[j] > best ? key[j] : best;
+            for (int j = 1; j < VPL; ++j) best = max(key[j], best);
             best = max_of<L>(best);
             if (best == 0) break;  // (the same in a token's lanes)
             uint32_t at = 0xffffffffu;
@@ -335,7 +357,7 @@ __global__ __launch_bounds__(kThreads) void k_route(RouteArgs a, int per, int pi
         for (int q = 0; q < kSlots; ++q) {
             p[q] = 0.0;
             if (id[q] >= 0) {
-                const float v = logit<DT>(row, id[q]);
+                const float v = logit(a, row, id[q]);
                 p[q] = a.sigmoid ? sigmoid(v) : shifted_exp(v, top);
             }
             total += p[q];
@@ -374,21 +396,17 @@ int route_tokens(int64_t tokens) { return tokens <= 64 ? 64 : (int)std::max<int6
 
 int hist_pitch(int experts) { return (experts + 3) / 4 * 4; }
 
-template <int DT, int L, int VPL>
+template <int L, int VPL>
 void launch_scores(const RouteArgs& a, int per, uint32_t blocks, hipStream_t st) {
     const int pitch = hist_pitch(a.experts);
-    if (blocks == 1) hipLaunchKernelGGL((k_route<DT, L, VPL, true>), dim3(1), dim3(kThreads), 0, st, a, per, pitch);
-    else hipLaunchKernelGGL((k_route<DT, L, VPL, false>), dim3(blocks), dim3(kThreads), 0, st, a, per, pitch);
-}
-
-template <int DT>
-void launch_scores(const RouteArgs& a, int per, uint32_t blocks, hipStream_t st) {
-    if (a.experts <= 32) launch_scores<DT, 16, 2>(a, per, blocks, st);
-    else if (a.experts <= 64) launch_scores<DT, 16, 4>(a, per, blocks, st);
-    else if (a.experts <= 128) launch_scores<DT, 16, 8>(a, per, blocks, st);
-    else if (a.experts <= 192) launch_scores<DT, 16, 12>(a, per, blocks, st);
-    else if (a.experts <= 256) launch_scores<DT, 16, 16>(a, per, blocks, st);
-    else launch_scores<DT, 64, 8>(a, per, blocks, st);
+    const dim3 grid(blocks), block(kThreads);
+    if (blocks == 1) {
+        if (a.bias) hipLaunchKernelGGL((k_route<uint64_t, L, VPL, true>), grid, block, 0, st, a, per, pitch);
+        else hipLaunchKernelGGL((k_route<uint32_t, L, VPL, true>), grid, block, 0, st, a, per, pitch);
+    } else {
+        if (a.bias) hipLaunchKernelGGL((k_route<uint64_t, L, VPL, false>), grid, block, 0, st, a, per, pitch);
+        else hipLaunchKernelGGL((k_route<uint32_t, L, VPL, false>), grid, block, 0, st, a, per, pitch);
+    }
 }
 
 }  // namespace
@@ -398,13 +416,16 @@ size_t route_space(int64_t tokens, int64_t experts) {
     return (size_t)((tokens + per - 1) / per) * hist_pitch((int)experts) * 4;
 }
 
-void launch_route(const RouteArgs& a, int dt, hipStream_t st) {
+void launch_route(const RouteArgs& a, hipStream_t st) {
     const int per = route_tokens(a.tokens);
     const uint32_t blocks = (uint32_t)((a.tokens + per - 1) / per);
     if (blocks > 0) {
-        if (dt == kF32) launch_scores<kF32>(a, per, blocks, st);
-        else if (dt == kBF16) launch_scores<kBF16>(a, per, blocks, st);
-        else launch_scores<kF16>(a, per, blocks, st);
+        if (a.experts <= 32) launch_scores<16, 2>(a, per, blocks, st);
+        else if (a.experts <= 64) launch_scores<16, 4>(a, per, blocks, st);
+        else if (a.experts <= 128) launch_scores<16, 8>(a, per, blocks, st);
+        else if (a.experts <= 192) launch_scores<16, 12>(a, per, blocks, st);
+        else if (a.experts <= 256) launch_scores<16, 16>(a, per, blocks, st);
+        else launch_scores<64, 8>(a, per, blocks, st);
         if (blocks == 1) return;
     }
     hipLaunchKernelGGL(k_route_sort, dim3(std::max(1u, blocks)), dim3(kThreads), 0, st, a, per, hist_pitch(a.experts));

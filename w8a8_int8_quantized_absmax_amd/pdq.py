@@ -1064,7 +1064,7 @@ class Routing:
     [tokens, k]; the rows token * k + slot sorted by expert: offsets int32 [experts + 1], rows int32
     [tokens * k]."""
 
-    __slots__ = ("_tensors", "_buffer", "tokens", "experts", "k", "index", "_c", "_ref")
+    __slots__ = ("_tensors", "_buffer", "tokens", "experts", "k", "index", "_at", "_c")
 
     def __init__(self, ids: torch.Tensor, weights: torch.Tensor, offsets: torch.Tensor, rows: torch.Tensor):
         if ids.dim() != 2 or offsets.dim() != 1 or offsets.shape[0] < 2:
@@ -1078,13 +1078,17 @@ class Routing:
             raise ValueError("the routing's tensors must be on one device")
         self._tensors, self._buffer = (ids, weights, offsets, rows), None
         self.tokens, self.experts, self.k, self.index = tokens, offsets.shape[0] - 1, k, ids.get_device()
-        self._c = _RoutingC(*(t.data_ptr() for t in self._tensors), tokens, self.experts, k)
-        self._ref = ctypes.byref(self._c)
+        self._at, self._c = tuple(t.data_ptr() for t in self._tensors), None
+
+    def _ref(self):
+        if self._c is None:
+            self._c = _RoutingC(*self._at, self.tokens, self.experts, self.k)
+        return ctypes.byref(self._c)
 
     def _all(self):
         if self._tensors is None:  # parts of route_experts' one buffer, as tensors when they are asked for
             n, e = self.tokens * self.k, self.experts + 1
-            ids, weights, rows, offsets = self._buffer[:3 * n + e].split((n, n, n, e))
+            ids, weights, rows, offsets, _ = self._buffer.split((n, n, n, e, self._buffer.shape[0] - 3 * n - e))
             self._tensors = (ids.view(self.tokens, self.k), weights.view(torch.float32).view(self.tokens, self.k),
                              offsets, rows)
         return self._tensors
@@ -1154,8 +1158,7 @@ def route_experts(logits, k: int, score: str = "softmax", bias=None, groups: int
              bias.data_ptr() if bias is not None else None, rule[1], at, at + 4 * n, offsets, at + 8 * n, ws, size)
     r = Routing.__new__(Routing)
     r._tensors, r._buffer, r.tokens, r.experts, r.k, r.index = None, buffer, tokens, experts, k, index
-    r._c = _RoutingC(at, at + 4 * n, offsets, at + 8 * n, tokens, experts, k)
-    r._ref = ctypes.byref(r._c)
+    r._at, r._c = (at, at + 4 * n, offsets, at + 8 * n), None
     return r
 
 
@@ -1203,6 +1206,6 @@ def experts_fp8(x, routing: Routing, gate_up: WeightFP8, down: WeightFP8, out=No
     size = experts_fp8_workspace_bytes(tokens, routing.k, experts, hidden, inner)
     workspace, size = _workspace(workspace, size, x, index)
     c = _ExpertsC(gate_up.at, gate_up.scale_at, down.at, down.scale_at, gate_up.scale_type, experts, hidden, inner)
-    _kv_call("pdq_experts_fp8", index, x.data_ptr(), _DT[x.dtype], _ld(x), routing._ref, ctypes.byref(c), y.data_ptr(),
+    _kv_call("pdq_experts_fp8", index, x.data_ptr(), _DT[x.dtype], _ld(x), routing._ref(), ctypes.byref(c), y.data_ptr(),
              _ld(y), workspace.data_ptr() if size else None, size)
     return {"y": y}
