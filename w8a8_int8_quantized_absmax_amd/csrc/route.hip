@@ -390,8 +390,9 @@ __global__ __launch_bounds__(kThreads) void k_route_sort(RouteArgs a, int per, i
 }
 
 // Tokens of a workgroup: 32 (16 lanes each), or as many as leave at most 256 workgroups, each of which
-// reads every other's counts.  Up to 64 tokens one workgroup does it all: its second round of
-// tokens takes less than another launch.
+// reads every other's counts (with 512 of half the size: 8192 x 256 40.7 us against 30.2, 16384 x 64
+// 18.6 / 15.8).  Up to 64 tokens one workgroup does it all: at 64 that takes 9.4 us where two launches
+// take 8.3, but the host 2.7 us less.
 int route_tokens(int64_t tokens) { return tokens <= 64 ? 64 : (int)std::max<int64_t>(32, (tokens + 255) / 256); }
 
 int hist_pitch(int experts) { return (experts + 3) / 4 * 4; }
