@@ -9,6 +9,8 @@ namespace pdq {
 
 namespace {
 
+constexpr int kDirect = 8, kDirectValues = 32768;  // rows; values that a workgroup codes
+
 template <bool F32S>
 struct BlockScale {
     float f;
@@ -34,6 +36,141 @@ __device__ __forceinline__ v4f mac16(v8i w, v8i x, v4f c, BlockScale<F32S> s, ui
         return fp8_mfma16(w, x, c, s.b, sx);
     }
 }
+
+// ---- a token or two: no more than kDirect rows, taken as they are ----
+//
+// Bound by reading the chosen experts' weights; two launches, no sorting and nothing in between but
+// h, in binary32.  Both kernels code what they multiply (a row of x; the rows of h of a token) into
+// LDS while their first weights are on their way.
+
+// h of one row (a token at one of its experts) and 16 inner channels a workgroup; its four
+// wavefronts take the groups of the hidden channels in turn.
+template <bool F32S, int DT>
+__global__ __launch_bounds__(256) void k_fp8_gate_up_direct(Fp8ExpertsArgs a) {
+    __shared__ __attribute__((aligned(16))) uint8_t codes[kDirectValues], scales[kDirectValues / kGroup];
+    __shared__ v4f red[2][4][4];
+    const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int flat = blockIdx.y, expert = a.ids[flat];
+    if ((uint32_t)expert >= (uint32_t)a.sorted.experts) return;
+    const int G = (int)fp8_groups(a.hidden), IG = (int)fp8_groups(a.inner), ngroups = a.inner / 16;
+    const int64_t pitch = fp8_scale_pitch(a.hidden);
+    const uint8_t* wp[2];
+    int64_t srow[2];
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+        const int64_t mat = 2 * (int64_t)expert + i;
+        wp[i] = a.gate_up + (mat * ngroups + blockIdx.x) * G * kGroupBytes;
+        srow[i] = (mat * IG + blockIdx.x / 8) * pitch;
+    }
+    constexpr int U = 4;
+    v8i w[2][U][2];  // [set][group][gate, up]
+    BlockScale<F32S> s[2][U][2];
+    auto load = [&](int set, int g0) {
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            const int g = min(g0 + 4 * u, G - 1);
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+                w[set][u][i] = fp8_fragment(wp[i] + (int64_t)g * kGroupBytes, lane);
+                s[set][u][i] = block_scale<F32S>(a.gate_up_s, srow[i] + g);
+            }
+        }
+    };
+    load(0, wave);
+    fp8_code_rows<DT>(static_cast<const char*>(a.raw) + flat / a.sorted.k * a.ldx * 2, 0, 1, a.hidden, codes, scales, 0);
+    __syncthreads();
+    v4f acc[2] = {v4f{}, v4f{}};
+    auto add = [&](int set, int g0) {
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            const int g = g0 + 4 * u;
+            if (g >= G) break;
+            const v8i x = fp8_row_fragment(codes, g, lane);
+            const uint32_t sx = scales[g];
+#pragma unroll
+            for (int i = 0; i < 2; ++i) acc[i] = mac16<F32S>(w[set][u][i], x, acc[i], s[set][u][i], sx);
+        }
+    };
+    for (int g = wave; g < G; g += 8 * U) {
+        load(1, g + 4 * U);
+        add(0, g);
+        load(0, g + 8 * U);
+        add(1, g + 4 * U);
+    }
+    // every column of the product is the row: the first one's four lanes
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+        fp8_settle(acc[i]);
+        if ((lane & 15) == 0) red[i][wave][lane >> 4] = acc[i];
+    }
+    __syncthreads();
+    if (threadIdx.x < 4) {
+        v4f v[2];
+#pragma unroll
+        for (int i = 0; i < 2; ++i)
+            v[i] = red[i][0][threadIdx.x] + red[i][1][threadIdx.x] + red[i][2][threadIdx.x] + red[i][3][threadIdx.x];
+        v4f h;
+#pragma unroll
+        for (int r = 0; r < 4; ++r) h[r] = fp8_silu_mul(v[0][r], v[1][r]);
+        *reinterpret_cast<v4f*>(a.partial + (int64_t)flat * a.inner + blockIdx.x * 16 + threadIdx.x * 4) = h;
+    }
+}
+
+// y of one token and 16 hidden channels a workgroup: its rows of h one after the other, the groups
+// of each dealt to the wavefronts.
+template <bool F32S, int OUT>
+__global__ __launch_bounds__(256) void k_fp8_down_direct(Fp8ExpertsArgs a) {
+    __shared__ __attribute__((aligned(16))) uint8_t codes[kDirectValues], scales[kDirectValues / kGroup];
+    __shared__ v4f red[4][4];
+    const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int k = a.sorted.k, token = blockIdx.y;
+    const int G = (int)fp8_groups(a.inner), HG = (int)fp8_groups(a.hidden), ngroups = a.hidden / 16;
+    const int64_t pitch = fp8_scale_pitch(a.inner);
+    const int steps = k * G;  // (slot, group) pairs, taken in turn
+    constexpr int U = 8;
+    v8i w[U];
+    BlockScale<F32S> s[U];
+    float weight[U];
+    auto load = [&](int p0) {
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            const int p = min(p0 + 4 * u, steps - 1), j = p / G, g = p - j * G;
+            const int expert = a.ids[token * k + j];
+            const bool there = p0 + 4 * u < steps && (uint32_t)expert < (uint32_t)a.sorted.experts;
+            const int64_t e = there ? expert : 0;
+            w[u] = fp8_fragment(a.down + ((e * ngroups + blockIdx.x) * G + g) * kGroupBytes, lane);
+            s[u] = block_scale<F32S>(a.down_s, (e * HG + blockIdx.x / 8) * pitch + g);
+            weight[u] = there ? a.weights[token * k + j] : 0.0f;
+        }
+    };
+    load(wave);
+    fp8_code_rows<kF32>(a.partial + (int64_t)token * k * a.inner, a.inner, k, a.inner, codes, scales, G * kGroup);
+    __syncthreads();
+    v4f y = v4f{};
+    for (int p0 = wave; p0 < steps; p0 += 4 * U) {
+        if (p0 != wave) load(p0);
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            const int p = p0 + 4 * u;
+            if (p >= steps) break;
+            const int j = p / G, g = p - j * G;
+            if ((uint32_t)a.ids[token * k + j] >= (uint32_t)a.sorted.experts) continue;  // (its h is not there)
+            v4f v = mac16<F32S>(w[u], fp8_row_fragment(codes + j * G * kGroup, g, lane), v4f{}, s[u], scales[p]);
+            fp8_settle(v);
+#pragma unroll
+            for (int r = 0; r < 4; ++r) y[r] = __fmaf_rn(v[r], weight[u], y[r]);
+        }
+    }
+    if ((lane & 15) == 0) red[wave][lane >> 4] = y;
+    __syncthreads();
+    if (threadIdx.x < 4) {
+        const v4f v = red[0][threadIdx.x] + red[1][threadIdx.x] + red[2][threadIdx.x] + red[3][threadIdx.x];
+        *reinterpret_cast<uint2*>(static_cast<uint16_t*>(a.y) + token * a.ldy + blockIdx.x * 16 + threadIdx.x * 4) =
+            make_uint2(f32x2_to_16<OUT>(v[0], v[1]), f32x2_to_16<OUT>(v[2], v[3]));
+    }
+}
+
+// ---- blocks of 16 sorted rows ----
 
 // One block of 16 rows and 128 inner channels a workgroup; wavefront w computes
 // gate and up of the channels 32 w .. 32 w + 31.
@@ -149,9 +286,12 @@ __global__ __launch_bounds__(256) void k_fp8_combine(Fp8ExpertsArgs a) {
 template <bool F32S>
 void launch_products(const Fp8ExpertsArgs& a, hipStream_t st) {
     // Rows of a tile by the average rows of an expert: a tile that is not full costs as much as a
-    // full one.  Below 24 one block of 16 rows at a time.
+    // full one.  Below 12 one block of 16 rows at a time.  Measured (us, blocks of 16 / tiles of 64 / 128 /
+    // 256), 4 of 32 experts of 4096 x 1360, average rows 8: 129 / 131 / 138 / 163, 16: 154 / 137 / 146 / 171,
+    // 32: 221 / 154 / 156 / 177, 64: 389 / 189 / 175 / 194, 191: 818 / 294 / 242 / 244, 512: 1617 / 631 / 511 / 451;
+    // 2 of 8 of 4096 x 14336, 128: 1684 / 522 / 370 / 410, 256: 2768 / 769 / 644 / 504.
     const int64_t each = a.sorted.total / a.sorted.experts;
-    const int rows = each >= 200 ? (F32S ? 192 : 256) : each >= 64 ? 128 : each >= 24 ? 64 : 0;
+    const int rows = each >= 200 ? (F32S ? 192 : 256) : each >= 48 ? 128 : each >= 12 ? 64 : 0;
     if (rows > 0) {
         Fp8TileArgs t{};
         t.x = a.x;
@@ -185,7 +325,28 @@ void launch_products(const Fp8ExpertsArgs& a, hipStream_t st) {
     hipLaunchKernelGGL((k_fp8_down<F32S>), dim3(blocks, (a.hidden + 63) / 64), dim3(256), 0, st, a);
 }
 
+template <bool F32S>
+void launch_direct(const Fp8ExpertsArgs& a, int dt, hipStream_t st) {
+    const dim3 up(a.inner / 16, a.sorted.total), down(a.hidden / 16, (uint32_t)a.tokens), block(256);
+    if (dt == kF16) {
+        hipLaunchKernelGGL((k_fp8_gate_up_direct<F32S, kF16>), up, block, 0, st, a);
+        hipLaunchKernelGGL((k_fp8_down_direct<F32S, kF16>), down, block, 0, st, a);
+    } else {
+        hipLaunchKernelGGL((k_fp8_gate_up_direct<F32S, kBF16>), up, block, 0, st, a);
+        hipLaunchKernelGGL((k_fp8_down_direct<F32S, kBF16>), down, block, 0, st, a);
+    }
+}
+
 }  // namespace
+
+bool fp8_experts_direct(int64_t rows, int64_t k, int64_t hidden, int64_t inner) {
+    return rows <= kDirect && fp8_groups(hidden) * kGroup <= kDirectValues && k * fp8_groups(inner) * kGroup <= kDirectValues;
+}
+
+void launch_fp8_experts_direct(const Fp8ExpertsArgs& a, int dt, hipStream_t st) {
+    if (a.ws_f32) launch_direct<true>(a, dt, st);
+    else launch_direct<false>(a, dt, st);
+}
 
 void launch_fp8_experts(const Fp8ExpertsArgs& a, int out_dt, hipStream_t st) {
     if (a.ws_f32) launch_products<true>(a, st);

@@ -84,6 +84,52 @@ __device__ __forceinline__ v4f fp8_mfma16(v8i w, v8i x, v4f c, int sw, int sx) {
     return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(w, x, c, 0, 0, 0, sw, 0, sx);
 }
 
+// A few rows' codes and scales, by the whole workgroup into LDS: rows of `pitch` bytes (K padded to whole
+// groups, and 16 bytes so that 16 rows' chunks lie in different banks), and a scale byte a group.
+template <int DT>
+__device__ __forceinline__ void fp8_code_rows(const void* x, int64_t ldx, int rows, int K, uint8_t* codes, uint8_t* scales,
+                                              int pitch) {
+    const int groups = (int)fp8_groups(K), c8 = threadIdx.x & 15, pieces = rows * groups, each = blockDim.x >> 4;
+    constexpr int U = 4;  // loads sent together
+    for (int p0 = threadIdx.x >> 4; p0 < (pieces + each - 1) / each * each; p0 += U * each) {  // a row's group by 16 lanes
+        Raw8<DT> raw[U];
+        int m[U], g[U];
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            const int p = p0 + u * each;
+            m[u] = min(p / groups, rows - 1);
+            g[u] = p - p / groups * groups;
+            const int k = g[u] * kGroup + c8 * 8;
+            raw[u] = p < pieces && k < K ? load_raw8<DT>(static_cast<const char*>(x) + m[u] * ldx * Elem<DT>::bytes, k / 8)
+                                         : zero_raw8<DT>();
+        }
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            if (p0 + u * each >= pieces) break;  // (the same in the 16 lanes)
+            float v[8];
+            widen8<DT>(raw[u], v);
+            uint32_t top = 0;
+#pragma unroll
+            for (int j = 0; j < 8; ++j) top = max(top, magnitude(v[j]));
+            const uint32_t b = fp8_scale_byte(row16_max(top));
+            const float inv = fp8_inverse(b);
+#pragma unroll
+            for (int j = 0; j < 8; ++j) v[j] = fp8_scaled(v[j], inv);
+            *reinterpret_cast<uint2*>(codes + m[u] * pitch + g[u] * kGroup + c8 * 8) =
+                make_uint2(fp8_pack4(v[0], v[1], v[2], v[3]), fp8_pack4(v[4], v[5], v[6], v[7]));
+            if (c8 == 0) scales[m[u] * groups + g[u]] = (uint8_t)b;
+        }
+    }
+}
+
+// A lane's fragment of a row coded there: any row, the chunk lane / 16 of each half of the group.
+__device__ __forceinline__ v8i fp8_row_fragment(const uint8_t* row, int g, int lane) {
+    const uint8_t* p = row + g * kGroup + (lane >> 4) * 16;
+    const v4i lo = *reinterpret_cast<const v4i*>(p);
+    const v4i hi = *reinterpret_cast<const v4i*>(p + kGroup / 2);
+    return v8i{lo[0], lo[1], lo[2], lo[3], hi[0], hi[1], hi[2], hi[3]};
+}
+
 // A product's result, for every lane, here: the compiler may otherwise move the
 // instruction into a branch that only some lanes take, and with it the writes of
 // its scale operands, which the lanes outside then lack.

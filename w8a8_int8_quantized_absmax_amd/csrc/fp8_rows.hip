@@ -29,33 +29,6 @@ struct Step {  // one group's operands
     uint32_t swb;  // else
 };
 
-// The rows' codes and scales in LDS: rows of `pitch` bytes, padded by 16 so that 16 rows' chunks lie in
-// 16 different banks' quads, then a row of scale bytes each.
-template <int DT>
-__device__ __forceinline__ void quantize_rows(const Fp8GemmArgs& a, uint8_t* codes, uint8_t* scales, int pitch) {
-    const int c8 = threadIdx.x & 15, pieces = a.M * a.groups;
-    const int each = blockDim.x >> 4;
-    for (int p = threadIdx.x >> 4; p < (pieces + each - 1) / each * each; p += each) {  // a row's group by 16 lanes
-        const int m = min(p / a.groups, a.M - 1), g = p - p / a.groups * a.groups, k = g * kGroup + c8 * 8;
-        const Raw8<DT> raw = p < pieces && k < a.K
-                                 ? load_raw8<DT>(static_cast<const char*>(a.raw) + m * a.ldx * Elem<DT>::bytes, k / 8)
-                                 : zero_raw8<DT>();
-        float v[8];
-        widen8<DT>(raw, v);
-        uint32_t top = 0;
-#pragma unroll
-        for (int j = 0; j < 8; ++j) top = max(top, magnitude(v[j]));
-        const uint32_t b = fp8_scale_byte(row16_max(top));
-        const float inv = fp8_inverse(b);
-        if (p >= pieces) continue;
-#pragma unroll
-        for (int j = 0; j < 8; ++j) v[j] = fp8_scaled(v[j], inv);
-        *reinterpret_cast<uint2*>(codes + m * pitch + k) =
-            make_uint2(fp8_pack4(v[0], v[1], v[2], v[3]), fp8_pack4(v[4], v[5], v[6], v[7]));
-        if (c8 == 0) scales[m * a.groups + g] = (uint8_t)b;
-    }
-}
-
 template <int NG, int MB, bool F32S, int OUT, bool FUSED, int W>
 __global__ __launch_bounds__(64 * W) void k_fp8_rows(Fp8GemmArgs a) {
     __shared__ v4f red[W][NG * MB][64];
@@ -131,9 +104,9 @@ __global__ __launch_bounds__(64 * W) void k_fp8_rows(Fp8GemmArgs a) {
 #pragma unroll
     for (int u = 0; u < U; ++u) load(cur[u], wave + W * u);
     if constexpr (FUSED) {
-        if (a.raw_dt == kF32) quantize_rows<kF32>(a, fused, scales, pitch);
-        else if (a.raw_dt == kBF16) quantize_rows<kBF16>(a, fused, scales, pitch);
-        else quantize_rows<kF16>(a, fused, scales, pitch);
+        if (a.raw_dt == kF32) fp8_code_rows<kF32>(a.raw, a.ldx, a.M, a.K, fused, scales, pitch);
+        else if (a.raw_dt == kBF16) fp8_code_rows<kBF16>(a.raw, a.ldx, a.M, a.K, fused, scales, pitch);
+        else fp8_code_rows<kF16>(a.raw, a.ldx, a.M, a.K, fused, scales, pitch);
         __syncthreads();
     }
     for (int g = wave; g < G; g += W * U) {

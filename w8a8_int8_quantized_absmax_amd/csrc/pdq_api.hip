@@ -961,6 +961,8 @@ struct ExpertsSpace {
     size_t all() const { return x + xs + h + hs + partial; }
 };
 ExpertsSpace experts_space(int64_t tokens, int64_t k, int64_t experts, int64_t hidden, int64_t inner) {
+    if (fp8_experts_direct(tokens * k, k, hidden, inner))  // h alone
+        return ExpertsSpace{0, 0, 0, 0, align256((size_t)(tokens * k * inner * 4))};
     const int64_t rows = 16 * fp8_blocks(tokens * k, experts);
     return ExpertsSpace{align256((size_t)(rows * fp8_groups(hidden) * kGroup)), align256((size_t)(rows * fp8_scale_pitch(hidden))),
                         align256((size_t)(rows * fp8_groups(inner) * kGroup)), align256((size_t)(rows * fp8_scale_pitch(inner))),
@@ -1205,6 +1207,12 @@ pdq_status pdq_experts_fp8(const void* x, pdq_dtype dt, int64_t ldx, const pdq_r
     a.y = y;
     a.ldy = ldy;
     a.tokens = tokens;
+    a.raw = x;
+    a.ldx = ldx;
+    if (fp8_experts_direct(tokens * k, k, H, I)) {
+        launch_fp8_experts_direct(a, dt, static_cast<hipStream_t>(stream));
+        return launched();
+    }
     launch_fp8_quant(q, dt, blocks, static_cast<hipStream_t>(stream));
     launch_fp8_experts(a, dt, static_cast<hipStream_t>(stream));
     return launched();

@@ -272,9 +272,11 @@ struct Fp8ExpertsArgs {
     uint8_t* hs;
     const int32_t* ids;
     const float* weights;
-    float* partial;  // [total, hidden]
+    float* partial;  // [total, hidden]; direct: h, [total, inner]
     void* y;
     int64_t ldy, tokens;
+    const void* raw;  // direct: x, pitch ldx
+    int64_t ldx;
 };
 // The tiled products, gemm_fp8.hip: dense, or (sorted) of the experts' layer.
 struct Fp8TileArgs {
@@ -303,6 +305,9 @@ inline int64_t fp8_blocks(int64_t total, int64_t experts) {
     return (total + 15 * (total < experts ? total : experts)) / 16;
 }
 void launch_fp8_experts(const Fp8ExpertsArgs& a, int out_dt, hipStream_t st);
+// A few rows, without sorting: gate and up, then down and the sum.
+bool fp8_experts_direct(int64_t rows, int64_t k, int64_t hidden, int64_t inner);
+void launch_fp8_experts_direct(const Fp8ExpertsArgs& a, int dt, hipStream_t st);
 
 struct RouteArgs {
     const void* logits;
