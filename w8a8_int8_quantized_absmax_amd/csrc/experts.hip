@@ -37,6 +37,17 @@ __device__ __forceinline__ v4f mac16(v8i w, v8i x, v4f c, BlockScale<F32S> s, ui
     }
 }
 
+// What gate and up are made of in the kernels that the weight's bytes bound: a difference of their last
+// bits moves some of h's codes, by a step each, so that every bit of the sum counts.
+template <bool F32S>
+__device__ __forceinline__ v4f mac16_wide(v8i w, const Fp8Wide& x, v4f c, BlockScale<F32S> s, float sx) {
+    const v4f p = fp8_mfma16_wide(fp8_widen(w), x);
+    const float both = __fmul_rn(sx, F32S ? s.f : fp8_scale_value(s.b));
+#pragma unroll
+    for (int r = 0; r < 4; ++r) c[r] = __fmaf_rn(p[r], both, c[r]);
+    return c;
+}
+
 // ---- a token or two: no more than kDirect rows, taken as they are ----
 //
 // Bound by reading the chosen experts' weights; two launches, no sorting and nothing in between but
@@ -85,10 +96,10 @@ __global__ __launch_bounds__(256) void k_fp8_gate_up_direct(Fp8ExpertsArgs a) {
         for (int u = 0; u < U; ++u) {
             const int g = g0 + 4 * u;
             if (g >= G) break;
-            const v8i x = fp8_row_fragment(codes, g, lane);
-            const uint32_t sx = scales[g];
+            const Fp8Wide x = fp8_widen(fp8_row_fragment(codes, g, lane));
+            const float sx = fp8_scale_value(scales[g]);
 #pragma unroll
-            for (int i = 0; i < 2; ++i) acc[i] = mac16<F32S>(w[set][u][i], x, acc[i], s[set][u][i], sx);
+            for (int i = 0; i < 2; ++i) acc[i] = mac16_wide<F32S>(w[set][u][i], x, acc[i], s[set][u][i], sx);
         }
     };
     for (int g = wave; g < G; g += 8 * U) {
@@ -198,14 +209,14 @@ __global__ __launch_bounds__(256) void k_fp8_gate_up(Fp8ExpertsArgs a) {
         }
     }
     for (int g = 0; g < G; ++g) {
-        const v8i x = fp8_fragment(xb + (int64_t)g * kGroupBytes, lane);
-        const uint32_t sx = xs[g];
+        const Fp8Wide x = fp8_widen(fp8_fragment(xb + (int64_t)g * kGroupBytes, lane));
+        const float sx = fp8_scale_value(xs[g]);
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
             const BlockScale<F32S> s = block_scale<F32S>(a.gate_up_s, srow[i] + g);
 #pragma unroll
             for (int j = 0; j < 2; ++j)
-                acc[i][j] = mac16<F32S>(fp8_fragment(wp[i][j] + (int64_t)g * kGroupBytes, lane), x, acc[i][j], s, sx);
+                acc[i][j] = mac16_wide<F32S>(fp8_fragment(wp[i][j] + (int64_t)g * kGroupBytes, lane), x, acc[i][j], s, sx);
         }
     }
 #pragma unroll
@@ -252,16 +263,39 @@ __global__ __launch_bounds__(256) void k_fp8_down(Fp8ExpertsArgs a) {
     const uint8_t* xs = a.hs + ((int64_t)blockIdx.x * 16 + (lane & 15)) * pitch;
     const uint8_t* wp = a.down + ((int64_t)t.expert * ngroups + n16) * G * kGroupBytes;
     const int64_t srow = ((int64_t)t.expert * fp8_groups(a.hidden) + n16 / 8) * pitch;
+    constexpr int U = 4;  // groups loaded together, two sets of them on their way
+    v8i w[2][U], x[2][U];
+    BlockScale<F32S> s[2][U];
+    uint32_t sx[2][U];
+    auto load = [&](int set, int g0) {
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            const int g = min(g0 + u, G - 1);
+            w[set][u] = fp8_fragment(wp + (int64_t)g * kGroupBytes, lane);
+            x[set][u] = fp8_fragment(xb + (int64_t)g * kGroupBytes, lane);
+            s[set][u] = block_scale<F32S>(a.down_s, srow + g);
+            sx[set][u] = xs[g];
+        }
+    };
     v4f acc = v4f{};
-    for (int g = 0; g < G; ++g)
-        acc = mac16<F32S>(fp8_fragment(wp + (int64_t)g * kGroupBytes, lane), fp8_fragment(xb + (int64_t)g * kGroupBytes, lane),
-                          acc, block_scale<F32S>(a.down_s, srow + g), xs[g]);
+    auto add = [&](int set, int g0) {
+#pragma unroll
+        for (int u = 0; u < U; ++u)
+            if (g0 + u < G) acc = mac16<F32S>(w[set][u], x[set][u], acc, s[set][u], sx[set][u]);
+    };
+    load(0, 0);
+    for (int g = 0; g < G; g += 2 * U) {
+        load(1, g + U);
+        add(0, g);
+        load(0, g + 2 * U);
+        add(1, g + U);
+    }
     fp8_settle(acc);
     const int flat = fp8_sorted_row(a.sorted, t, lane & 15);
     if (flat < 0) return;
-    const float w = a.weights[flat];
+    const float weight = a.weights[flat];
 #pragma unroll
-    for (int r = 0; r < 4; ++r) acc[r] = __fmul_rn(acc[r], w);
+    for (int r = 0; r < 4; ++r) acc[r] = __fmul_rn(acc[r], weight);
     *reinterpret_cast<v4f*>(a.partial + (int64_t)flat * a.hidden + n16 * 16 + 4 * (lane >> 4)) = acc;
 }
 

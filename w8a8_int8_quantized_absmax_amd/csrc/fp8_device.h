@@ -84,6 +84,41 @@ __device__ __forceinline__ v4f fp8_mfma16(v8i w, v8i x, v4f c, int sw, int sx) {
     return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(w, x, c, 0, 0, 0, sw, 0, sx);
 }
 
+// The same product on 16-bit operands, with every product whole and the sum binary32: the codes are
+// widened (exactly, v_cvt_scalef32_pk_bf16_fp8), and the group's scale multiplies the sum.  The FP8
+// products align eight products to the largest of their exponents and keep 13 bits behind it, some 2^-15
+// of a sum; this one is off by some 2^-25.  At a fourth of the rate: where reading the weight is what
+// takes the time.
+struct Fp8Wide {
+    v8bf v[4];
+};
+__device__ __forceinline__ Fp8Wide fp8_widen(v8i f) {
+    Fp8Wide w;
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+            const auto lo = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8((unsigned)f[2 * i + j], 1.0f, false);
+            const auto hi = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8((unsigned)f[2 * i + j], 1.0f, true);
+            w.v[i][4 * j] = lo[0];
+            w.v[i][4 * j + 1] = lo[1];
+            w.v[i][4 * j + 2] = hi[0];
+            w.v[i][4 * j + 3] = hi[1];
+        }
+    return w;
+}
+__device__ __forceinline__ v4f fp8_mfma16_wide(const Fp8Wide& w, const Fp8Wide& x) {
+    v4f c = v4f{};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) c = __builtin_amdgcn_mfma_f32_16x16x32_bf16(w.v[i], x.v[i], c, 0, 0, 0);
+    return c;
+}
+
+// What an e8m0 byte stands for.
+__device__ __forceinline__ float fp8_scale_value(uint32_t b) {
+    return __uint_as_float(b == 255u ? 0x7fc00000u : b == 0u ? 0x00400000u : b << 23);
+}
+
 // A few rows' codes and scales, by the whole workgroup into LDS: rows of `pitch` bytes (K padded to whole
 // groups, and 16 bytes so that 16 rows' chunks lie in different banks), and a scale byte a group.
 template <int DT>
