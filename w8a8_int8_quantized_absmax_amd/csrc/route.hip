@@ -312,11 +312,18 @@ __global__ __launch_bounds__(kThreads) void k_route(RouteArgs a, int per, int pi
                     if (first > -INFINITY) best[q] = order_key(a.group_score == 2 && second > -INFINITY ? first + second : first);
                 }
             }
-            for (int h = 0; h < a.groups; ++h) {
-                uint64_t o = 0;
+            // (their places in LDS taken over by the groups' keys)
+            unsigned long long* const keys = reinterpret_cast<unsigned long long*>(space.scores[team]);
+            __builtin_amdgcn_fence(__ATOMIC_SEQ_CST, "workgroup");
+            __builtin_amdgcn_wave_barrier();
 #pragma unroll
-                for (int q = 0; q < 64 / L; ++q)
-                    if (h / L == q) o = __shfl((unsigned long long)best[q], (lane & ~(L - 1)) + h % L);
+            for (int q = 0; q < 64 / L; ++q)
+                if (r + L * q < a.groups) keys[r + L * q] = best[q];
+            __builtin_amdgcn_fence(__ATOMIC_SEQ_CST, "workgroup");
+            __builtin_amdgcn_wave_barrier();
+#pragma unroll 4
+            for (int h = 0; h < a.groups; ++h) {
+                const uint64_t o = keys[h];
 #pragma unroll
                 for (int q = 0; q < 64 / L; ++q) rank[q] += o > best[q] || (o == best[q] && h < r + L * q);
             }
@@ -327,9 +334,12 @@ __global__ __launch_bounds__(kThreads) void k_route(RouteArgs a, int per, int pi
                 kept |= (L == 64 ? b : b >> (lane & 48) & 0xffff) << (L * q & 63);
             }
             __builtin_amdgcn_wave_barrier();
+            const float per_size = 1.0f / (float)size;  // (exact enough: quotients of whole numbers up to 512)
 #pragma unroll
-            for (int j = 0; j < VPL; ++j)
-                if (!(kept >> min((r + L * j) / size, 63) & 1)) key[j] = 0;
+            for (int j = 0; j < VPL; ++j) {
+                const int g = (int)(((float)(r + L * j) + 0.5f) * per_size);
+                if (!(kept >> min(g, 63) & 1)) key[j] = 0;
+            }
         }
         int id[kSlots];
 #pragma unroll

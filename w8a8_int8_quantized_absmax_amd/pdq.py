@@ -691,13 +691,17 @@ def _dense2(t):
     return t.stride() == (t.shape[1], 1) or t.is_contiguous()
 
 
+_current_device = getattr(torch._C, "_cuda_getDevice", None)
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+
+
 def _kv_call(fn, index: int, *args) -> None:
     """A key/value call on the current stream of device `index`, with that device current.  These calls run once a
     layer and token, where the host's microseconds count: the raw stream is asked for, no stream object made."""
-    if index != torch._C._cuda_getDevice():
+    if index != _current_device():
         with torch.cuda.device(index):
             return _kv_call(fn, index, *args)
-    st = getattr(_lib or lib(), fn)(*args, torch._C._cuda_getCurrentRawStream(index))
+    st = getattr(_lib or lib(), fn)(*args, _raw_stream(index))
     if st != 0:
         raise PdqError(fn, st)
 
@@ -982,6 +986,16 @@ def quantize_fp8(x: torch.Tensor) -> CodesFP8:
     return q
 
 
+def _rows(t, name, kind, dtypes):
+    """_check_mat for what is called once a layer and token -> the row pitch."""
+    if t.dim() != 2 or kind not in dtypes or not t.is_cuda:
+        _check_mat(t, name, dtypes)
+    pitch, one = t.stride()
+    if one != 1:
+        _check_mat(t, name, dtypes)
+    return pitch if t.shape[0] > 1 else t.shape[1]
+
+
 def _fp8_operands(w, k, index, bias, m, out, dtype, like):
     """The checks that linear_fp8 and gemm_fp8 share -> y, its row pitch."""
     if type(w) is not WeightFP8 or w.lead:
@@ -1014,15 +1028,16 @@ def linear_fp8(x, w: WeightFP8, bias=None, out=None, dtype=None, workspace=None)
     (quantize_fp8 and gemm_fp8: codes for several weights.)
 
     y is f16 for f16 x, else bf16, or of `dtype`."""
-    _check_mat(x, "x")
+    kind = x.dtype
+    ldx = _rows(x, "x", kind, _DT)
     m, k = x.shape
-    index, kind = x.get_device(), x.dtype
+    index = x.get_device()
     y, ldy = _fp8_operands(w, k, index, bias, m, out, dtype or (torch.bfloat16 if kind is torch.float32 else kind), x)
     size, at = linear_fp8_workspace_bytes(m, k), None
     if size or workspace is not None:
         workspace, size = _workspace(workspace, size, x, index)
         at = workspace.data_ptr()
-    _kv_call("pdq_linear_fp8", index, x.data_ptr(), _DT[kind], m, k, _ld(x), w.at, w.scale_at, w.scale_type,
+    _kv_call("pdq_linear_fp8", index, x.data_ptr(), _DT[kind], m, k, ldx, w.at, w.scale_at, w.scale_type,
              bias.data_ptr() if bias is not None else None, w.n, y.data_ptr(), _DT[y.dtype], ldy, at, size)
     return {"y": y}
 
@@ -1131,9 +1146,10 @@ def route_experts(logits, k: int, score: str = "softmax", bias=None, groups: int
     score: "softmax" or "sigmoid"; bias float32 [experts]: added for the choice alone; groups,
     top_groups, group_score: only the best top_groups of `groups` runs of experts take part, by the sum
     of their group_score largest; renormalize: a token's weights sum to 1, times scale."""
-    _check_mat(logits, "logits")
+    kind = logits.dtype
+    ldl = _rows(logits, "logits", kind, _DT)
     tokens, experts = logits.shape
-    index, kind = logits.get_device(), logits.dtype
+    index = logits.get_device()
     if bias is not None:
         _check_dense(bias, "bias", torch.float32, (experts,))
         if bias.get_device() != index:
@@ -1154,7 +1170,7 @@ def route_experts(logits, k: int, score: str = "softmax", bias=None, groups: int
         at = buffer.data_ptr()
         ws = workspace.data_ptr()
     offsets = at + 12 * n
-    _kv_call("pdq_route_experts", index, logits.data_ptr(), _DT[kind], tokens, experts, _ld(logits),
+    _kv_call("pdq_route_experts", index, logits.data_ptr(), _DT[kind], tokens, experts, ldl,
              bias.data_ptr() if bias is not None else None, rule[1], at, at + 4 * n, offsets, at + 8 * n, ws, size)
     r = Routing.__new__(Routing)
     r._tensors, r._buffer, r.tokens, r.experts, r.k, r.index = None, buffer, tokens, experts, k, index
@@ -1183,7 +1199,8 @@ def experts_fp8(x, routing: Routing, gate_up: WeightFP8, down: WeightFP8, out=No
 
     x: [tokens, hidden] bf16 or f16; gate_up: a WeightFP8 [experts, 2, inner, hidden]; down:
     [experts, hidden, inner], both with scales of one type."""
-    _check_mat(x, "x", _HALF)
+    kind = x.dtype
+    ldx = _rows(x, "x", kind, _HALF)
     tokens, hidden = x.shape
     index = x.get_device()
     experts, inner = routing.experts, gate_up.n
@@ -1197,15 +1214,16 @@ def experts_fp8(x, routing: Routing, gate_up: WeightFP8, down: WeightFP8, out=No
     if not index == routing.index == gate_up.index == down.index:
         raise ValueError("x, the routing and the weights must be on one device")
     if out is None:
-        y = x.new_empty((tokens, hidden))
+        y, ldy = x.new_empty((tokens, hidden)), hidden
     else:
         y = out
-        _check_mat(y, "out", (x.dtype,))
+        _check_mat(y, "out", (kind,))
         if y.shape != x.shape or y.get_device() != index:
             raise ValueError("out must have x's shape and device")
+        ldy = _ld(y)
     size = experts_fp8_workspace_bytes(tokens, routing.k, experts, hidden, inner)
     workspace, size = _workspace(workspace, size, x, index)
     c = _ExpertsC(gate_up.at, gate_up.scale_at, down.at, down.scale_at, gate_up.scale_type, experts, hidden, inner)
-    _kv_call("pdq_experts_fp8", index, x.data_ptr(), _DT[x.dtype], _ld(x), routing._ref(), ctypes.byref(c), y.data_ptr(),
-             _ld(y), workspace.data_ptr() if size else None, size)
+    _kv_call("pdq_experts_fp8", index, x.data_ptr(), _DT[kind], ldx, routing._ref(), ctypes.byref(c), y.data_ptr(),
+             ldy, workspace.data_ptr() if size else None, size)
     return {"y": y}
