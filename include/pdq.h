@@ -628,7 +628,8 @@ pdq_status pdq_kv_attention(const void* q, pdq_dtype dt, int64_t tokens, int64_t
  * multiple of 128: pdq_fp8_bytes(rows, K) bytes, rows and K values beyond the matrix
  * 0.  Scales of a row (of a weight's 128 rows) are followed by padding up to
  * pdq_fp8_scale_pitch(K) = 4 ceil(K / 512) of them.  K, alignment and the sizes'
- * limits as above.  A call on `count` matrices takes them one behind the other.
+ * limits as above, but one product at most 2^38 outputs.  A call on `count` matrices takes them
+ * one behind the other.  What a call writes overlaps nothing else that it reads or writes.
  */
 typedef enum {
     PDQ_E8M0 = 0,      /* a power of two, one byte */
@@ -657,8 +658,9 @@ pdq_status pdq_pack_weight_fp8(const uint8_t* codes, const void* scale, pdq_scal
                                int64_t N, int64_t K, uint8_t* wq, void* w_scale, void* stream);
 
 /*
- * Linear layer: pdq_quantize_fp8, then pdq_gemm_fp8 (one launch for few values: to about the same
- * result, the order of its sums is another).  The parts, for callers that feed several weights.
+ * Linear layer: pdq_quantize_fp8, then pdq_gemm_fp8.  Few values (pdq_linear_fp8_workspace 0) are coded
+ * within the product's launch: the same codes, but the order of the sums is another, so that the last bit
+ * of y may differ from the two calls'.  The parts are for callers that feed several weights.
  *   x        [M, K] of x_dt, row pitch ldx
  *   xq       packed codes out, pdq_fp8_bytes(M, K) bytes, 16-byte aligned
  *   x_scale  e8m0 out [M, pdq_fp8_scale_pitch(K)], 4-byte aligned
@@ -723,12 +725,17 @@ pdq_status pdq_route_experts(const void* logits, pdq_dtype dt, int64_t tokens, i
 /*
  * The experts' layer: y[t] = sum over a token's slots j of
  *   weights[t, j] * Down_e h,  h = silu(Gate_e x[t]) * (Up_e x[t]),  e = ids[t, j],
- * x and h coded in FP8 as above, products, h and the sum over the slots (in their order) in
- * binary32, silu as in pdq_silu_mul_quantize_per_token; y rounded once.
+ * x and h coded in FP8 as above (h once more: a difference of the sums' last bits can move a code of h by
+ * a step), products, h and the sum over the slots in binary32, silu as in
+ * pdq_silu_mul_quantize_per_token; y rounded once.  The order of all sums follows from the sizes alone and
+ * is the same on every call; the slots' is their own, except for a few rows (tokens * k <= 8), whose
+ * K values go by wavefronts.  For few rows an expert the sums of gate and up are free of the matrix
+ * unit's alignment described above.
  *   x        [tokens, hidden] of dt (BF16 or F16), row pitch ldx
  *   routing  (host struct of device pointers) as pdq_route_experts leaves it.  What the arrays
  *            hold cannot be refused: an entry that is not a row or an expert of the call is passed
- *            over, and a slot whose id names an expert but whose row is not sorted is undefined.
+ *            over; the values of a token one of whose slots names an expert, but whose row is not
+ *            sorted to it, are undefined, and so is all of y where the offsets descend.
  *   experts  (host struct of device pointers) gate_up: 2 * experts matrices [inner, hidden],
  *            gate then up of each expert; down: experts matrices [hidden, inner]; their scales
  *            all of scale_t.  hidden and inner as K above.

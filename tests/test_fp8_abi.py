@@ -86,6 +86,13 @@ def test_gemm_and_quantize(L):
     assert L.pdq_quantize_fp8(P, 1, 4, 64, 64, P + 8, P, None) == ALIGN
 
 
+def test_product_limit(L):
+    # 2^38 outputs; the pointers are followed by no one, as the bias is misaligned
+    def f(m, n):
+        return L.pdq_gemm_fp8(P, P, m, 16, P, P, 0, P + 2, n, P, 1, n, None)
+    assert f(1 << 21, 1 << 17) == ALIGN and f(1 << 21, (1 << 17) + 1) == SHAPE
+
+
 def test_route(L):
     def f(x=P, dt=0, t=4, e=16, ld=16, b=None, score=0, k=2, g=1, tg=1, gs=1, renorm=1, scale=1.0, ids=P, w=P, o=P, r=P,
           ws=P, size=1 << 20, rule=True):
@@ -156,3 +163,14 @@ def test_oracle_experts_small():
     y, _ = FO.experts(x, np.array([[0], [-1]]), np.array([[0.5], [0.0]]), gu, one, d, one[:, 0])
     h = FO.values(np.full((1, 16), FO.silu_mul(4.0, 4.0)))[0]
     assert np.allclose(y[0], 0.5 * h.sum()) and not y[1].any()
+
+
+def test_binding_refuses_host_tensors():
+    x, z = torch.zeros((4, 64), dtype=torch.bfloat16), torch.zeros((4, 8))
+    ids, rows = torch.zeros((4, 2), dtype=torch.int32), torch.zeros(8, dtype=torch.int32)
+    for call in (lambda: pdq.quantize_weight_fp8(x), lambda: pdq.quantize_fp8(x), lambda: pdq.linear_fp8(x, None),
+                 lambda: pdq.pack_weight_fp8(x.to(torch.float8_e4m3fn), torch.ones((1, 1))),
+                 lambda: pdq.route_experts(z, 2), lambda: pdq.experts_fp8(x, None, None, None),
+                 lambda: pdq.Routing(ids, torch.zeros((4, 2)), torch.zeros(9, dtype=torch.int32), rows)):
+        with pytest.raises(ValueError):
+            call()

@@ -179,18 +179,27 @@ struct Fp8Tile {
     int block;   // its first block of 16 rows
 };
 
-// Every lane of the wavefront takes part and gets the same answer.  What the
-// offsets hold cannot be checked on the host: they are clamped to rows that are
-// there, and a tile's blocks may exceed what well-formed offsets give, which the
-// caller's grid bounds (a tile of 16 rows is block `index`).
+// Expert e's sorted rows.  What the offsets hold cannot be checked on the host: they are clamped to
+// rows that are there, and where they do not ascend there are no tiles (from that run of 64 experts
+// on), so that all tiles together never hold more rows, or blocks, than there are.
+struct Fp8Span {
+    int lo, count;
+    bool descends;
+};
+__device__ __forceinline__ Fp8Span fp8_span(const Fp8Sorted& s, int e) {  // e at most s.experts
+    const int lo = min(max(s.offsets[e], 0), s.total);
+    const int hi = min(max(s.offsets[min(e + 1, s.experts)], 0), s.total);
+    return Fp8Span{lo, hi - lo, hi < lo};
+}
+
+// Every lane of the wavefront takes part and gets the same answer.
 template <int kRows>
 __device__ __forceinline__ Fp8Tile fp8_tile(const Fp8Sorted& s, int index, int lane) {
     int tiles0 = 0, blocks0 = 0;
     for (int e0 = 0; e0 < s.experts; e0 += 64) {
-        const int e = min(e0 + lane, s.experts);
-        const int lo = min(max(s.offsets[e], 0), s.total);
-        const int hi = min(max(s.offsets[min(e + 1, s.experts)], lo), s.total);
-        const int count = hi - lo, blocks = (count + 15) / 16, tiles = (count + kRows - 1) / kRows;
+        const Fp8Span span = fp8_span(s, min(e0 + lane, s.experts));
+        if (__ballot(span.descends)) break;
+        const int lo = span.lo, count = span.count, blocks = (count + 15) / 16, tiles = (count + kRows - 1) / kRows;
         int bsum = blocks, tsum = tiles;  // inclusive sums over the lanes
 #pragma unroll
         for (int d = 1; d < 64; d <<= 1) {
@@ -216,15 +225,14 @@ __device__ __forceinline__ Fp8Tile fp8_tile(const Fp8Sorted& s, int index, int l
     return Fp8Tile{-1, 0, 0, 0};
 }
 
-// How many tiles of kRows sorted rows there are.
+// How many tiles of kRows sorted rows there are; none if the offsets descend anywhere.
 template <int kRows>
 __device__ __forceinline__ int fp8_tiles(const Fp8Sorted& s, int lane) {
     int n = 0;
     for (int e0 = 0; e0 < s.experts; e0 += 64) {
-        const int e = min(e0 + lane, s.experts);
-        const int lo = min(max(s.offsets[e], 0), s.total);
-        const int hi = min(max(s.offsets[min(e + 1, s.experts)], lo), s.total);
-        n += (hi - lo + kRows - 1) / kRows;
+        const Fp8Span span = fp8_span(s, min(e0 + lane, s.experts));
+        if (__ballot(span.descends)) return 0;
+        n += (span.count + kRows - 1) / kRows;
     }
     return __builtin_amdgcn_readfirstlane(wave_sum(n));
 }

@@ -906,7 +906,8 @@ pdq_status check_fp8_gemm(int64_t M, int64_t K, const uint8_t* wq, const void* w
     if (!scale_ok(scale_t)) return PDQ_ERR_DTYPE;
     PDQ_TRY(check_mk(M, K, K));
     PDQ_TRY(check_stack(1, N, K));
-    if (M * N > kMaxOutputs || ldy < N) return PDQ_ERR_SHAPE;
+    // (kMaxThreads: the smallest tiles, 128 x 256, by 256 threads)
+    if (M * N > std::min(kMaxOutputs, kMaxThreads * 128) || ldy < N) return PDQ_ERR_SHAPE;
     if (N > 0 && (!wq || !w_scale)) return PDQ_ERR_NULL;
     if (M > 0 && (!xq || !x_scale)) return PDQ_ERR_NULL;
     if (M > 0 && N > 0 && !y) return PDQ_ERR_NULL;
