@@ -729,8 +729,8 @@ pdq_status pdq_route_experts(const void* logits, pdq_dtype dt, int64_t tokens, i
  * a step), products, h and the sum over the slots in binary32, silu as in
  * pdq_silu_mul_quantize_per_token; y rounded once.  The order of all sums follows from the sizes alone and
  * is the same on every call; the slots' is their own, except for a few rows (tokens * k <= 8), whose
- * K values go by wavefronts.  For few rows an expert the sums of gate and up are free of the matrix
- * unit's alignment described above.
+ * K values go by wavefronts.  For few rows an expert, and for F16 always, the sums of gate and up
+ * are free of the matrix unit's alignment described above, which moves a few of h's codes by a step.
  *   x        [tokens, hidden] of dt (BF16 or F16), row pitch ldx
  *   routing  (host struct of device pointers) as pdq_route_experts leaves it.  What the arrays
  *            hold cannot be refused: an entry that is not a row or an expert of the call is passed

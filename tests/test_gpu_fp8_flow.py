@@ -135,6 +135,19 @@ def test_experts_uneven(tokens, experts, k, hidden, inner, scales):
     run_experts(tokens, tokens, experts, k, hidden, inner, scales, "bf16", skewed(tokens, tokens, experts, max(1, experts // 3)))
 
 
+@pytest.mark.parametrize("scales", ["pow2", "f32"])
+@pytest.mark.parametrize("tokens", [8, 12, 60, 150, 240])
+def test_experts_of_binary16_rows_are_fine(tokens, scales):
+    """With binary16 rows gate and up are sums in binary32: some hundred additions of 1024 products, each off by 2^-25
+    of a part of the sum by chance, less than 2^-21 of it; h of both then passes a border between two codes (2^-3
+    to 2^-4 of h apart) for 2 * 2^-21 / 2^-3.5 = 2^-16.5 of the values, an error of 2^-3.5 each: 2^-8.2 2^-3.5 < 2^-11.5 of
+    y's size, in quadrature with y's rounding (2^-11 / sqrt(3) at most) less than 2^-11; and the down product's
+    alignment, 2^-12 (fp8_cases.check_linear)."""
+    x, r, gate_up, down, y = run_experts(tokens, tokens, 3, 2, 1024, 272, scales, "f16", randn(tokens, tokens, 3, spread=0.0))
+    y64, _ = FO.experts(values(x), r.ids.cpu().numpy(), values(r.weights), *gate_up[1:], *down[1:])
+    assert np.linalg.norm(values(y) - y64) <= (2.0 ** -11 + 2.0 ** -12) * np.linalg.norm(y64)
+
+
 # a few rows: up to 8, of which a workgroup codes 32768 values at most
 @pytest.mark.parametrize("scales", ["pow2", "f32"])
 @pytest.mark.parametrize("tokens,experts,k,hidden,inner", [

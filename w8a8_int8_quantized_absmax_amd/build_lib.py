@@ -32,7 +32,8 @@ HIPCC_FLAGS = [
 
 # flags of one source: results of matrix instructions in vector registers, where its kernels' other
 # instructions read them (accumulation registers would cost a copy a value)
-FILE_FLAGS = {"gemm_fp8_f32.hip": ["-mllvm", "-amdgpu-mfma-vgpr-form=1"]}
+_VGPR_FORM = ["-mllvm", "-amdgpu-mfma-vgpr-form=1"]
+FILE_FLAGS = {"gemm_fp8_f32.hip": _VGPR_FORM, "gemm_fp8_wide.hip": _VGPR_FORM}
 
 
 def _quiet(text: str) -> str:

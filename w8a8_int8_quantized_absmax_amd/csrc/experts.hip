@@ -318,7 +318,7 @@ __global__ __launch_bounds__(256) void k_fp8_combine(Fp8ExpertsArgs a) {
 }
 
 template <bool F32S>
-void launch_products(const Fp8ExpertsArgs& a, hipStream_t st) {
+void launch_products(const Fp8ExpertsArgs& a, int dt, hipStream_t st) {
     // Rows of a tile by the average rows of an expert: a tile that is not full costs as much as a
     // full one.  Below 12 one block of 16 rows at a time.  Measured (us, blocks of 16 / tiles of 64 / 128 /
     // 256), 4 of 32 experts of 4096 x 1360, average rows 8: 129 / 131 / 138 / 163, 16: 154 / 137 / 146 / 171,
@@ -340,7 +340,11 @@ void launch_products(const Fp8ExpertsArgs& a, hipStream_t st) {
         t.h = a.h;
         t.hs = a.hs;
         t.h_pitch = (int)fp8_scale_pitch(a.inner);
-        launch_fp8_expert_tiles(t, true, rows, st);
+        // Widened products take 256 registers for less of a tile: 64 rows, or 128 from an average of 150.  Measured
+        // (us, all in tiles of 64 / 128, binary16), the 32 experts above, 32: 159 / 202, 64: 200 / 225, 128: 281 / 300,
+        // 191: 362 / 339; the 8, 64: 359 / 429.
+        const bool wide = dt == kF16;
+        launch_fp8_expert_tiles(t, true, wide, !wide ? rows : each >= 150 ? 128 : 64, st);
         t.x = a.h;
         t.xs = a.hs;
         t.w = a.down;
@@ -351,7 +355,7 @@ void launch_products(const Fp8ExpertsArgs& a, hipStream_t st) {
         t.y = a.partial;
         t.ldy = a.hidden;
         t.weights = a.weights;
-        launch_fp8_expert_tiles(t, false, rows, st);
+        launch_fp8_expert_tiles(t, false, false, rows, st);
         return;
     }
     const uint32_t blocks = (uint32_t)fp8_blocks(a.sorted.total, a.sorted.experts);
@@ -383,8 +387,8 @@ void launch_fp8_experts_direct(const Fp8ExpertsArgs& a, int dt, hipStream_t st) 
 }
 
 void launch_fp8_experts(const Fp8ExpertsArgs& a, int out_dt, hipStream_t st) {
-    if (a.ws_f32) launch_products<true>(a, st);
-    else launch_products<false>(a, st);
+    if (a.ws_f32) launch_products<true>(a, out_dt, st);
+    else launch_products<false>(a, out_dt, st);
     const dim3 grid((uint32_t)a.tokens, (a.hidden + 1023) / 1024);
     if (out_dt == kF16) hipLaunchKernelGGL((k_fp8_combine<kF16>), grid, dim3(256), 0, st, a);
     else hipLaunchKernelGGL((k_fp8_combine<kBF16>), grid, dim3(256), 0, st, a);

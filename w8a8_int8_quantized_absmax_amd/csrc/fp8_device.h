@@ -92,19 +92,23 @@ __device__ __forceinline__ v4f fp8_mfma16(v8i w, v8i x, v4f c, int sw, int sx) {
 struct Fp8Wide {
     v8bf v[4];
 };
+__device__ __forceinline__ v8bf fp8_widen8(unsigned a, unsigned b) {
+    v8bf w;
+#pragma unroll
+    for (int j = 0; j < 2; ++j) {
+        const auto lo = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(j ? b : a, 1.0f, false);
+        const auto hi = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(j ? b : a, 1.0f, true);
+        w[4 * j] = lo[0];
+        w[4 * j + 1] = lo[1];
+        w[4 * j + 2] = hi[0];
+        w[4 * j + 3] = hi[1];
+    }
+    return w;
+}
 __device__ __forceinline__ Fp8Wide fp8_widen(v8i f) {
     Fp8Wide w;
 #pragma unroll
-    for (int i = 0; i < 4; ++i)
-#pragma unroll
-        for (int j = 0; j < 2; ++j) {
-            const auto lo = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8((unsigned)f[2 * i + j], 1.0f, false);
-            const auto hi = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8((unsigned)f[2 * i + j], 1.0f, true);
-            w.v[i][4 * j] = lo[0];
-            w.v[i][4 * j + 1] = lo[1];
-            w.v[i][4 * j + 2] = hi[0];
-            w.v[i][4 * j + 3] = hi[1];
-        }
+    for (int i = 0; i < 4; ++i) w.v[i] = fp8_widen8((unsigned)f[2 * i], (unsigned)f[2 * i + 1]);
     return w;
 }
 __device__ __forceinline__ v4f fp8_mfma16_wide(const Fp8Wide& w, const Fp8Wide& x) {

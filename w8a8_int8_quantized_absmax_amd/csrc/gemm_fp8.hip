@@ -21,10 +21,14 @@ void launch_fp8_tiles(const Fp8TileArgs& a, int out_dt, int rows, hipStream_t st
     }
 }
 
-void launch_fp8_expert_tiles(const Fp8TileArgs& a, bool gate_up, int rows, hipStream_t st) {
+void launch_fp8_expert_tiles(const Fp8TileArgs& a, bool gate_up, bool wide, int rows, hipStream_t st) {
     const int64_t some = std::min(a.sorted.total, a.sorted.experts);
     const int64_t most = (a.sorted.total + (rows - 1) * some) / rows;  // tiles of rows
     const uint32_t tiles = (uint32_t)(most * (gate_up ? (a.N + 127) / 128 : (a.N + BN - 1) / BN));
+    if (wide) {
+        launch_fp8_tiles_wide(a, rows, tiles, st);
+        return;
+    }
     if (a.ws_f32) {
         launch_fp8_tiles_f32(a, gate_up ? kGateUp : kDown, 0, rows, tiles, st);
         return;

@@ -91,7 +91,12 @@ enum { kDense = 0, kGateUp = 1, kDown = 2 };
 // F32S: binary32 block scales.  A group's product then has a scale of its own to be multiplied by,
 // a multiply-add a value, which takes half of the vector unit's time.  The accumulators are in
 // vector registers (NA at most 3: 192 of 256), the products' results wait kLag products for theirs.
-template <int EPI, int OUT, int NA, bool F32S>
+//
+// WIDE (gate and up of binary16 rows, NA at most 2): the codes are widened between LDS and the product, and 16-bit
+// products take their place (fp8_widen); a group's sum is multiplied by both scales.  The FP8 products'
+// alignment moves a few of h's codes by a step (2^-3 of them): unseen beside a bfloat16 rounding, but
+// six times a binary16 one.
+template <int EPI, int OUT, int NA, bool F32S, bool WIDE = false>
 __global__ __launch_bounds__(256) void k_fp8_tile(Fp8TileArgs a) {
     // [step % 2][half], each an object of its own: the compiler then knows which loads into LDS
     // a read has to wait for.  Behind the first, four groups' scales.
@@ -142,7 +147,7 @@ __global__ __launch_bounds__(256) void k_fp8_tile(Fp8TileArgs a) {
         for (int j = 0; j < 8; ++j) {
             acc[i][j] = v4f{};
             // accumulation registers: the products then work on them in place
-            if constexpr (!F32S) asm volatile("" : "+a"(acc[i][j]));
+            if constexpr (!F32S && !WIDE) asm volatile("" : "+a"(acc[i][j]));
         }
     if constexpr (EPI == kDense) {
         s_aux[tid] = a.bias && n0 + tid < a.N ? a.bias[n0 + tid] : 0.0f;
@@ -269,7 +274,9 @@ __global__ __launch_bounds__(256) void k_fp8_tile(Fp8TileArgs a) {
     // evenly between the products: four wavefronts' reads behind each other's products would
     // keep LDS busy for longer than the products take.
     constexpr int kLag = 4, kRing = 8;
-    v4f part_sum[kRing];
+    v4f part_sum[kRing];  // WIDE: [row % 2][channels' block]
+    v8bf wide_b[4][4];
+    float both[2];
 #pragma unroll
     for (int q = 0; q < kRing; ++q) part_sum[q] = v4f{};
     auto half = [&](auto HA, auto HB, auto BYTE, auto&& load, auto&& read1, auto N1, auto&& read2, auto N2) {
@@ -286,7 +293,41 @@ __global__ __launch_bounds__(256) void k_fp8_tile(Fp8TileArgs a) {
                 wait_loads_and_sync<2 * kLoads>();
                 __builtin_amdgcn_sched_barrier(0);
             }
-            if constexpr (F32S) {
+            if constexpr (WIDE) {
+                // a quarter (j) of the group's K values: row block i by the half's four blocks of channels
+                const int at = i & 1;
+                if (j == 0) {
+                    const uint32_t byte = (uint32_t)sx[ha * NA + i] >> 8 * kByte & 255;
+                    const float w = F32S ? ws[hb] : fp8_scale_value((uint32_t)sw[hb] >> 8 * kByte & 255);
+                    both[at] = __fmul_rn(fp8_scale_value(byte), w);
+                }
+                if (i == 0 && !(ha == 1 && q < L)) {  // (those of the quadrant before are the same ones)
+#pragma unroll
+                    for (int b = 0; b < 4; ++b)
+                        wide_b[b][j] = fp8_widen8(fb[hb][b][j >> 1][2 * (j & 1)], fb[hb][b][j >> 1][2 * (j & 1) + 1]);
+                }
+                const v8bf wide_a = fp8_widen8(fa[ha][i][j >> 1][2 * (j & 1)], fa[ha][i][j >> 1][2 * (j & 1) + 1]);
+#pragma unroll
+                for (int b = 0; b < 4; ++b) {
+                    v4f& to = part_sum[at * 4 + b];
+                    to = __builtin_amdgcn_mfma_f32_16x16x32_bf16(wide_b[b][j], wide_a, j ? to : v4f{}, 0, 0, 0);
+                    asm volatile("" : "+v"(to));
+                }
+                auto add = [&](int pa, int ph, int row) {  // the sums of row block `row`, in half ph of the channels
+#pragma unroll
+                    for (int b = 0; b < 4; ++b) {
+                        v4f& to = acc[pa * NA + row][ph * 4 + b];
+#pragma unroll
+                        for (int r = 0; r < 4; ++r) to[r] = __fmaf_rn(part_sum[(row & 1) * 4 + b][r], both[row & 1], to[r]);
+                        asm volatile("" : "+v"(to));
+                    }
+                };
+                if (NA == 2 && j == 1 && q >= 4) {  // the row block before, its products done by now
+                    const int before_q = q - 4;
+                    add(ha, before_q < L ? decltype(HB)::value : 1 - decltype(HB)::value, before_q % L / 4);
+                }
+                if (j == 3 && (NA == 1 || q == 2 * L - 1)) add(ha, hb, i);
+            } else if constexpr (F32S) {
                 part_sum[q % kRing] = mfma<kByte>(whole(fb[hb][j]), whole(fa[ha][i]), v4f{}, sw[hb], sx[ha * NA + i]);
                 asm volatile("" : "+v"(part_sum[q % kRing]));  // here: not where its value is first asked for
                 // the product kLag before: of this half, of the step's first, or of the step before
@@ -348,7 +389,7 @@ __global__ __launch_bounds__(256) void k_fp8_tile(Fp8TileArgs a) {
         g += 2;
     } while (g < G);
     wait_loads_and_sync<0>();  // the regions are no longer read or written
-    if constexpr (F32S) {  // the last step's last products
+    if constexpr (F32S && !WIDE) {  // the last step's last products
 #pragma unroll
         for (int p = 4 * NA - kLag; p < 4 * NA; ++p)
 #pragma unroll

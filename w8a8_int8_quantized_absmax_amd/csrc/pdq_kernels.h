@@ -298,7 +298,8 @@ struct Fp8TileArgs {
 // rows of a tile: 256 (e8m0 scales), 192 (binary32 scales), 128, of the experts also 64
 void launch_fp8_tiles(const Fp8TileArgs& a, int out_dt, int rows, hipStream_t st);
 void launch_fp8_tiles_f32(const Fp8TileArgs& a, int epi, int out_dt, int rows, uint32_t tiles, hipStream_t st);
-void launch_fp8_expert_tiles(const Fp8TileArgs& a, bool gate_up, int rows, hipStream_t st);
+void launch_fp8_tiles_wide(const Fp8TileArgs& a, int rows, uint32_t tiles, hipStream_t st);  // gate and up
+void launch_fp8_expert_tiles(const Fp8TileArgs& a, bool gate_up, bool wide, int rows, hipStream_t st);
 
 // The most blocks of 16 rows that `total` rows of `experts` experts take.
 inline int64_t fp8_blocks(int64_t total, int64_t experts) {
