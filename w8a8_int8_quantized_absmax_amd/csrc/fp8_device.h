@@ -64,6 +64,8 @@ __device__ __forceinline__ uint32_t row16_max(uint32_t v) {
     return max(v, dpp_u32<0x140>(v));  // row_mirror
 }
 
+// The larger magnitude, NaN if one is.
+__device__ __forceinline__ float larger(float a, float b) { return __builtin_elementwise_maximum(fabsf(a), fabsf(b)); }
 __device__ __forceinline__ uint32_t magnitude(float x) { return __float_as_uint(x) & 0x7fffffffu; }
 
 // A lane's 32 bytes of a fragment of 16 rows x 128 K values: row lane % 16, the
@@ -241,11 +243,11 @@ __device__ __forceinline__ int fp8_tiles(const Fp8Sorted& s, int lane) {
     return __builtin_amdgcn_readfirstlane(wave_sum(n));
 }
 
-// silu(g) * u: e = 2^(-|g| log2 e) and 1 / (1 + e) by the hardware's exp2 and reciprocal.
+// silu(g) * u = g u / (1 + e), e = 2^(-g log2 e), by the hardware's exp2 and reciprocal (where e is beyond 2^126 or
+// infinite, 0).
 __device__ __forceinline__ float fp8_silu_mul(float g, float u) {
-    const float e = __builtin_amdgcn_exp2f(-fabsf(g) * 1.4426950408889634f);
-    const float r = __builtin_amdgcn_rcpf(1.0f + e);
-    return (g * (g >= 0.0f ? r : e * r)) * u;
+    const float e = __builtin_amdgcn_exp2f(g * -1.4426950408889634f);
+    return g * __builtin_amdgcn_rcpf(1.0f + e) * u;
 }
 
 // The token and slot of row r of a tile, -1 where there is none (or the entry is not a row of the call).

@@ -21,6 +21,8 @@
 //   after the next, after each barrier: two barriers a step, every load sent 1.5 steps
 //   (some 3000 clocks) before it is needed.
 // - The scales of four groups are one dword a row; they come through LDS too.
+// What one tile of a compute unit costs beside its steps (1.5 us each at NA = 4): some 5 us, 7 for gate and
+// up, of it 3 and 5 the vector unit's in the epilogue, which no other tile's products run beside.
 
 #pragma once
 
@@ -437,16 +439,17 @@ __global__ __launch_bounds__(256) void k_fp8_tile(Fp8TileArgs a) {
         uint32_t* const tops = sc;  // [2][256]
 #pragma unroll
         for (int i = 0; i < 2 * NA; ++i) {
-            uint32_t top = 0;
+            float most = 0.0f;
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
                 const bool there = n0 + wn * 64 + 16 * j < a.N;  // a multiple of 16
 #pragma unroll
                 for (int r = 0; r < 4; ++r) {
                     acc[i][j][r] = there ? fp8_silu_mul(acc[i][j][r], acc[i][j + 4][r]) : 0.0f;
-                    top = max(top, magnitude(acc[i][j][r]));
+                    most = larger(most, acc[i][j][r]);
                 }
             }
+            uint32_t top = magnitude(most);
             top = max(top, (uint32_t)__shfl_xor((int)top, 16));
             top = max(top, (uint32_t)__shfl_xor((int)top, 32));
             tops[wn * 256 + rbase + 16 * i + row0] = top;
@@ -465,7 +468,7 @@ __global__ __launch_bounds__(256) void k_fp8_tile(Fp8TileArgs a) {
             for (int j = 0; j < 4; ++j) {
                 float v[4];
 #pragma unroll
-                for (int e = 0; e < 4; ++e) v[e] = fp8_scaled(acc[i][j][e], inv);
+                for (int e = 0; e < 4; ++e) v[e] = acc[i][j][e] * inv;  // (whatever a group with a NaN scale holds is NaN)
                 *reinterpret_cast<uint32_t*>(image + i * kGroupBytes + wn * kWBlock + fp8_pos(row0, j) + 4 * quad) =
                     fp8_pack4(v[0], v[1], v[2], v[3]);
             }
