@@ -322,10 +322,11 @@ void launch_products(const Fp8ExpertsArgs& a, int dt, hipStream_t st) {
     // Rows of a tile by the average rows of an expert: a tile that is not full costs as much as a
     // full one.  Below 12 one block of 16 rows at a time.  Measured (us, blocks of 16 / tiles of 64 / 128 /
     // 256), 4 of 32 experts of 4096 x 1360, average rows 8: 129 / 131 / 138 / 163, 16: 154 / 137 / 146 / 171,
-    // 32: 221 / 154 / 156 / 177, 64: 389 / 189 / 175 / 194, 191: 818 / 294 / 242 / 244, 512: 1617 / 631 / 511 / 451;
-    // 2 of 8 of 4096 x 14336, 128: 1684 / 522 / 370 / 410, 256: 2768 / 769 / 644 / 504.
+    // 32: 221 / 154 / 156 / 177, 64: 389 / 189 / 175 / 194, 128: - / 262 / 227 / 237, 191: 818 / 293 / 248-259 / 239-240,
+    // 512: 1617 / 631 / 511 / 451; 2 of 8 of 4096 x 14336, 128: 1684 / 522 / 370 / 410, 256: 2768 / 769 / 644 / 504.
     const int64_t each = a.sorted.total / a.sorted.experts;
-    const int rows = each >= 200 ? (F32S ? 192 : 256) : each >= 48 ? 128 : each >= 12 ? 64 : 0;
+    const int large = F32S ? 192 : 256;
+    const int rows = each >= 160 ? large : each >= 48 ? 128 : each >= 12 ? 64 : 0;
     if (rows > 0) {
         Fp8TileArgs t{};
         t.x = a.x;
@@ -344,7 +345,7 @@ void launch_products(const Fp8ExpertsArgs& a, int dt, hipStream_t st) {
         // (us, all in tiles of 64 / 128, binary16), the 32 experts above, 32: 159 / 202, 64: 200 / 225, 128: 281 / 300,
         // 191: 362 / 339; the 8, 64: 359 / 429.
         const bool wide = dt == kF16;
-        launch_fp8_expert_tiles(t, true, wide, !wide ? rows : each >= 150 ? 128 : 64, st);
+        launch_fp8_gate_up_tiles(t, wide, !wide ? rows : each >= 150 ? 128 : 64, st);
         t.x = a.h;
         t.xs = a.hs;
         t.w = a.down;
@@ -355,7 +356,9 @@ void launch_products(const Fp8ExpertsArgs& a, int dt, hipStream_t st) {
         t.y = a.partial;
         t.ldy = a.hidden;
         t.weights = a.weights;
-        launch_fp8_expert_tiles(t, false, false, rows, st);
+        // Down in large tiles or, below, two of 128 x 128 a compute unit.  Measured (us, 128 x 256 / 128 x 128): the 8
+        // experts, 64: 318 / 287, 256: 512 / 567 (256 x 256 / 128 x 128); the 32, 16: 135 / 135, 64: 162 / 161.
+        launch_fp8_down_tiles(t, rows == large ? Fp8TileShape{large, 256} : Fp8TileShape{128, 128}, st);
         return;
     }
     const uint32_t blocks = (uint32_t)fp8_blocks(a.sorted.total, a.sorted.experts);

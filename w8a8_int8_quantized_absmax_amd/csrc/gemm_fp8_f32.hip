@@ -5,22 +5,21 @@
 
 namespace pdq {
 
-void launch_fp8_tiles_f32(const Fp8TileArgs& a, int epi, int out_dt, int rows, uint32_t tiles, hipStream_t st) {
+void launch_fp8_tiles_f32(const Fp8TileArgs& a, int epi, int out_dt, Fp8TileShape tile, uint32_t tiles, hipStream_t st) {
     const dim3 grid(tiles), block(256);
     if (epi == kDense && out_dt == kF16) {
-        if (rows == 192) hipLaunchKernelGGL((k_fp8_tile<kDense, kF16, 3, true>), grid, block, 0, st, a);
-        else hipLaunchKernelGGL((k_fp8_tile<kDense, kF16, 2, true>), grid, block, 0, st, a);
+        if (tile.rows == 192) hipLaunchKernelGGL((k_fp8_tile<kDense, kF16, 3, 4, true>), grid, block, 0, st, a);
+        else hipLaunchKernelGGL((k_fp8_tile<kDense, kF16, 2, 2, true>), grid, block, 0, st, a);
     } else if (epi == kDense) {
-        if (rows == 192) hipLaunchKernelGGL((k_fp8_tile<kDense, kBF16, 3, true>), grid, block, 0, st, a);
-        else hipLaunchKernelGGL((k_fp8_tile<kDense, kBF16, 2, true>), grid, block, 0, st, a);
+        if (tile.rows == 192) hipLaunchKernelGGL((k_fp8_tile<kDense, kBF16, 3, 4, true>), grid, block, 0, st, a);
+        else hipLaunchKernelGGL((k_fp8_tile<kDense, kBF16, 2, 2, true>), grid, block, 0, st, a);
     } else if (epi == kGateUp) {
-        if (rows == 192) hipLaunchKernelGGL((k_fp8_tile<kGateUp, 0, 3, true>), grid, block, 0, st, a);
-        else if (rows == 128) hipLaunchKernelGGL((k_fp8_tile<kGateUp, 0, 2, true>), grid, block, 0, st, a);
-        else hipLaunchKernelGGL((k_fp8_tile<kGateUp, 0, 1, true>), grid, block, 0, st, a);
+        if (tile.rows == 192) hipLaunchKernelGGL((k_fp8_tile<kGateUp, 0, 3, 4, true>), grid, block, 0, st, a);
+        else if (tile.rows == 128) hipLaunchKernelGGL((k_fp8_tile<kGateUp, 0, 2, 4, true>), grid, block, 0, st, a);
+        else hipLaunchKernelGGL((k_fp8_tile<kGateUp, 0, 1, 4, true>), grid, block, 0, st, a);
     } else {
-        if (rows == 192) hipLaunchKernelGGL((k_fp8_tile<kDown, 0, 3, true>), grid, block, 0, st, a);
-        else if (rows == 128) hipLaunchKernelGGL((k_fp8_tile<kDown, 0, 2, true>), grid, block, 0, st, a);
-        else hipLaunchKernelGGL((k_fp8_tile<kDown, 0, 1, true>), grid, block, 0, st, a);
+        if (tile.rows == 192) hipLaunchKernelGGL((k_fp8_tile<kDown, 0, 3, 4, true>), grid, block, 0, st, a);
+        else hipLaunchKernelGGL((k_fp8_tile<kDown, 0, 2, 2, true>), grid, block, 0, st, a);
     }
 }
 

@@ -1,5 +1,5 @@
 // Tiled product of 8-bit floating-point codes (gfx950): the kernel of gemm_fp8.hip (power-of-two
-// scales of the weights) and gemm_fp8_f32.hip (binary32 ones).
+// scales of the weights), gemm_fp8_f32.hip (binary32 ones) and gemm_fp8_wide.hip (widened codes).
 //
 //   acc[m, n] = sum over groups g of 128: S_x[m, g] S_w[n / 128, g] sum xq wq
 //
@@ -7,8 +7,9 @@
 // scales are operands of it, and nothing else touches the accumulators: an FP8 product
 // with a scale for each block of 128 costs what one without scales does.
 //
-// A tile of 64 NA rows x 256 channels (NA 4, 2 or 1) a workgroup of four wavefronts, 2 x 2, each
-// 32 NA rows x 128 channels.  Bound by the matrix unit (at NA = 4 by the power that it draws:
+// A tile of 64 NA rows x 64 NB channels a workgroup of four wavefronts, 2 x 2, each 32 NA rows x 32 NB
+// channels.  NA = NB = 4, or 2 and 4: one workgroup a compute unit; 2 and 2: two, which fill each other's begins
+// and ends, where a compute unit has few tiles.  Bound by the matrix unit (at NA = 4 by the power that it draws:
 // 16x16x128 runs 8% faster than 32x32x64 there, 4.29 against 3.96 PFLOP/s from registers
 // alone), so that all else has to run beside it:
 // - K in steps of a group.  Operands come through LDS, without registers: a packed block of 16
@@ -21,7 +22,8 @@
 //   after the next, after each barrier: two barriers a step, every load sent 1.5 steps
 //   (some 3000 clocks) before it is needed.
 // - The scales of four groups are one dword a row; they come through LDS too.
-// What one tile of a compute unit costs beside its steps (1.5 us each at NA = 4): some 5 us, 7 for gate and
+// - The outputs leave from the accumulators (through LDS, for longer runs of a row together: the same time).
+// What one tile of a compute unit costs beside its steps (1.5 us each at NA = NB = 4): some 5 us, 7 for gate and
 // up, of it 3 and 5 the vector unit's in the epilogue, which no other tile's products run beside.
 
 #pragma once
@@ -34,12 +36,8 @@ namespace pdq {
 
 namespace {
 
-constexpr int BN = 256;
 constexpr int kXcds = 8;
 constexpr int kGroupM = 4;  // tile rows walked together
-// A wavefront's part of the outputs leaves through LDS, 16 rows at a time: 128 binary32 values or
-// 16-bit ones, padded so that a row begins 4 banks behind the one before.
-constexpr int kOutPitch32 = 128 * 4 + 16, kOutPitch16 = 128 * 2 + 16;
 
 typedef __attribute__((address_space(3))) void* lds_ptr_t;
 
@@ -92,20 +90,22 @@ enum { kDense = 0, kGateUp = 1, kDown = 2 };
 //
 // F32S: binary32 block scales.  A group's product then has a scale of its own to be multiplied by,
 // a multiply-add a value, which takes half of the vector unit's time.  The accumulators are in
-// vector registers (NA at most 3: 192 of 256), the products' results wait kLag products for theirs.
+// vector registers (NA at most 3: 192 of 256), the products' results wait kLag products for theirs.  (With
+// NA = NB = 2 one workgroup multiplies while the other adds: 1024 x 4096 x 4096 in 23 us where 128 x 256 took 33.)
 //
 // WIDE (gate and up of binary16 rows, NA at most 2): the codes are widened between LDS and the product, and 16-bit
 // products take their place (fp8_widen); a group's sum is multiplied by both scales.  The FP8 products'
 // alignment moves a few of h's codes by a step (2^-3 of them): unseen beside a bfloat16 rounding, but
 // six times a binary16 one.
-template <int EPI, int OUT, int NA, bool F32S, bool WIDE = false>
-__global__ __launch_bounds__(256) void k_fp8_tile(Fp8TileArgs a) {
+template <int EPI, int OUT, int NA, int NB, bool F32S, bool WIDE = false>
+__global__ __launch_bounds__(256, NB == 4 ? 1 : 2) void k_fp8_tile(Fp8TileArgs a) {
+    constexpr int BN = 64 * NB;
     // [step % 2][half], each an object of its own: the compiler then knows which loads into LDS
     // a read has to wait for.  Behind the first, four groups' scales.
-    constexpr int kARegion = 4 * NA * kWBlock, kBRegion = 16 * kWBlock, kScaleWords = 512;
+    constexpr int kARegion = 4 * NA * kWBlock, kBRegion = 4 * NB * kWBlock, kScaleWords = 512;
     __shared__ __attribute__((aligned(1024))) uint8_t A00[kARegion + 4 * kScaleWords], A01[kARegion], A10[kARegion], A11[kARegion];
     __shared__ __attribute__((aligned(1024))) uint8_t B00[kBRegion], B01[kBRegion], B10[kBRegion], B11[kBRegion];
-    __shared__ float s_aux[BN];  // kDense: bias; kDown: the rows' weights
+    __shared__ __attribute__((aligned(16))) float s_aux[256];  // kDense: bias; kDown: the rows' weights
     __shared__ int32_t s_flat[EPI == kDown ? 256 : 1];
     uint32_t* const sc = reinterpret_cast<uint32_t*>(A00 + kARegion);
     auto regionA = [&](auto buf, auto half) -> uint8_t* {
@@ -142,17 +142,17 @@ __global__ __launch_bounds__(256) void k_fp8_tile(Fp8TileArgs a) {
     const int n0 = tn * (EPI == kGateUp ? 128 : BN);
     const int G = a.groups;
 
-    v4f acc[8][8];  // the first 2 NA rows used
+    v4f acc[8][8];  // 2 NA rows, 2 NB columns used
 #pragma unroll
     for (int i = 0; i < 2 * NA; ++i)
 #pragma unroll
-        for (int j = 0; j < 8; ++j) {
+        for (int j = 0; j < 2 * NB; ++j) {
             acc[i][j] = v4f{};
             // accumulation registers: the products then work on them in place
             if constexpr (!F32S && !WIDE) asm volatile("" : "+a"(acc[i][j]));
         }
     if constexpr (EPI == kDense) {
-        s_aux[tid] = a.bias && n0 + tid < a.N ? a.bias[n0 + tid] : 0.0f;
+        if (tid < BN) s_aux[tid] = a.bias && n0 + tid < a.N ? a.bias[n0 + tid] : 0.0f;
     } else if constexpr (EPI == kDown) {
         const int flat = fp8_sorted_row(a.sorted, t, tid);
         s_flat[tid] = flat;
@@ -160,8 +160,8 @@ __global__ __launch_bounds__(256) void k_fp8_tile(Fp8TileArgs a) {
     }
     __syncthreads();
 
-    // Loads of a half of a step: 4 NA blocks of 1 KB of the rows, 16 of the channels, of which a
-    // wavefront sends NA and 4.  Offsets are from the tile's first block; blocks past the last of
+    // Loads of a half of a step: 4 NA blocks of 1 KB of the rows, 4 NB of the channels, of which a
+    // wavefront sends NA and NB.  Offsets are from the tile's first block; blocks past the last of
     // the operand are the last one's: they only feed outputs that are not stored.
     const int blocks_n = (a.N + 15) / 16;  // of one matrix
     const int lasta = EPI == kDense ? (a.M - 1) / 16 : t.block + (t.rows - 1) / 16;
@@ -170,7 +170,7 @@ __global__ __launch_bounds__(256) void k_fp8_tile(Fp8TileArgs a) {
         a.w + ((EPI == kGateUp ? 2 : 1) * (int64_t)t.expert * blocks_n + n0 / 16) * G * kGroupBytes;
     const auto wrsrc = resource(wbase);
     const auto ursrc = resource(EPI == kGateUp ? wbase + (int64_t)blocks_n * G * kGroupBytes : wbase);
-    int oa[2][4], ob[2][4];  // [half]; 4 of them whatever NA is: an array of a dependent size loses the host's stub
+    int oa[2][4], ob[2][4];  // [half]; 4 of them whatever NA and NB are: an array of a dependent size loses the host's stub
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
 #pragma unroll
@@ -180,13 +180,13 @@ __global__ __launch_bounds__(256) void k_fp8_tile(Fp8TileArgs a) {
                        (piece & 1) * kWBlock + lane * 16;
         }
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const int piece = wave * 4 + i, b = piece >> 1;  // block b % 4 of wavefront column b / 4
-            const int at = EPI == kGateUp ? b : b / 4 * 8 + h * 4 + b % 4;
+        for (int i = 0; i < NB; ++i) {
+            const int piece = wave * NB + i, b = piece >> 1;  // block b % NB of wavefront column b / NB
+            const int at = EPI == kGateUp ? b : b / NB * 2 * NB + h * NB + b % NB;
             ob[h][i] = min(at, blocks_n - 1 - n0 / 16) * (G * kGroupBytes) + (piece & 1) * kWBlock + lane * 16;
         }
     }
-    constexpr int kLoads = NA + 4;
+    constexpr int kLoads = NA + NB;
     auto issue = [&](auto buf, auto ha, auto hb, int g, int q) {  // load q of the halves ha of the rows, hb of the channels
         const int at = min(g, G - 1) * kGroupBytes;
         constexpr int A = decltype(ha)::value, B = decltype(hb)::value;
@@ -195,7 +195,7 @@ __global__ __launch_bounds__(256) void k_fp8_tile(Fp8TileArgs a) {
                                                      oa[A][q < NA ? q : 0], at, 0, 0);
         else
             __builtin_amdgcn_raw_ptr_buffer_load_lds(B ? ursrc : wrsrc,
-                                                     (lds_ptr_t)(regionB(buf, hb) + (wave * 4 + q - NA) * kWBlock), 16,
+                                                     (lds_ptr_t)(regionB(buf, hb) + (wave * NB + q - NA) * kWBlock), 16,
                                                      ob[B][q < NA ? 0 : q - NA], at, 0, 0);
     };
     // Four groups' scales: of the activation row `tid`, and of the tile's two blocks of
@@ -206,7 +206,7 @@ __global__ __launch_bounds__(256) void k_fp8_tile(Fp8TileArgs a) {
     const uint8_t* ps = a.xs + (int64_t)min(m0 + tid, last_row) * a.pitch;
     auto scale_row = [&](int b) {  // of the tile's block b of weight rows
         if constexpr (EPI == kGateUp) return ((2 * (int64_t)t.expert + b) * blocks_w + tn) * a.pitch;
-        else return ((int64_t)t.expert * blocks_w + min(n0 / 128 + b, blocks_w - 1)) * a.pitch;
+        else return ((int64_t)t.expert * blocks_w + min((n0 + 32 * NB * b) / 128, blocks_w - 1)) * a.pitch;
     };
     const uint8_t* pw = static_cast<const uint8_t*>(a.ws) + (F32S ? 0 : scale_row(lane & 1));
     auto issue_scales = [&](int g) {
@@ -222,7 +222,7 @@ __global__ __launch_bounds__(256) void k_fp8_tile(Fp8TileArgs a) {
     };
     auto read_b = [&](auto buf, auto half, int q) {
         fb[decltype(half)::value][q >> 1][q & 1] =
-            *reinterpret_cast<const v4i*>(regionB(buf, half) + (wn * 4 + (q >> 1)) * kGroupBytes + (q & 1) * kWBlock + off);
+            *reinterpret_cast<const v4i*>(regionB(buf, half) + (wn * NB + (q >> 1)) * kGroupBytes + (q & 1) * kWBlock + off);
     };
     auto whole = [](const v4i (&f)[2]) { return v8i{f[0][0], f[0][1], f[0][2], f[0][3], f[1][0], f[1][1], f[1][2], f[1][3]}; };
     int sx[8], sw[2];
@@ -268,7 +268,7 @@ __global__ __launch_bounds__(256) void k_fp8_tile(Fp8TileArgs a) {
 #pragma unroll
     for (int q = 0; q < 2 * NA; ++q) read_a(I0{}, I0{}, q);
 #pragma unroll
-    for (int q = 0; q < 8; ++q) read_b(I0{}, I0{}, q);
+    for (int q = 0; q < 2 * NB; ++q) read_b(I0{}, I0{}, q);
 
     // Half a step: the rows' half HA by the channels' HB, then by the other.  The first products run
     // ahead of the barrier behind which `load` may refill what was read and `read1`, `read2` (n1,
@@ -284,13 +284,13 @@ __global__ __launch_bounds__(256) void k_fp8_tile(Fp8TileArgs a) {
     auto half = [&](auto HA, auto HB, auto BYTE, auto&& load, auto&& read1, auto N1, auto&& read2, auto N2) {
         constexpr int ha = decltype(HA)::value, kByte = decltype(BYTE)::value;
         constexpr int n1 = decltype(N1)::value, n2 = decltype(N2)::value;
-        constexpr int L = 4 * NA;                       // products of a quadrant
+        constexpr int L = NB * NA;                      // products of a quadrant
         constexpr int kAhead = NA == 4 ? 2 : 1;         // products before the barrier
         constexpr int kSpan1 = L - kAhead - L / 4, kSpan2 = L - L / 4;  // the last reads' latency under the last quarter
         __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
         for (int q = 0; q < 2 * L; ++q) {
-            const int i = q % L / 4, j = q % 4, hb = q < L ? decltype(HB)::value : 1 - decltype(HB)::value;
+            const int i = q % L / NB, j = q % NB, hb = q < L ? decltype(HB)::value : 1 - decltype(HB)::value;
             if (q == kAhead) {
                 wait_loads_and_sync<2 * kLoads>();
                 __builtin_amdgcn_sched_barrier(0);
@@ -337,13 +337,13 @@ __global__ __launch_bounds__(256) void k_fp8_tile(Fp8TileArgs a) {
                 const int pb = q >= kLag ? (p < L ? decltype(HB)::value : 1 - decltype(HB)::value)
                                          : (ha ? decltype(HB)::value : 1 - decltype(HB)::value);
                 const float s = q < kLag && ha == 0 ? before[pb] : ws[pb];
-                v4f& to = acc[pa * NA + p % L / 4][pb * 4 + p % 4];
+                v4f& to = acc[pa * NA + p % L / NB][pb * NB + p % NB];
 #pragma unroll
                 for (int r = 0; r < 4; ++r) to[r] = __fmaf_rn(part_sum[(q + kRing - kLag) % kRing][r], s, to[r]);
                 asm volatile("" : "+v"(to));
             } else {
-                acc[ha * NA + i][hb * 4 + j] =
-                    mfma<kByte>(whole(fb[hb][j]), whole(fa[ha][i]), acc[ha * NA + i][hb * 4 + j], sw[hb], sx[ha * NA + i]);
+                acc[ha * NA + i][hb * NB + j] =
+                    mfma<kByte>(whole(fb[hb][j]), whole(fa[ha][i]), acc[ha * NA + i][hb * NB + j], sw[hb], sx[ha * NA + i]);
             }
             __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
@@ -362,7 +362,7 @@ __global__ __launch_bounds__(256) void k_fp8_tile(Fp8TileArgs a) {
         using F = std::integral_constant<int, s & 1>;        // the half of the channels that comes first
         using O = std::integral_constant<int, (s + 1) & 1>;  // the other, the next step's first
         using ReadsA = std::integral_constant<int, 2 * NA>;
-        using ReadsB = std::integral_constant<int, 8>;
+        using ReadsB = std::integral_constant<int, 2 * NB>;
         if constexpr (F32S) {
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
@@ -393,11 +393,11 @@ __global__ __launch_bounds__(256) void k_fp8_tile(Fp8TileArgs a) {
     wait_loads_and_sync<0>();  // the regions are no longer read or written
     if constexpr (F32S && !WIDE) {  // the last step's last products
 #pragma unroll
-        for (int p = 4 * NA - kLag; p < 4 * NA; ++p)
+        for (int p = NB * NA - kLag; p < NB * NA; ++p)
 #pragma unroll
             for (int r = 0; r < 4; ++r) {
-                v4f& to = acc[NA + p / 4][4 + p % 4];
-                to[r] = __fmaf_rn(part_sum[(4 * NA + p) % kRing][r], ws[1], to[r]);
+                v4f& to = acc[NA + p / NB][NB + p % NB];
+                to[r] = __fmaf_rn(part_sum[(NB * NA + p) % kRing][r], ws[1], to[r]);
             }
     }
 
@@ -406,32 +406,36 @@ __global__ __launch_bounds__(256) void k_fp8_tile(Fp8TileArgs a) {
     const int el = (int)__builtin_amdgcn_mbcnt_hi(~0u, __builtin_amdgcn_mbcnt_lo(~0u, 0u));
     const int row0 = el & 15, quad = el >> 4;
     const int rbase = wm * 32 * NA;
-    uint8_t* const part = wave == 0 ? B00 : wave == 1 ? B01 : wave == 2 ? B10 : B11;  // the wavefront's own
     if constexpr (EPI == kDense) {
+        // Two blocks' quads are swapped between neighbouring rows of 16 lanes, so that a lane has eight outputs of one
+        // block, 64 bytes of a row together.
         uint16_t* y = static_cast<uint16_t*>(a.y);
         const bool vec = (reinterpret_cast<uintptr_t>(y) & 15) == 0 && a.ldy % 8 == 0;
+        const int nl = 16 * (quad & 1) + 8 * (quad >> 1);  // within the two blocks
 #pragma unroll
-        for (int i = 0; i < 2 * NA; ++i) {
+        for (int j = 0; j < 2 * NB; j += 2) {
+            const int n = n0 + wn * 32 * NB + 16 * j + nl;
+            const v4f b0 = *reinterpret_cast<const v4f*>(s_aux + wn * 32 * NB + 16 * j + 4 * quad);
+            const v4f b1 = *reinterpret_cast<const v4f*>(s_aux + wn * 32 * NB + 16 * (j + 1) + 4 * quad);
 #pragma unroll
-            for (int j = 0; j < 8; ++j) {
-                const int nl = 16 * j + 4 * quad;
-                float v[4];
+            for (int i = 0; i < 2 * NA; ++i) {
+                const v4f v0 = acc[i][j], v1 = acc[i][j + 1];
+                uint32_t w[4];
 #pragma unroll
-                for (int e = 0; e < 4; ++e) v[e] = __fadd_rn(acc[i][j][e], s_aux[wn * 128 + nl + e]);
-                *reinterpret_cast<uint2*>(part + row0 * kOutPitch16 + nl * 2) =
-                    make_uint2(f32x2_to_16<OUT>(v[0], v[1]), f32x2_to_16<OUT>(v[2], v[3]));
-            }
-#pragma unroll
-            for (int q = 0; q < 4; ++q) {
-                const int r = 4 * q + quad, m = m0 + rbase + 16 * i + r, n = n0 + wn * 128 + 8 * row0;
-                const uint4 w = *reinterpret_cast<const uint4*>(part + r * kOutPitch16 + 16 * row0);
+                for (int e = 0; e < 2; ++e) {
+                    const auto s = __builtin_amdgcn_permlane16_swap(
+                        f32x2_to_16<OUT>(__fadd_rn(v0[2 * e], b0[2 * e]), __fadd_rn(v0[2 * e + 1], b0[2 * e + 1])),
+                        f32x2_to_16<OUT>(__fadd_rn(v1[2 * e], b1[2 * e]), __fadd_rn(v1[2 * e + 1], b1[2 * e + 1])), false, false);
+                    w[e] = s[0];
+                    w[2 + e] = s[1];
+                }
+                const int m = m0 + rbase + 16 * i + row0;
                 if (m >= a.M || n >= a.N) continue;
                 uint16_t* dst = y + (int64_t)m * a.ldy + n;
                 if (vec && n + 8 <= a.N) {
-                    *reinterpret_cast<uint4*>(dst) = w;
+                    *reinterpret_cast<uint4*>(dst) = make_uint4(w[0], w[1], w[2], w[3]);
                 } else {
-                    const uint32_t u[4] = {w.x, w.y, w.z, w.w};
-                    for (int e = 0; e < 8 && n + e < a.N; ++e) dst[e] = (uint16_t)(u[e >> 1] >> (16 * (e & 1)));
+                    for (int e = 0; e < 8 && n + e < a.N; ++e) dst[e] = (uint16_t)(w[e >> 1] >> (16 * (e & 1)));
                 }
             }
         }
@@ -485,20 +489,16 @@ __global__ __launch_bounds__(256) void k_fp8_tile(Fp8TileArgs a) {
         float* y = static_cast<float*>(a.y);
 #pragma unroll
         for (int i = 0; i < 2 * NA; ++i) {
-            const float w = s_aux[rbase + 16 * i + row0];
+            const int row = rbase + 16 * i + row0, flat = s_flat[row];
+            const float w = s_aux[row];
+            if (flat < 0) continue;
+            float* const to = y + (int64_t)flat * a.ldy + n0 + wn * 32 * NB + 4 * quad;
 #pragma unroll
-            for (int j = 0; j < 8; ++j) {
+            for (int j = 0; j < 2 * NB; ++j) {
                 v4f v;
 #pragma unroll
                 for (int e = 0; e < 4; ++e) v[e] = __fmul_rn(acc[i][j][e], w);
-                *reinterpret_cast<v4f*>(part + row0 * kOutPitch32 + (16 * j + 4 * quad) * 4) = v;
-            }
-#pragma unroll
-            for (int q = 0; q < 8; ++q) {
-                const int r = 2 * q + (el >> 5), n = n0 + wn * 128 + 4 * (el & 31);
-                const v4f v = *reinterpret_cast<const v4f*>(part + r * kOutPitch32 + (el & 31) * 16);
-                const int flat = s_flat[rbase + 16 * i + r];
-                if (flat >= 0 && n < a.N) *reinterpret_cast<v4f*>(y + (int64_t)flat * a.ldy + n) = v;
+                if (n0 + wn * 32 * NB + 16 * j < a.N) *reinterpret_cast<v4f*>(to + 16 * j) = v;
             }
         }
     }

@@ -8,11 +8,11 @@ namespace pdq {
 void launch_fp8_tiles_wide(const Fp8TileArgs& a, int rows, uint32_t tiles, hipStream_t st) {
     const dim3 grid(tiles), block(256);
     if (a.ws_f32) {
-        if (rows == 128) hipLaunchKernelGGL((k_fp8_tile<kGateUp, 0, 2, true, true>), grid, block, 0, st, a);
-        else hipLaunchKernelGGL((k_fp8_tile<kGateUp, 0, 1, true, true>), grid, block, 0, st, a);
+        if (rows == 128) hipLaunchKernelGGL((k_fp8_tile<kGateUp, 0, 2, 4, true, true>), grid, block, 0, st, a);
+        else hipLaunchKernelGGL((k_fp8_tile<kGateUp, 0, 1, 4, true, true>), grid, block, 0, st, a);
     } else {
-        if (rows == 128) hipLaunchKernelGGL((k_fp8_tile<kGateUp, 0, 2, false, true>), grid, block, 0, st, a);
-        else hipLaunchKernelGGL((k_fp8_tile<kGateUp, 0, 1, false, true>), grid, block, 0, st, a);
+        if (rows == 128) hipLaunchKernelGGL((k_fp8_tile<kGateUp, 0, 2, 4, false, true>), grid, block, 0, st, a);
+        else hipLaunchKernelGGL((k_fp8_tile<kGateUp, 0, 1, 4, false, true>), grid, block, 0, st, a);
     }
 }
 

@@ -906,7 +906,7 @@ pdq_status check_fp8_gemm(int64_t M, int64_t K, const uint8_t* wq, const void* w
     if (!scale_ok(scale_t)) return PDQ_ERR_DTYPE;
     PDQ_TRY(check_mk(M, K, K));
     PDQ_TRY(check_stack(1, N, K));
-    // (kMaxThreads: the smallest tiles, 128 x 256, by 256 threads)
+    // (kMaxThreads: tiles of 128 x 256 by 256 threads)
     if (M * N > std::min(kMaxOutputs, kMaxThreads * 128) || ldy < N) return PDQ_ERR_SHAPE;
     if (N > 0 && (!wq || !w_scale)) return PDQ_ERR_NULL;
     if (M > 0 && (!xq || !x_scale)) return PDQ_ERR_NULL;
@@ -935,25 +935,32 @@ Fp8GemmArgs fp8_gemm_args(int64_t M, int64_t K, const uint8_t* wq, const void* w
     return a;
 }
 
-// Rows of a tile of the tiled kernel for an FP8 product, 0: the kernel for few rows.  The estimates are in
-// microseconds for G groups, from times measured on MI355X with 64 .. 1024 rows, N 1024 .. 28672 and K
-// 1408 .. 14336; they are within a quarter of those.  A round of up to 256 tiles takes as long however many
-// tiles it holds; the other kernel's time goes with its workgroups (64 rows x 32 or 64 channels).  E.g.
-// K = 4096 (few rows / 128 / 256 rows a tile): 128 x 28672 48 / 38 / 43, 512 x 28672 148 / 68 / 53,
-// 256 x 4096 14.7 / 30.5 / 42, 1024 x 4096 38 / 29 / 42; 1024 x 14336 -> 4096 106 / 107 / 142.
-int fp8_tile_rows(int64_t M, int64_t N, int64_t G, bool f32) {
-    if (M <= 64) return 0;
-    auto rounds = [&](int64_t rows) {
-        return (double)((((M + rows - 1) / rows) * ((N + 255) / 256) + 255) / 256);
-    };
+// The tile of an FP8 product, 0 rows: the kernel for few rows.  The estimates are in microseconds for G
+// groups, from times measured on MI355X with 64 .. 4096 rows, N 1024 .. 28672 and K 1360 .. 14336; they
+// are within a quarter of those from K = 4096 on.  A round of up to 256 tiles takes as long however many tiles it holds (128 x 128: 512
+// tiles, or 256 for less); the other kernel's time goes with its workgroups (64 rows x 32 or 64 channels).  E.g. K =
+// 4096 (few rows / 128 x 128 / 128 x 256 / 256 x 256): 256 x 4096 12.3 / 14.1 / 21.9 / 38, 512 x 4096 22.6 / 15.5 / 22.5 / 38,
+// 1024 x 4096 40.5 / 18.2 / 24.5 / 39, 128 x 28672 45.6 / 21.7 / 26.2 / 40.5, 2048 x 4096 75 / 35.6 / 29.3 / 41.5, 4096 x 11008 434 /
+// 178 / 163 / 144; 1024 x 14336 -> 4096 109 / 60 / 75 / 112.  Binary32 scales (few rows / 128 x 128 / 128 x 256 / 192 x 256): 1024
+// x 4096 40.8 / 23.5 / 33.0 / 43.9, 2048 x 4096 78 / 36.7 / 37.0 / 46.4, 8192 x 8192 - / 269 / - / 278; 8192 x 14336 -> 4096 - / 543 /
+// - / 506: 128 x 256 is never the best there.
+Fp8TileShape fp8_tile_shape(int64_t M, int64_t N, int64_t G, bool f32) {
+    if (M <= 64) return Fp8TileShape{0, 0};
+    auto tiles = [&](int64_t rows, int64_t channels) { return ((M + rows - 1) / rows) * ((N + channels - 1) / channels); };
+    auto rounds = [&](int64_t rows) { return (double)((tiles(rows, 256) + 255) / 256); };
     const int width = fp8_rows_width(M, N);
     const double groups = (double)(((M + 63) / 64) * ((N + 16 * width - 1) / (16 * width)));
     const double few = 3.5 + G * std::max(1.0, groups / 256) * (width == 4 ? 0.29 : width == 2 ? 0.22 : 0.16);
+    const double one = f32 ? 3.5 + 0.6 * G : 3 + 0.52 * G, two = f32 ? std::max(one + 0.4 * G, 1.2 * G - 3) : one + 0.5 * G;
+    const int64_t small = tiles(128, 128), rest = small % 512;
+    const double t128 = small * 256 > kMaxThreads ? 1e18 : (double)(small / 512) * two + (rest == 0 ? 0 : rest <= 256 ? one : two);
+    const double t128x256 = rounds(128) * (1.5 + 0.95 * G);  // (f32: not there)
     const int large = f32 ? 192 : 256;
-    const double t128 = rounds(128) * (f32 ? 3 + 1.05 * G : 1.5 + 0.95 * G);
-    const double tl = rounds(large) * (f32 ? 6 + 1.35 * G : 4 + 1.4 * G);
-    if (few <= std::min(t128, tl)) return 0;
-    return tl < t128 ? large : 128;
+    const double tl = rounds(large) * (f32 ? std::max(6 + 1.35 * G, 1.5 * G) : 4 + 1.4 * G);
+    const double best = std::min(t128, f32 ? tl : std::min(tl, t128x256));
+    if (few <= best) return Fp8TileShape{0, 0};
+    if (best == tl) return Fp8TileShape{large, 256};
+    return best == t128 ? Fp8TileShape{128, 128} : Fp8TileShape{128, 256};
 }
 
 // The parts of the experts' layer's workspace, in bytes.
@@ -1038,7 +1045,7 @@ pdq_status pdq_quantize_fp8(const void* x, pdq_dtype x_dt, int64_t M, int64_t K,
 
 int pdq_gemm_fp8_tile(int64_t M, int64_t N, int64_t K, pdq_scale_type scale_t) {
     if (M < 1 || N < 1 || K < 1 || M > kMaxRows || N > kMaxRows || K > kMaxK || !scale_ok(scale_t)) return -1;
-    return fp8_tile_rows(M, N, fp8_groups(K), scale_t == PDQ_SCALE_F32);
+    return fp8_tile_shape(M, N, fp8_groups(K), scale_t == PDQ_SCALE_F32).rows;
 }
 
 pdq_status pdq_gemm_fp8(const uint8_t* xq, const uint8_t* x_scale, int64_t M, int64_t K, const uint8_t* wq,
@@ -1046,8 +1053,8 @@ pdq_status pdq_gemm_fp8(const uint8_t* xq, const uint8_t* x_scale, int64_t M, in
                         pdq_dtype y_dt, int64_t ldy, void* stream) {
     PDQ_TRY(check_fp8_gemm(M, K, wq, w_scale, scale_t, bias, N, xq, x_scale, y, y_dt, ldy));
     if (M == 0 || N == 0) return PDQ_OK;
-    const int trows = fp8_tile_rows(M, N, fp8_groups(K), scale_t == PDQ_SCALE_F32);
-    if (trows > 0) {
+    const Fp8TileShape tile = fp8_tile_shape(M, N, fp8_groups(K), scale_t == PDQ_SCALE_F32);
+    if (tile.rows > 0) {
         Fp8TileArgs t{};
         t.x = xq;
         t.xs = x_scale;
@@ -1061,7 +1068,7 @@ pdq_status pdq_gemm_fp8(const uint8_t* xq, const uint8_t* x_scale, int64_t M, in
         t.bias = bias;
         t.y = y;
         t.ldy = ldy;
-        launch_fp8_tiles(t, y_dt, trows, static_cast<hipStream_t>(stream));
+        launch_fp8_tiles(t, y_dt, tile, static_cast<hipStream_t>(stream));
         return launched();
     }
     launch_fp8_rows(fp8_gemm_args(M, K, wq, w_scale, scale_t, bias, N, xq, x_scale, y, ldy), y_dt,

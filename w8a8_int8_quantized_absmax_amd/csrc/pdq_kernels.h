@@ -295,11 +295,16 @@ struct Fp8TileArgs {
     uint8_t* hs;
     int h_pitch;
 };
-// rows of a tile: 256 (e8m0 scales), 192 (binary32 scales), 128, of the experts also 64
-void launch_fp8_tiles(const Fp8TileArgs& a, int out_dt, int rows, hipStream_t st);
-void launch_fp8_tiles_f32(const Fp8TileArgs& a, int epi, int out_dt, int rows, uint32_t tiles, hipStream_t st);
+// 256 x 256 (e8m0 scales), 192 x 256 (binary32 scales), 128 x 256 (e8m0 scales, dense) or 128 x 128.
+struct Fp8TileShape {
+    int rows, channels;
+};
+void launch_fp8_tiles(const Fp8TileArgs& a, int out_dt, Fp8TileShape tile, hipStream_t st);
+// Of the experts: gate and up in tiles of 256 rows (e8m0 scales), 192 (binary32 scales), 128 or 64; wide: 128 or 64.
+void launch_fp8_gate_up_tiles(const Fp8TileArgs& a, bool wide, int rows, hipStream_t st);
+void launch_fp8_down_tiles(const Fp8TileArgs& a, Fp8TileShape tile, hipStream_t st);
+void launch_fp8_tiles_f32(const Fp8TileArgs& a, int epi, int out_dt, Fp8TileShape tile, uint32_t tiles, hipStream_t st);
 void launch_fp8_tiles_wide(const Fp8TileArgs& a, int rows, uint32_t tiles, hipStream_t st);  // gate and up
-void launch_fp8_expert_tiles(const Fp8TileArgs& a, bool gate_up, bool wide, int rows, hipStream_t st);
 
 // The most blocks of 16 rows that `total` rows of `experts` experts take.
 inline int64_t fp8_blocks(int64_t total, int64_t experts) {
