@@ -199,6 +199,26 @@ def test_rows_and_offsets_of_any_content(tokens, experts):
     assert torch.equal(out, y)
 
 
+# ---- every tile of the product, outputs in whole and in single stores ----
+
+@pytest.mark.parametrize("gap", [24, 8, 5])
+@pytest.mark.parametrize("m,n,k,scales,dt", [
+    (1900, 4088, 400, "pow2", "f16"),   # 128 x 256
+    (1100, 2056, 528, "pow2", "bf16"), (1100, 2056, 528, "f32", "f16"),   # 128 x 128
+    (2000, 8184, 272, "pow2", "bf16"), (1500, 8184, 272, "f32", "bf16")])   # 256 x 256, 192 x 256
+def test_linear_tiles(m, n, k, scales, dt, gap):
+    w, wq, ws = weight(n, (), n, k, scales)
+    x = randn(m, m, k).to(DT[dt])
+    bias = 0.1 * randn(n + 1, n)
+    assert pdq.gemm_fp8_tile(m, n, k, w.scale_type) > 0
+    y, untouched = gapped(m, n, DT[dt], gap=gap)
+    pdq.linear_fp8(x.cuda(), w, bias.cuda(), out=y)
+    untouched()
+    rows = np.unique(np.concatenate([np.arange(0, m, max(1, m // 9)), np.arange(max(0, m - 20), m)]))
+    check_linear(y[torch.from_numpy(rows).cuda()], *FO.linear(values(x[rows]), wq, ws, values(bias)), k)
+    assert torch.equal(pdq.linear_fp8(x.cuda(), w, bias.cuda())["y"], y)
+
+
 # ---- seeded random sizes ----
 
 @pytest.mark.parametrize("seed", range(24))
