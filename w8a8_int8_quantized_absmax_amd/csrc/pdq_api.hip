@@ -938,7 +938,8 @@ Fp8GemmArgs fp8_gemm_args(int64_t M, int64_t K, const uint8_t* wq, const void* w
 // The tile of an FP8 product, 0 rows: the kernel for few rows.  The estimates are in microseconds for G
 // groups, from times measured on MI355X with 64 .. 4096 rows, N 1024 .. 28672 and K 1360 .. 14336; they
 // are within a quarter of those from K = 4096 on.  A round of up to 256 tiles takes as long however many tiles it holds (128 x 128: 512
-// tiles, or 256 for less); the other kernel's time goes with its workgroups (64 rows x 32 or 64 channels).  E.g. K =
+// tiles, or 256 for less); the other kernel's goes with its workgroups (64 rows x 32 or 64 channels) by rounds of 256 (400 x
+// 3008 x 4096, 1.3 of them: 23.3 us, 14.2 in tiles; 600 x 2048 x 11008, as many: 40.1, but tiles 51.7).  E.g. K =
 // 4096 (few rows / 128 x 128 / 128 x 256 / 256 x 256): 256 x 4096 12.3 / 14.1 / 21.9 / 38, 512 x 4096 22.6 / 15.5 / 22.5 / 38,
 // 1024 x 4096 40.5 / 18.2 / 24.5 / 39, 128 x 28672 45.6 / 21.7 / 26.2 / 40.5, 2048 x 4096 75 / 35.6 / 29.3 / 41.5, 4096 x 11008 434 /
 // 178 / 163 / 144; 1024 x 14336 -> 4096 109 / 60 / 75 / 112.  Binary32 scales (few rows / 128 x 128 / 128 x 256 / 192 x 256): 1024
@@ -950,7 +951,7 @@ Fp8TileShape fp8_tile_shape(int64_t M, int64_t N, int64_t G, bool f32) {
     auto rounds = [&](int64_t rows) { return (double)((tiles(rows, 256) + 255) / 256); };
     const int width = fp8_rows_width(M, N);
     const double groups = (double)(((M + 63) / 64) * ((N + 16 * width - 1) / (16 * width)));
-    const double few = 3.5 + G * std::max(1.0, groups / 256) * (width == 4 ? 0.29 : width == 2 ? 0.22 : 0.16);
+    const double few = 3.5 + G * std::ceil(groups / 256) * (width == 4 ? 0.29 : width == 2 ? 0.22 : 0.16);
     const double one = f32 ? 3.5 + 0.6 * G : 3 + 0.52 * G, two = f32 ? std::max(one + 0.4 * G, 1.2 * G - 3) : one + 0.5 * G;
     const int64_t small = tiles(128, 128), rest = small % 512;
     const double t128 = small * 256 > kMaxThreads ? 1e18 : (double)(small / 512) * two + (rest == 0 ? 0 : rest <= 256 ? one : two);
