@@ -244,7 +244,7 @@ __global__ __launch_bounds__(256) void k_fp8_gate_up(Fp8ExpertsArgs a) {
     for (int j = 0; j < 2; ++j) {
         const int c = 2 * wave + j;  // chunk of 16 channels in the group
 #pragma unroll
-        for (int r = 0; r < 4; ++r) h[j][r] = fp8_scaled(h[j][r], inv);
+        for (int r = 0; r < 4; ++r) h[j][r] *= inv;  // (whatever a group with a NaN scale holds is NaN)
         *reinterpret_cast<uint32_t*>(hb + (c >> 2) * kWBlock + fp8_pos(row, c & 3) + 4 * (lane >> 4)) =
             fp8_pack4(h[j][0], h[j][1], h[j][2], h[j][3]);
     }

@@ -41,10 +41,6 @@ __device__ __forceinline__ uint32_t fp8_scale_byte(uint32_t top) {
 // whose codes are zeros.
 __device__ __forceinline__ float fp8_inverse(uint32_t b) { return b == 255u ? 0.0f : __uint_as_float((254u - b) << 23); }
 
-// x / S of a group without NaN scale; a group with one holds infinities or NaN,
-// whose product with 0 is not 0.
-__device__ __forceinline__ float fp8_scaled(float x, float inv) { return inv == 0.0f ? 0.0f : x * inv; }
-
 // Four codes, rounded to nearest even (v_cvt_pk_fp8_f32; |v| <= 448).
 __device__ __forceinline__ uint32_t fp8_pack4(float a, float b, float c, float d) {
     int r = __builtin_amdgcn_cvt_pk_fp8_f32(a, b, 0, false);
@@ -67,6 +63,21 @@ __device__ __forceinline__ uint32_t row16_max(uint32_t v) {
 // The larger magnitude, NaN if one is.
 __device__ __forceinline__ float larger(float a, float b) { return __builtin_elementwise_maximum(fabsf(a), fabsf(b)); }
 __device__ __forceinline__ uint32_t magnitude(float x) { return __float_as_uint(x) & 0x7fffffffu; }
+
+// The bits of the largest magnitude of eight values (maxima of three that keep a NaN: four instructions), and their
+// codes at scale byte b.
+__device__ __forceinline__ uint32_t fp8_top8(const float (&v)[8]) {
+    float m = larger(v[0], v[1]);
+#pragma unroll
+    for (int j = 2; j < 8; ++j) m = larger(m, v[j]);
+    return magnitude(m);
+}
+__device__ __forceinline__ uint2 fp8_code8(const float (&v)[8], uint32_t b) {
+    const float inv = fp8_inverse(b);
+    const uint2 c = make_uint2(fp8_pack4(v[0] * inv, v[1] * inv, v[2] * inv, v[3] * inv),
+                               fp8_pack4(v[4] * inv, v[5] * inv, v[6] * inv, v[7] * inv));
+    return b == 255u ? make_uint2(0, 0) : c;  // (infinities and NaN times 0 are not 0)
+}
 
 // A lane's 32 bytes of a fragment of 16 rows x 128 K values: row lane % 16, the
 // chunk lane / 16 of each of the two blocks.  The order of K values within a
@@ -149,15 +160,8 @@ __device__ __forceinline__ void fp8_code_rows(const void* x, int64_t ldx, int ro
             if (p0 + u * each >= pieces) break;  // (the same in the 16 lanes)
             float v[8];
             widen8<DT>(raw[u], v);
-            uint32_t top = 0;
-#pragma unroll
-            for (int j = 0; j < 8; ++j) top = max(top, magnitude(v[j]));
-            const uint32_t b = fp8_scale_byte(row16_max(top));
-            const float inv = fp8_inverse(b);
-#pragma unroll
-            for (int j = 0; j < 8; ++j) v[j] = fp8_scaled(v[j], inv);
-            *reinterpret_cast<uint2*>(codes + m[u] * pitch + g[u] * kGroup + c8 * 8) =
-                make_uint2(fp8_pack4(v[0], v[1], v[2], v[3]), fp8_pack4(v[4], v[5], v[6], v[7]));
+            const uint32_t b = fp8_scale_byte(row16_max(fp8_top8(v)));
+            *reinterpret_cast<uint2*>(codes + m[u] * pitch + g[u] * kGroup + c8 * 8) = fp8_code8(v, b);
             if (c8 == 0) scales[m[u] * groups + g[u]] = (uint8_t)b;
         }
     }

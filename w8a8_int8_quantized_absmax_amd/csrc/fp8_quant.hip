@@ -50,16 +50,10 @@ __global__ __launch_bounds__(256) void k_fp8_quant(Fp8QuantArgs a) {
         if (g0 + i >= a.groups) break;
         float v[8];
         widen8<DT>(raw[i], v);
-        uint32_t top = 0;
-#pragma unroll
-        for (int j = 0; j < 8; ++j) top = max(top, magnitude(v[j]));
-        const uint32_t b = fp8_scale_byte(row16_max(top));
-        const float inv = fp8_inverse(b);
-#pragma unroll
-        for (int j = 0; j < 8; ++j) v[j] = fp8_scaled(v[j], inv);
+        const uint32_t b = fp8_scale_byte(row16_max(fp8_top8(v)));
         const int c16 = c8 >> 1;
         *reinterpret_cast<uint2*>(image + i * kGroupBytes + (c16 >> 2) * kWBlock + fp8_pos(r, c16 & 3) + 8 * (c8 & 1)) =
-            make_uint2(fp8_pack4(v[0], v[1], v[2], v[3]), fp8_pack4(v[4], v[5], v[6], v[7]));
+            fp8_code8(v, b);
         scales |= b << (8 * i);
     }
     if (c8 == 0 && (a.sorted.offsets || row < a.M))
@@ -96,8 +90,7 @@ __global__ __launch_bounds__(256) void k_fp8_weight(Fp8WeightArgs a) {
     for (int i = 0; i < 8; ++i) {
         float v[8];
         widen8<DT>(raw[i], v);
-#pragma unroll
-        for (int j = 0; j < 8; ++j) top = max(top, magnitude(v[j]));
+        top = max(top, fp8_top8(v));
     }
     top = row16_max(top);
     top = max(top, (uint32_t)__shfl_xor((int)top, 16));
@@ -105,7 +98,6 @@ __global__ __launch_bounds__(256) void k_fp8_weight(Fp8WeightArgs a) {
     if ((threadIdx.x & 63) == 0) tops[threadIdx.x >> 6] = top;
     __syncthreads();
     const uint32_t b = fp8_scale_byte(max(max(tops[0], tops[1]), max(tops[2], tops[3])));
-    const float inv = fp8_inverse(b);
     const int64_t ngroups = (a.N + 15) / 16;
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
@@ -113,12 +105,9 @@ __global__ __launch_bounds__(256) void k_fp8_weight(Fp8WeightArgs a) {
         if (g16 >= ngroups) break;
         float v[8];
         widen8<DT>(raw[i], v);
-#pragma unroll
-        for (int j = 0; j < 8; ++j) v[j] = fp8_scaled(v[j], inv);
         const int c16 = c8 >> 1;
         uint8_t* blk = a.q + ((mat * ngroups + g16) * groups + g) * kGroupBytes + (c16 >> 2) * kWBlock;
-        *reinterpret_cast<uint2*>(blk + fp8_pos(r16, c16 & 3) + 8 * (c8 & 1)) =
-            make_uint2(fp8_pack4(v[0], v[1], v[2], v[3]), fp8_pack4(v[4], v[5], v[6], v[7]));
+        *reinterpret_cast<uint2*>(blk + fp8_pos(r16, c16 & 3) + 8 * (c8 & 1)) = fp8_code8(v, b);
     }
     // the row's padding up to the pitch: scales of 1
     uint8_t* s = a.scale + (mat * nblocks + nb) * pitch;
