@@ -28,9 +28,10 @@ __device__ __forceinline__ BlockScale<F32S> block_scale(const void* s, int64_t a
 template <bool F32S>
 __device__ __forceinline__ v4f mac16(v8i w, v8i x, v4f c, BlockScale<F32S> s, uint32_t sx) {
     if constexpr (F32S) {
-        const v4f p = fp8_mfma16(w, x, v4f{}, 127, sx);
+        const Fp8Split both = fp8_split(s.f);
+        const v4f p = fp8_mfma16(w, x, v4f{}, both.b, sx);
 #pragma unroll
-        for (int r = 0; r < 4; ++r) c[r] = __fmaf_rn(p[r], s.f, c[r]);
+        for (int r = 0; r < 4; ++r) c[r] = __fmaf_rn(p[r], both.f, c[r]);
         return c;
     } else {
         return fp8_mfma16(w, x, c, s.b, sx);

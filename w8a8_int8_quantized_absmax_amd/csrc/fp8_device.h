@@ -131,6 +131,18 @@ __device__ __forceinline__ v4f fp8_mfma16_wide(const Fp8Wide& w, const Fp8Wide& 
     return c;
 }
 
+// A binary32 scale as a power of two in the e8m0 format, an operand of the matrix instruction, and the factor that is left, 1 to
+// 2 (less for scales below 2^-126): S_x times a sum of codes alone may pass 2^128 where the result does not.  Exact for
+// every value; infinities and NaN stay in the factor, and so does 0.
+struct Fp8Split {
+    float f;
+    int b;
+};
+__device__ __forceinline__ Fp8Split fp8_split(float s) {
+    const int e = (int)(__float_as_uint(s) >> 23 & 255u), b = e == 255 ? 127 : e;
+    return Fp8Split{__builtin_ldexpf(s, 127 - b), b};
+}
+
 // What an e8m0 byte stands for.
 __device__ __forceinline__ float fp8_scale_value(uint32_t b) {
     return __uint_as_float(b == 255u ? 0x7fc00000u : b == 0u ? 0x00400000u : b << 23);

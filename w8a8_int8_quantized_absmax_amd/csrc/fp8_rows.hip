@@ -10,8 +10,8 @@
 // activation rows; its four wavefronts take the groups in turn, and a group of 16
 // channels is one contiguous 2 KB run of the packed weight, which lane by lane is
 // the operand of one 16x16x128 product: no LDS before the sum of the four partial
-// results.  The e8m0 scales go into the product itself; binary32 block scales
-// multiply its result, one multiply-add a value.
+// results.  The e8m0 scales go into the product itself, of binary32 block scales the
+// exponents; what is left of those multiplies its result, one multiply-add a value.
 
 #include "fp8_device.h"
 
@@ -86,14 +86,15 @@ __global__ __launch_bounds__(64 * W) void k_fp8_rows(Fp8GemmArgs a) {
 #pragma unroll
         for (int j = 0; j < MB; ++j) acc[i][j] = v4f{};
     auto add = [&](const Step<NG, MB, F32S, FUSED>& s) {
+        const Fp8Split sw = F32S ? fp8_split(s.sw) : Fp8Split{};
 #pragma unroll
         for (int i = 0; i < NG; ++i)
 #pragma unroll
             for (int j = 0; j < MB; ++j) {
                 if constexpr (F32S) {
-                    const v4f p = fp8_mfma16(s.w[i], s.x[j], v4f{}, 127, s.sx[j]);
+                    const v4f p = fp8_mfma16(s.w[i], s.x[j], v4f{}, sw.b, s.sx[j]);
 #pragma unroll
-                    for (int r = 0; r < 4; ++r) acc[i][j][r] = __fmaf_rn(p[r], s.sw, acc[i][j][r]);
+                    for (int r = 0; r < 4; ++r) acc[i][j][r] = __fmaf_rn(p[r], sw.f, acc[i][j][r]);
                 } else {
                     acc[i][j] = fp8_mfma16(s.w[i], s.x[j], acc[i][j], s.swb, s.sx[j]);
                 }

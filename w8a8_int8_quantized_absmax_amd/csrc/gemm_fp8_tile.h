@@ -90,8 +90,8 @@ enum { kDense = 0, kGateUp = 1, kDown = 2 };
 // halves of a wavefront's channels, so that a lane holds both of a channel, and h's codes come
 // out; kDown: weighted binary32 rows at their token and slot.
 //
-// F32S: binary32 block scales.  A group's product then has a scale of its own to be multiplied by,
-// a multiply-add a value, which takes half of the vector unit's time.  The accumulators are in
+// F32S: binary32 block scales.  Their exponents go into the product (fp8_split), and what is left, 1 to 2, multiplies a group's
+// product, a multiply-add a value, which takes half of the vector unit's time.  The accumulators are in
 // vector registers (NA at most 3: 192 of 256), the products' results wait kLag products for theirs.  (With
 // NA = NB = 2 one workgroup multiplies while the other adds: 1024 x 4096 x 4096 in 23 us where 128 x 256 took 33.)
 //
@@ -227,24 +227,30 @@ __global__ __launch_bounds__(256, NB == 4 ? 1 : 2) void k_fp8_tile(Fp8TileArgs a
             *reinterpret_cast<const v4i*>(regionB(buf, half) + (wn * NB + (q >> 1)) * kGroupBytes + (q & 1) * kWBlock + off);
     };
     auto whole = [](const v4i (&f)[2]) { return v8i{f[0][0], f[0][1], f[0][2], f[0][3], f[1][0], f[1][1], f[1][2], f[1][3]}; };
-    int sx[8], sw[2];
+    int sx[8], sw[2] = {0, 0};
     auto read_scales = [&](int g) {  // of steps g and g + 1 (g even) in the low bytes
         const int shift = 8 * (g & 2), width = g + 1 < G ? 16 : 8;
         auto two = [&](uint32_t four) { return (int)__builtin_amdgcn_ubfe(four, shift, width); };
 #pragma unroll
         for (int i = 0; i < 2 * NA; ++i) sx[i] = two(sc[(wm * 2 * NA + i) * 16 + (lane & 15)]);
-        if constexpr (F32S) {
-            sw[0] = sw[1] = 0x7f7f;
-        } else {
+        if constexpr (!F32S) {
             sw[0] = two(sc[256 + wave * 64 + (EPI == kGateUp ? 0 : wn)]);
             sw[1] = EPI == kGateUp ? two(sc[256 + wave * 64 + 1]) : sw[0];
         }
     };
-    // F32S: the scales of step g of the wavefront's halves of channels, and of the step before
+    // F32S: the scales (their factors: fp8_split) of step g of the wavefront's halves of channels, and of the step before
     float ws[2] = {0.0f, 0.0f}, before[2] = {0.0f, 0.0f}, next[2][2];
     const float* pf[2];
 #pragma unroll
     for (int h = 0; h < 2; ++h) pf[h] = static_cast<const float*>(a.ws) + (F32S ? scale_row(EPI == kGateUp ? h : wn) : 0);
+    // The next step's, split between this one's products, the factors in scalar registers: with vector registers in each
+    // multiply-add 8192 x 14336 -> 4096 takes 515 us instead of 502.
+    Fp8Split ahead[2] = {};
+    auto split_ahead = [&](int s, int h) {
+        const Fp8Split split = fp8_split(next[s][h]);
+        ahead[h].f = __int_as_float(__builtin_amdgcn_readfirstlane(__float_as_int(split.f)));
+        ahead[h].b = split.b;
+    };
     auto fetch_f32 = [&](int g) {  // g even; a group beyond the last counts nothing
         const int at = min(g, G - 1) & ~1;
 #pragma unroll
@@ -266,7 +272,11 @@ __global__ __launch_bounds__(256, NB == 4 ? 1 : 2) void k_fp8_tile(Fp8TileArgs a
     for (int q = 0; q < kLoads; ++q) issue(I1{}, I1{}, I0{}, 1, q);
     wait_loads_and_sync<3 * kLoads>();
     read_scales(0);
-    if constexpr (F32S) fetch_f32(0);
+    if constexpr (F32S) {
+        fetch_f32(0);
+#pragma unroll
+        for (int h = 0; h < 2; ++h) split_ahead(0, h);
+    }
 #pragma unroll
     for (int q = 0; q < 2 * NA; ++q) read_a(I0{}, I0{}, q);
 #pragma unroll
@@ -369,7 +379,12 @@ __global__ __launch_bounds__(256, NB == 4 ? 1 : 2) void k_fp8_tile(Fp8TileArgs a
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
                 before[h] = ws[h];
-                ws[h] = next[s][h];
+                if constexpr (WIDE) {
+                    ws[h] = next[s][h];
+                } else {
+                    ws[h] = ahead[h].f;
+                    sw[h] = ahead[h].b << 8 * s;
+                }
             }
             if constexpr (s == 1) fetch_f32(g + 1);
         }
@@ -379,7 +394,11 @@ __global__ __launch_bounds__(256, NB == 4 ? 1 : 2) void k_fp8_tile(Fp8TileArgs a
                  issue(Buf{}, I0{}, F{}, g + 2, q);
              },
              [&](int q) { read_b(Buf{}, O{}, q); }, ReadsB{}, [&](int q) { read_a(Buf{}, I1{}, q); }, ReadsA{});
-        half(I1{}, O{}, S, [&](int q) { issue(Buf{}, I1{}, O{}, g + 2, q); },
+        half(I1{}, O{}, S,
+             [&](int q) {
+                 if (F32S && !WIDE && q < 2) split_ahead(1 - s, q);  // of the next step, between products
+                 issue(Buf{}, I1{}, O{}, g + 2, q);
+             },
              [&](int q) { read_a(Nxt{}, I0{}, q); }, ReadsA{}, [&](int q) { read_b(Nxt{}, O{}, q); }, ReadsB{});
         if constexpr (s == 1) read_scales(g + 1);
     };
