@@ -4,7 +4,7 @@ import pytest
 import torch
 
 import oracle.fp8_oracle as FO
-from fp8_cases import check_linear, randn, values, weight
+from fp8_cases import DT, check_linear, randn, values, weight
 from test_gpu_experts import check
 from w8a8_int8_quantized_absmax_amd import pdq
 
@@ -74,6 +74,26 @@ def test_experts(tokens, experts, k, scales):
     gate_up = scaled(gate_up, by)
     down = scaled(weight(tokens + 1, (experts,), hidden, inner, scales)[0], 2.0 ** -100)
     x = (randn(tokens + 2, tokens, hidden).clamp(-3.5, 3.5) * 2.0 ** 118).bfloat16()
+    r = pdq.route_experts(randn(tokens + 3, tokens, experts, spread=0.0).cuda(), k)
+    y = pdq.experts_fp8(x.cuda(), r, gate_up[0], down[0])["y"]
+    check(y, x, r, gate_up, down)
+
+
+@pytest.mark.parametrize("scales", ["pow2", "f32"])
+@pytest.mark.parametrize("dt,up,by", [("bf16", 125, 40), ("f16", 13, 126)])
+@pytest.mark.parametrize("tokens,experts,k", [(1, 4, 2), (4, 2, 2), (20, 8, 2), (40, 4, 2), (200, 2, 2), (400, 2, 2)])
+def test_blocks_of_zeros(tokens, experts, k, dt, up, by, scales):
+    """Blocks of zero codes under a scale that passes 2^128 with the rows': they add nothing."""
+    hidden, inner = 400, 272
+    g = weight(tokens, (experts, 2), inner, hidden, scales)[0]
+    codes, s = g.codes(), g.scales()
+    codes.view(torch.uint8)[..., 128:256] = 0
+    s[..., 1] = 2.0 ** by
+    s[:, :, :, [0, 2, 3]] *= 2.0 ** -up
+    g = pdq.pack_weight_fp8(codes, (s if scales == "f32" else s.to(torch.float8_e8m0fnu)).contiguous())
+    gate_up = g, g.codes().cpu().double().numpy(), g.scales().cpu().double().numpy()
+    down = weight(tokens + 1, (experts,), hidden, inner, scales)
+    x = (randn(tokens + 2, tokens, hidden).clamp(-3.5, 3.5) * 2.0 ** up).to(DT[dt])
     r = pdq.route_experts(randn(tokens + 3, tokens, experts, spread=0.0).cuda(), k)
     y = pdq.experts_fp8(x.cuda(), r, gate_up[0], down[0])["y"]
     check(y, x, r, gate_up, down)

@@ -39,10 +39,11 @@ __device__ __forceinline__ v4f mac16(v8i w, v8i x, v4f c, BlockScale<F32S> s, ui
 }
 
 // What gate and up are made of in the kernels that the weight's bytes bound: a difference of their last
-// bits moves some of h's codes, by a step each, so that every bit of the sum counts.
+// bits moves some of h's codes, by a step each, so that every bit of the sum counts.  x: widened by fp8_by of its scale, sx:
+// what is left of that.
 template <bool F32S>
 __device__ __forceinline__ v4f mac16_wide(v8i w, const Fp8Wide& x, v4f c, BlockScale<F32S> s, float sx) {
-    const v4f p = fp8_mfma16_wide(fp8_widen(w), x);
+    const v4f p = fp8_mfma16_wide(fp8_widen(w, 1.0f), x);
     const float both = __fmul_rn(sx, F32S ? s.f : fp8_scale_value(s.b));
 #pragma unroll
     for (int r = 0; r < 4; ++r) c[r] = __fmaf_rn(p[r], both, c[r]);
@@ -97,10 +98,10 @@ __global__ __launch_bounds__(256) void k_fp8_gate_up_direct(Fp8ExpertsArgs a) {
         for (int u = 0; u < U; ++u) {
             const int g = g0 + 4 * u;
             if (g >= G) break;
-            const Fp8Wide x = fp8_widen(fp8_row_fragment(codes, g, lane));
-            const float sx = fp8_scale_value(scales[g]);
+            const Fp8By sx = fp8_by(scales[g]);
+            const Fp8Wide x = fp8_widen(fp8_row_fragment(codes, g, lane), sx.by);
 #pragma unroll
-            for (int i = 0; i < 2; ++i) acc[i] = mac16_wide<F32S>(w[set][u][i], x, acc[i], s[set][u][i], sx);
+            for (int i = 0; i < 2; ++i) acc[i] = mac16_wide<F32S>(w[set][u][i], x, acc[i], s[set][u][i], sx.rest);
         }
     };
     for (int g = wave; g < G; g += 8 * U) {
@@ -210,14 +211,14 @@ __global__ __launch_bounds__(256) void k_fp8_gate_up(Fp8ExpertsArgs a) {
         }
     }
     for (int g = 0; g < G; ++g) {
-        const Fp8Wide x = fp8_widen(fp8_fragment(xb + (int64_t)g * kGroupBytes, lane));
-        const float sx = fp8_scale_value(xs[g]);
+        const Fp8By sx = fp8_by(xs[g]);
+        const Fp8Wide x = fp8_widen(fp8_fragment(xb + (int64_t)g * kGroupBytes, lane), sx.by);
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
             const BlockScale<F32S> s = block_scale<F32S>(a.gate_up_s, srow[i] + g);
 #pragma unroll
             for (int j = 0; j < 2; ++j)
-                acc[i][j] = mac16_wide<F32S>(fp8_fragment(wp[i][j] + (int64_t)g * kGroupBytes, lane), x, acc[i][j], s, sx);
+                acc[i][j] = mac16_wide<F32S>(fp8_fragment(wp[i][j] + (int64_t)g * kGroupBytes, lane), x, acc[i][j], s, sx.rest);
         }
     }
 #pragma unroll

@@ -290,6 +290,9 @@ __global__ __launch_bounds__(256, NB == 4 ? 1 : 2) void k_fp8_tile(Fp8TileArgs a
     constexpr int kLag = 4, kRing = 8;
     v4f part_sum[kRing];  // WIDE: [row % 2][channels' block]
     v8bf wide_b[4][4];
+    // Of binary16 rows S_x is 2^-33 to 2^8.  Its codes are widened by 2^16, which its scale lacks then: so no S_x S_w
+    // passes 2^128 where the sum is 0.
+    constexpr uint32_t kWideBy = 16;
     float both[2];
 #pragma unroll
     for (int q = 0; q < kRing; ++q) part_sum[q] = v4f{};
@@ -312,15 +315,16 @@ __global__ __launch_bounds__(256, NB == 4 ? 1 : 2) void k_fp8_tile(Fp8TileArgs a
                 const int at = i & 1;
                 if (j == 0) {
                     const uint32_t byte = (uint32_t)sx[ha * NA + i] >> 8 * kByte & 255;
-                    const float w = F32S ? ws[hb] : fp8_scale_value((uint32_t)sw[hb] >> 8 * kByte & 255);
-                    both[at] = __fmul_rn(fp8_scale_value(byte), w);
+                    // (byte 0: the group behind an odd last one)
+                    const float s = __uint_as_float(byte == 255u ? 0x7fc00000u : __builtin_elementwise_sub_sat(byte, kWideBy) << 23);
+                    both[at] = __fmul_rn(s, ws[hb]);
                 }
                 if (i == 0 && !(ha == 1 && q < L)) {  // (those of the quadrant before are the same ones)
 #pragma unroll
                     for (int b = 0; b < 4; ++b)
-                        wide_b[b][j] = fp8_widen8(fb[hb][b][j >> 1][2 * (j & 1)], fb[hb][b][j >> 1][2 * (j & 1) + 1]);
+                        wide_b[b][j] = fp8_widen8(fb[hb][b][j >> 1][2 * (j & 1)], fb[hb][b][j >> 1][2 * (j & 1) + 1], 1.0f);
                 }
-                const v8bf wide_a = fp8_widen8(fa[ha][i][j >> 1][2 * (j & 1)], fa[ha][i][j >> 1][2 * (j & 1) + 1]);
+                const v8bf wide_a = fp8_widen8(fa[ha][i][j >> 1][2 * (j & 1)], fa[ha][i][j >> 1][2 * (j & 1) + 1], (float)(1 << kWideBy));
 #pragma unroll
                 for (int b = 0; b < 4; ++b) {
                     v4f& to = part_sum[at * 4 + b];
@@ -375,6 +379,10 @@ __global__ __launch_bounds__(256, NB == 4 ? 1 : 2) void k_fp8_tile(Fp8TileArgs a
         using O = std::integral_constant<int, (s + 1) & 1>;  // the other, the next step's first
         using ReadsA = std::integral_constant<int, 2 * NA>;
         using ReadsB = std::integral_constant<int, 2 * NB>;
+        if constexpr (WIDE && !F32S) {
+#pragma unroll
+            for (int h = 0; h < 2; ++h) ws[h] = fp8_scale_value((uint32_t)sw[h] >> 8 * s & 255);
+        }
         if constexpr (F32S) {
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
