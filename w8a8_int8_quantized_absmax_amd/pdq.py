@@ -10,6 +10,7 @@ from __future__ import annotations
 
 import ctypes
 import functools
+import operator
 import os
 import re
 
@@ -1131,11 +1132,22 @@ def route_workspace_bytes(tokens: int, experts: int) -> int:
 
 
 @functools.lru_cache(maxsize=256)
-def _route_rule(score, k, groups, top_groups, group_score, renormalize, scale):
+def _rule_struct(score, k, groups, top_groups, group_score, renormalize, scale):
     if score not in _SCORES:
         raise ValueError(f"score must be one of {sorted(_SCORES)}")
-    c = _RouteRuleC(_SCORES[score], k, groups, top_groups, group_score, 1 if renormalize else 0, scale)
+    for v in (k, groups, top_groups, group_score):
+        if not -2 ** 31 <= v < 2 ** 31:  # (the C struct's fields would lose the upper bits)
+            raise ValueError(f"{v} in a routing rule")
+    c = _RouteRuleC(_SCORES[score], k, groups, top_groups, group_score, renormalize, scale)
     return c, ctypes.byref(c)
+
+
+def _route_rule(score, k, groups, top_groups, group_score, renormalize, scale):
+    """The rule as a C struct, kept by the values alone: an object that is passed for one (a tensor) may change."""
+    if not (type(k) is type(groups) is type(top_groups) is type(group_score) is int and type(scale) is float):
+        k, groups, top_groups, group_score = map(operator.index, (k, groups, top_groups, group_score))
+        scale = float(scale)
+    return _rule_struct(score, k, groups, top_groups, group_score, 1 if renormalize else 0, scale)
 
 
 def route_experts(logits, k: int, score: str = "softmax", bias=None, groups: int = 1, top_groups: int = 1,
@@ -1154,6 +1166,7 @@ def route_experts(logits, k: int, score: str = "softmax", bias=None, groups: int
         _check_dense(bias, "bias", torch.float32, (experts,))
         if bias.get_device() != index:
             raise ValueError("bias must be on logits' device")
+    k = operator.index(k)
     if not 1 <= k <= experts:
         raise ValueError(f"k = {k} of {experts} experts")
     rule = _route_rule(score, k, groups, top_groups, group_score, renormalize, scale)
