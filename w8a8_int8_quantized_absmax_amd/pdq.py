@@ -613,6 +613,23 @@ def _check_dense(t, name, dtype, shape=None):
         raise ValueError(f"{name} has shape {tuple(t.shape)}, {tuple(shape)} needed")
 
 
+class _Fixed:
+    """Objects whose calls go by the addresses and sizes that were checked when they were made: an attribute set afterwards
+    would change neither.  (In place their tensors may change; what makes such an object sets it by _put.)"""
+
+    __slots__ = ()
+
+    def __setattr__(self, name, value):
+        raise AttributeError(f"{type(self).__name__}.{name} cannot be set: its calls go by what it was made of; make another")
+
+    def __delattr__(self, name):
+        raise AttributeError(f"{type(self).__name__}.{name} cannot be deleted")
+
+    def _put(self, **values):
+        for name, value in values.items():
+            object.__setattr__(self, name, value)
+
+
 class KVCache:
     """A pool of pages of the INT8 key/value cache (include/pdq.h, pdq_kv_cache).
 
@@ -839,7 +856,7 @@ def _fp8_unpack(data: torch.Tensor, count: int, n: int, k: int) -> torch.Tensor:
     return rows[:, :n, :k].contiguous().view(torch.float8_e4m3fn)
 
 
-class WeightFP8:
+class WeightFP8(_Fixed):
     """FP8 weights with a scale for each block of 128 x 128 (include/pdq.h): one [n, k]
     matrix, or a stack of them with the leading dimensions `lead`.
 
@@ -861,10 +878,9 @@ class WeightFP8:
             raise ValueError(f"data holds {data.numel()} bytes, {count} packed {n} x {k} weights need {count * size}")
         if data.device != scale.device:
             raise ValueError("the weight's tensors must be on one device")
-        self.data, self.scale, self.n, self.k, self.lead = data, scale, int(n), int(k), tuple(scale.shape[:-2])
-        self.scale_type = SCALE_F32 if scale.dtype == torch.float32 else E8M0
-        self.device, self.index = data.device, data.get_device()
-        self.at, self.scale_at = data.data_ptr(), scale.data_ptr()
+        self._put(data=data, scale=scale, n=int(n), k=int(k), lead=tuple(scale.shape[:-2]),
+                  scale_type=SCALE_F32 if scale.dtype == torch.float32 else E8M0, device=data.device,
+                  index=data.get_device(), at=data.data_ptr(), scale_at=scale.data_ptr())
 
     @property
     def shape(self):
@@ -882,21 +898,22 @@ class WeightFP8:
         return self.scale.float()[..., :(self.k + 127) // 128]
 
 
-class CodesFP8:
+class _CodesFP8Parts:  # (what quantize_fp8 fills: a plain attribute costs the host a third of _put's)
+    __slots__ = ("buffer", "rows", "k", "size", "pitch", "index")
+
+
+class CodesFP8(_Fixed, _CodesFP8Parts):
     """FP8 activation codes of a [rows, k] matrix, packed, and their groups' e8m0 scales behind them,
     in one buffer (16-byte aligned)."""
 
-    __slots__ = ("buffer", "rows", "k", "size", "pitch", "index")
+    __slots__ = ()
 
     def __init__(self, buffer: torch.Tensor, rows: int, k: int):
         size, pitch = _fp8_sizes(rows, k)
         if not buffer.is_cuda or not buffer.is_contiguous() or buffer.nbytes < size + rows * pitch:
             raise ValueError(f"packed {rows} x {k} codes with their scales need a contiguous device tensor of "
                              f"{size + rows * pitch} bytes")
-        self._take(buffer, rows, k, size, pitch, buffer.get_device())
-
-    def _take(self, buffer, rows, k, size, pitch, index):
-        self.buffer, self.rows, self.k, self.size, self.pitch, self.index = buffer, rows, k, size, pitch, index
+        self._put(buffer=buffer, rows=rows, k=k, size=size, pitch=pitch, index=buffer.get_device())
 
     @property
     def shape(self):
@@ -925,8 +942,10 @@ class CodesFP8:
 def _codes_fp8(like, m, k, index):
     """New codes of a [m, k] matrix, in like's dtype (a new tensor of another one costs the host more)."""
     size, pitch = _fp8_sizes(m, k)
-    c = CodesFP8.__new__(CodesFP8)
-    c._take(like.new_empty((size + m * pitch + 3) // like.element_size() + 1), m, k, size, pitch, index)
+    c = _CodesFP8Parts()
+    c.buffer, c.rows, c.k = like.new_empty((size + m * pitch + 3) // like.element_size() + 1), m, k
+    c.size, c.pitch, c.index = size, pitch, index
+    c.__class__ = CodesFP8
     return c
 
 
@@ -1075,12 +1094,16 @@ class _ExpertsC(ctypes.Structure):
                 ("experts", _i64), ("hidden", _i64), ("inner", _i64)]
 
 
-class Routing:
+class _RoutingParts:
+    __slots__ = ("_tensors", "_buffer", "tokens", "experts", "k", "index", "_at", "_c")
+
+
+class Routing(_Fixed, _RoutingParts):
     """The experts of each token (include/pdq.h, pdq_route_experts): ids int32 and weights float32
     [tokens, k]; the rows token * k + slot sorted by expert: offsets int32 [experts + 1], rows int32
     [tokens * k]."""
 
-    __slots__ = ("_tensors", "_buffer", "tokens", "experts", "k", "index", "_at", "_c")
+    __slots__ = ()
 
     def __init__(self, ids: torch.Tensor, weights: torch.Tensor, offsets: torch.Tensor, rows: torch.Tensor):
         if ids.dim() != 2 or offsets.dim() != 1 or offsets.shape[0] < 2:
@@ -1092,21 +1115,21 @@ class Routing:
         _check_dense(rows, "rows", torch.int32, (tokens * k,))
         if not ids.device == weights.device == offsets.device == rows.device:
             raise ValueError("the routing's tensors must be on one device")
-        self._tensors, self._buffer = (ids, weights, offsets, rows), None
-        self.tokens, self.experts, self.k, self.index = tokens, offsets.shape[0] - 1, k, ids.get_device()
-        self._at, self._c = tuple(t.data_ptr() for t in self._tensors), None
+        tensors = (ids, weights, offsets, rows)
+        self._put(_tensors=tensors, _buffer=None, tokens=tokens, experts=offsets.shape[0] - 1, k=k, index=ids.get_device(),
+                  _at=tuple(t.data_ptr() for t in tensors), _c=None)
 
     def _ref(self):
         if self._c is None:
-            self._c = _RoutingC(*self._at, self.tokens, self.experts, self.k)
+            self._put(_c=_RoutingC(*self._at, self.tokens, self.experts, self.k))
         return ctypes.byref(self._c)
 
     def _all(self):
         if self._tensors is None:  # parts of route_experts' one buffer, as tensors when they are asked for
             n, e = self.tokens * self.k, self.experts + 1
             ids, weights, rows, offsets, _ = self._buffer.split((n, n, n, e, self._buffer.shape[0] - 3 * n - e))
-            self._tensors = (ids.view(self.tokens, self.k), weights.view(torch.float32).view(self.tokens, self.k),
-                             offsets, rows)
+            self._put(_tensors=(ids.view(self.tokens, self.k), weights.view(torch.float32).view(self.tokens, self.k),
+                                offsets, rows))
         return self._tensors
 
     @property
@@ -1185,9 +1208,10 @@ def route_experts(logits, k: int, score: str = "softmax", bias=None, groups: int
     offsets = at + 12 * n
     _kv_call("pdq_route_experts", index, logits.data_ptr(), _DT[kind], tokens, experts, ldl,
              bias.data_ptr() if bias is not None else None, rule[1], at, at + 4 * n, offsets, at + 8 * n, ws, size)
-    r = Routing.__new__(Routing)
+    r = _RoutingParts()
     r._tensors, r._buffer, r.tokens, r.experts, r.k, r.index = None, buffer, tokens, experts, k, index
     r._at, r._c = (at, at + 4 * n, offsets, at + 8 * n), None
+    r.__class__ = Routing
     return r
 
 
