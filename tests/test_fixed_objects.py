@@ -22,6 +22,11 @@ def test_no_attribute_can_be_set(cls):
         delattr(o, names[0])
 
 
+@pytest.mark.parametrize("cls", [pdq.KVCache, pdq.KVBatch])
+def test_no_attribute_of_a_cache_can_be_set(cls):
+    test_no_attribute_can_be_set(cls)
+
+
 @pytest.mark.gpu
 def test_of_the_objects_that_calls_make():
     import torch
@@ -38,3 +43,18 @@ def test_of_the_objects_that_calls_make():
     w.scale.view(torch.uint8).add_(1)  # in place: twice the weight
     assert torch.equal(pdq.linear_fp8(x, w)["y"], 2 * y) and torch.equal(pdq.gemm_fp8(q, w)["y"], 2 * y)
     assert type(r) is pdq.Routing and r.ids.shape == (20, 2) and type(q) is pdq.CodesFP8 and q.shape == (20, 256)
+
+
+@pytest.mark.gpu
+def test_of_a_cache_and_its_batch():
+    import torch
+
+    cache = pdq.KVCache.empty(4, 2, 64)
+    batch = pdq.KVBatch(torch.zeros((1, 4), dtype=torch.int32, device="cuda"), torch.ones(1, dtype=torch.int32, device="cuda"))
+    for o, names in ((cache, ("k", "v", "k_scale", "pages", "dim")), (batch, ("page_table", "seq_len", "cu_q", "batch"))):
+        for name in names:
+            with pytest.raises(AttributeError):
+                setattr(o, name, getattr(o, name))
+    x = torch.randn((1, 2, 64), device="cuda").bfloat16()
+    pdq.kv_append(x, x, cache, batch)
+    assert torch.isfinite(pdq.kv_attention(x, cache, batch)["y"]).all()

@@ -630,7 +630,7 @@ class _Fixed:
             object.__setattr__(self, name, value)
 
 
-class KVCache:
+class KVCache(_Fixed):
     """A pool of pages of the INT8 key/value cache (include/pdq.h, pdq_kv_cache).
 
     k [pages, heads, page, dim] and v [pages, heads, page / 4, dim, 4] int8,
@@ -649,11 +649,9 @@ class KVCache:
         _check_dense(v_scale, "v_scale", torch.float32, (pages, heads))
         if not k.device == v.device == k_scale.device == v_scale.device:
             raise ValueError("the cache's tensors must be on one device")
-        self.k, self.v, self.k_scale, self.v_scale = k, v, k_scale, v_scale
-        self.pages, self.heads, self.page, self.dim, self.device = pages, heads, page, dim, k.device
-        self.index = k.get_device()
-        self._c = _KVCacheC(k.data_ptr(), v.data_ptr(), k_scale.data_ptr(), v_scale.data_ptr(), pages, heads, page, dim)
-        self._ref = ctypes.byref(self._c)
+        c = _KVCacheC(k.data_ptr(), v.data_ptr(), k_scale.data_ptr(), v_scale.data_ptr(), pages, heads, page, dim)
+        self._put(k=k, v=v, k_scale=k_scale, v_scale=v_scale, pages=pages, heads=heads, page=page, dim=dim, device=k.device,
+                  index=k.get_device(), _c=c, _ref=ctypes.byref(c))
 
     @classmethod
     def empty(cls, pages: int, heads: int, dim: int, page: int = 64, device="cuda") -> "KVCache":
@@ -663,7 +661,7 @@ class KVCache:
                    torch.empty((pages, heads), dtype=torch.float32, device=device))
 
 
-class KVBatch:
+class KVBatch(_Fixed):
     """The sequences of a call (include/pdq.h, pdq_kv_batch): page_table int32
     [batch, max_pages], seq_len int32 [batch] (the new tokens included), cu_q int32
     [batch + 1] row offsets of the new tokens, or None: one row a sequence.  The
@@ -680,11 +678,10 @@ class KVBatch:
             _check_dense(cu_q, "cu_q", torch.int32, (batch + 1,))
         if page_table.device != seq_len.device or (cu_q is not None and cu_q.device != seq_len.device):
             raise ValueError("the batch's tensors must be on one device")
-        self.page_table, self.seq_len, self.cu_q, self.batch = page_table, seq_len, cu_q, batch
-        self.device, self.index = seq_len.device, seq_len.get_device()
-        self._c = _KVBatchC(page_table.data_ptr(), _ld(page_table), seq_len.data_ptr(),
-                            cu_q.data_ptr() if cu_q is not None else None, batch, max_pages)
-        self._ref = ctypes.byref(self._c)
+        c = _KVBatchC(page_table.data_ptr(), _ld(page_table), seq_len.data_ptr(),
+                      cu_q.data_ptr() if cu_q is not None else None, batch, max_pages)
+        self._put(page_table=page_table, seq_len=seq_len, cu_q=cu_q, batch=batch, device=seq_len.device,
+                  index=seq_len.get_device(), _c=c, _ref=ctypes.byref(c))
 
 
 def _check_kv_rows(t, name, cache, heads=None, dtype=None):
