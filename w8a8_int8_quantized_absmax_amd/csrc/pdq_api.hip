@@ -899,15 +899,20 @@ pdq_status check_stack(int64_t count, int64_t N, int64_t K) {
     return PDQ_OK;
 }
 
+// One product: its operands, and as many outputs as a launch's threads take (tiles of 128 x 256 by 256 of them).
+pdq_status check_fp8_sizes(int64_t M, int64_t N, int64_t K) {
+    PDQ_TRY(check_mk(M, K, K));
+    PDQ_TRY(check_stack(1, N, K));
+    return M * N > std::min(kMaxOutputs, kMaxThreads * 128) ? PDQ_ERR_SHAPE : PDQ_OK;
+}
+
 pdq_status check_fp8_gemm(int64_t M, int64_t K, const uint8_t* wq, const void* w_scale, pdq_scale_type scale_t,
                           const float* bias, int64_t N, const uint8_t* xq, const uint8_t* x_scale, const void* y,
                           pdq_dtype y_dt, int64_t ldy) {
     if (y_dt != PDQ_BF16 && y_dt != PDQ_F16) return PDQ_ERR_DTYPE;
     if (!scale_ok(scale_t)) return PDQ_ERR_DTYPE;
-    PDQ_TRY(check_mk(M, K, K));
-    PDQ_TRY(check_stack(1, N, K));
-    // (kMaxThreads: tiles of 128 x 256 by 256 threads)
-    if (M * N > std::min(kMaxOutputs, kMaxThreads * 128) || ldy < N) return PDQ_ERR_SHAPE;
+    PDQ_TRY(check_fp8_sizes(M, N, K));
+    if (ldy < N) return PDQ_ERR_SHAPE;
     if (N > 0 && (!wq || !w_scale)) return PDQ_ERR_NULL;
     if (M > 0 && (!xq || !x_scale)) return PDQ_ERR_NULL;
     if (M > 0 && N > 0 && !y) return PDQ_ERR_NULL;
@@ -1045,7 +1050,7 @@ pdq_status pdq_quantize_fp8(const void* x, pdq_dtype x_dt, int64_t M, int64_t K,
 }
 
 int pdq_gemm_fp8_tile(int64_t M, int64_t N, int64_t K, pdq_scale_type scale_t) {
-    if (M < 1 || N < 1 || K < 1 || M > kMaxRows || N > kMaxRows || K > kMaxK || !scale_ok(scale_t)) return -1;
+    if (M < 1 || N < 1 || !scale_ok(scale_t) || check_fp8_sizes(M, N, K) != PDQ_OK) return -1;
     return fp8_tile_shape(M, N, fp8_groups(K), scale_t == PDQ_SCALE_F32).rows;
 }
 
