@@ -940,32 +940,50 @@ Fp8GemmArgs fp8_gemm_args(int64_t M, int64_t K, const uint8_t* wq, const void* w
     return a;
 }
 
-// The tile of an FP8 product, 0 rows: the kernel for few rows.  The estimates are in microseconds for G
-// groups, from times measured on MI355X with 64 .. 4096 rows, N 1024 .. 28672 and K 1360 .. 14336; they
-// are within a quarter of those from K = 4096 on.  A round of up to 256 tiles takes as long however many tiles it holds (128 x 128: 512
-// tiles, or 256 for less); the other kernel's goes with its workgroups (64 rows x 32 or 64 channels) by rounds of 256 (400 x
-// 3008 x 4096, 1.3 of them: 23.3 us, 14.2 in tiles; 600 x 2048 x 11008, as many: 40.1, but tiles 51.7).  E.g. K =
-// 4096 (few rows / 128 x 128 / 128 x 256 / 256 x 256): 256 x 4096 12.3 / 14.1 / 21.9 / 38, 512 x 4096 22.6 / 15.5 / 22.5 / 38,
-// 1024 x 4096 40.5 / 18.2 / 24.5 / 39, 128 x 28672 45.6 / 21.7 / 26.2 / 40.5, 2048 x 4096 75 / 35.6 / 29.3 / 41.5, 4096 x 11008 434 /
-// 178 / 163 / 144; 1024 x 14336 -> 4096 109 / 60 / 75 / 112.  Binary32 scales (few rows / 128 x 128 / 128 x 256 / 192 x 256): 1024
-// x 4096 40.8 / 23.5 / 33.0 / 43.9, 2048 x 4096 78 / 36.7 / 37.0 / 46.4, 8192 x 8192 - / 269 / - / 278; 8192 x 14336 -> 4096 - / 543 /
-// - / 506: 128 x 256 is never the best there.
+// The tile of an FP8 product, 0 rows: the kernel for few rows.  The estimates are in microseconds for G groups, from times
+// measured on MI355X, every kernel at 416 sizes (65 .. 65536 rows, N 64 .. 28672, K 16 .. 14336, both types of scales; a part of them with
+// the weights in the last-level cache): what the rule takes is slower than the best by 2% on average.
+// - Few rows: rounds of 256 workgroups (64 rows x 16, 32 or 64 channels), the last one as long as a full one: 600 x 2048 x 11008, 1.3 of
+//   them, 40.9 (128 x 128: 49.5), 512 x 4096 x 11008, two, 47.5 (54.0).  Where the blocks of rows that share a weight's channels
+//   run on different XCDs, each reads the weight: 400 x 3008 x 11008 50.7 (43.3).
+// - 128 x 128: rounds of 512 tiles, two a compute unit, or of 256 for less (1024 x 4096 x 11008 54.9, 2048 x 4096 x 11008 100.8).  The other
+//   tiles: rounds of 256.
+// - Outputs whose rows are no multiple of 8 leave in single stores: 600 x 1003 x 1360 7.1 / 11.5 / 19.1 / 34.1 (few rows / 128 x 128 / 128 x
+//   256 / 256 x 256), 600 x 2048 x 1360 8.2 / 7.7 / 11.1 / 18.4.
+// E.g. K 4096: 200 x 4096 14.1 / 19.0 / 28.1 / 38.3, 1024 x 4096 39.1 / 21.0 / 28.6 / 40.5, 2048 x 4096 74.5 / 38.9 / 32.7 / 46.9, 4096 x
+// 11008 434 / 178 / 163 / 144; one group, 65536 x 4096: 396 / 179 / 187 / 186.  Binary32 scales (few rows / 128 x 128 / 192 x 256): 512 x 4096
+// 23.8 / 21.5 / 42.8, 8192 x 8192 - / 269 / 278, 8192 x 14336 -> 4096 - / 543 / 506; 128 x 256 is never the best there.
 Fp8TileShape fp8_tile_shape(int64_t M, int64_t N, int64_t G, bool f32) {
     if (M <= 64) return Fp8TileShape{0, 0};
-    auto tiles = [&](int64_t rows, int64_t channels) { return ((M + rows - 1) / rows) * ((N + channels - 1) / channels); };
-    auto rounds = [&](int64_t rows) { return (double)((tiles(rows, 256) + 255) / 256); };
+    auto count = [&](int64_t rows, int64_t channels) { return ((M + rows - 1) / rows) * ((N + channels - 1) / channels); };
+    auto ceil256 = [](int64_t n) { return (double)((n + 255) / 256); };
+    // rounds of 256 that take `full`, the last one down to `some` the fewer it has
+    auto rounds = [&](int64_t n, double some, double full) {
+        const int64_t rest = n % 256;
+        return (double)(n / 256) * full + (rest ? some + (full - some) * rest / 256 : 0);
+    };
+    const bool single = N % 8 != 0;
+
     const int width = fp8_rows_width(M, N);
-    const double groups = (double)(((M + 63) / 64) * ((N + 16 * width - 1) / (16 * width)));
-    const double few = 3.5 + G * std::ceil(groups / 256) * (width == 4 ? 0.29 : width == 2 ? 0.22 : 0.16);
-    const double one = f32 ? 3.5 + 0.6 * G : 3 + 0.52 * G, two = f32 ? std::max(one + 0.4 * G, 1.2 * G - 3) : one + 0.5 * G;
-    const int64_t small = tiles(128, 128), rest = small % 512;
-    const double t128 = small * 256 > kMaxThreads ? 1e18 : (double)(small / 512) * two + (rest == 0 ? 0 : rest <= 256 ? one : two);
-    const double t128x256 = rounds(128) * (1.5 + 0.95 * G);  // (f32: not there)
-    const int large = f32 ? 192 : 256;
-    const double tl = rounds(large) * (f32 ? std::max(6 + 1.35 * G, 1.5 * G) : 4 + 1.4 * G);
-    const double best = std::min(t128, f32 ? tl : std::min(tl, t128x256));
+    const int64_t blocks = (N + 16 * width - 1) / (16 * width), groups = (M + 63) / 64 * blocks;
+    const double turns = width == 2 ? std::max(1.0, groups / 128.0 - 1) : ceil256(groups);
+    const double a_group = width == 4 ? (f32 ? 0.13 : 0.11) + 0.195 * turns : width == 2 ? 0.08 + 0.16 * turns : 0.02 + 0.14 * turns;
+    const double few = groups * 512 > kMaxThreads ? 1e18 : (3 + (f32 ? 1.5 : 1.3) * turns + G * a_group) * (blocks % 8 ? 1.15 : 1.0);
+
+    const int64_t small = count(128, 128), rest = small % 512;
+    const double one = f32 ? 3.5 + 0.58 * G : 2.5 + 0.55 * G, two = std::max(5.5 + 0.95 * G, 1.2 * G - 3);
+    const double more = std::min(1.4 * one, two);  // a second tile on some compute units
+    const double last = rest == 0 ? 0 : rest <= 256 ? one : more + (two - more) * (rest - 256) / 256;
+    const double t128 = small * 256 > kMaxThreads ? 1e18 : (double)(small / 512) * two + last + (single ? 3.5 * ceil256(small) : 0);
+
+    const int64_t wide = count(128, 256), most = count(f32 ? 192 : 256, 256);
+    const double t128x256 = f32 ? 1e18 : rounds(wide, 4 + 0.85 * G, 4 + 0.93 * G) + (single ? 8 * ceil256(wide) : 0);
+    const double full = f32 ? std::max(std::max(8.0 + G, 6 + 1.35 * G), 1.5 * G) : std::max(10 + 0.9 * G, 4 + 1.4 * G);
+    const double large = rounds(most, f32 ? 7 + 1.11 * G : 7.5 + 1.02 * G, full) + (single ? (f32 ? 11 : 14) * ceil256(most) : 0);
+
+    const double best = std::min(t128, std::min(t128x256, large));
     if (few <= best) return Fp8TileShape{0, 0};
-    if (best == tl) return Fp8TileShape{large, 256};
+    if (best == large) return Fp8TileShape{f32 ? 192 : 256, 256};
     return best == t128 ? Fp8TileShape{128, 128} : Fp8TileShape{128, 256};
 }
 
