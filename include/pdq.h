@@ -665,7 +665,9 @@ pdq_status pdq_pack_weight_fp8(const uint8_t* codes, const void* scale, pdq_scal
  *   x        [M, K] of x_dt, row pitch ldx
  *   xq       packed codes out, pdq_fp8_bytes(M, K) bytes, 16-byte aligned
  *   x_scale  e8m0 out [M, pdq_fp8_scale_pitch(K)], 4-byte aligned
- *   wq, w_scale (16-byte aligned), scale_t  one matrix of pdq_quantize_weight_fp8 or pdq_pack_weight_fp8
+ *   wq, w_scale (16-byte aligned), scale_t  one matrix of pdq_quantize_weight_fp8 or pdq_pack_weight_fp8; of a
+ *            stack the i-th is at wq + i pdq_fp8_bytes(N, K), its scales at w_scale + i ceil(N / 128)
+ *            pdq_fp8_scale_pitch(K) of them: of e8m0 ones only where that is a multiple of 16 bytes
  *   bias     [N] float or NULL
  *   y        [M, N] of y_dt (BF16 or F16) out, row pitch ldy >= N
  *   workspace  device scratch of at least pdq_linear_fp8_workspace(M, K) bytes (0 for few
