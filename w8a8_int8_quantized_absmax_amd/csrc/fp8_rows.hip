@@ -21,7 +21,7 @@ namespace {
 
 constexpr int kFusedBytes = 20480;  // codes and scales of 16384 values in at most 16 padded rows
 
-template <int NG, int MB, bool F32S, bool FUSED>
+template <int NG, int MB>
 struct Step {  // one group's operands
     v8i w[NG], x[MB];
     uint32_t sx[MB];
@@ -58,7 +58,7 @@ __global__ __launch_bounds__(64 * W) void k_fp8_rows(Fp8GemmArgs a) {
         const v4i hi = *reinterpret_cast<const v4i*>(p + step + half);
         return v8i{lo[0], lo[1], lo[2], lo[3], hi[0], hi[1], hi[2], hi[3]};
     };
-    auto load = [&](Step<NG, MB, F32S, FUSED>& s, int g) {
+    auto load = [&](Step<NG, MB>& s, int g) {
         g = min(g, G - 1);
 #pragma unroll
         for (int i = 0; i < NG; ++i) s.w[i] = frag(wp[i] + (int64_t)g * kGroupBytes, 0, kWBlock);
@@ -72,7 +72,7 @@ __global__ __launch_bounds__(64 * W) void k_fp8_rows(Fp8GemmArgs a) {
         if constexpr (F32S) s.sw = static_cast<const float*>(a.ws)[srow + g];
         else s.swb = static_cast<const uint8_t*>(a.ws)[srow + g];
     };
-    auto load_fused = [&](Step<NG, MB, F32S, FUSED>& s, int g) {
+    auto load_fused = [&](Step<NG, MB>& s, int g) {
         g = min(g, G - 1);
 #pragma unroll
         for (int i = 0; i < MB; ++i) {
@@ -85,7 +85,7 @@ __global__ __launch_bounds__(64 * W) void k_fp8_rows(Fp8GemmArgs a) {
     for (int i = 0; i < NG; ++i)
 #pragma unroll
         for (int j = 0; j < MB; ++j) acc[i][j] = v4f{};
-    auto add = [&](const Step<NG, MB, F32S, FUSED>& s) {
+    auto add = [&](const Step<NG, MB>& s) {
         const Fp8Split sw = F32S ? fp8_split(s.sw) : Fp8Split{};
 #pragma unroll
         for (int i = 0; i < NG; ++i)
@@ -101,7 +101,7 @@ __global__ __launch_bounds__(64 * W) void k_fp8_rows(Fp8GemmArgs a) {
             }
     };
     constexpr int U = 4 / (NG > MB ? NG : MB);  // groups loaded together
-    Step<NG, MB, F32S, FUSED> cur[U], nxt[U];
+    Step<NG, MB> cur[U], nxt[U];
 #pragma unroll
     for (int u = 0; u < U; ++u) load(cur[u], wave + W * u);
     if constexpr (FUSED) {
