@@ -615,9 +615,13 @@ def _check_dense(t, name, dtype, shape=None):
 
 class _Fixed:
     """Objects whose calls go by the addresses and sizes that were checked when they were made: an attribute set afterwards
-    would change neither.  (In place their tensors may change; what makes such an object sets it by _put.)"""
+    would change neither.  (In place their tensors may change; what makes such an object sets it by _put.)  A copy is made
+    of _parts, the constructor's arguments: its addresses are its own."""
 
     __slots__ = ()
+
+    def __reduce__(self):
+        return type(self), self._parts()
 
     def __setattr__(self, name, value):
         raise AttributeError(f"{type(self).__name__}.{name} cannot be set: its calls go by what it was made of; make another")
@@ -653,6 +657,9 @@ class KVCache(_Fixed):
         self._put(k=k, v=v, k_scale=k_scale, v_scale=v_scale, pages=pages, heads=heads, page=page, dim=dim, device=k.device,
                   index=k.get_device(), _c=c, _ref=ctypes.byref(c))
 
+    def _parts(self):
+        return self.k, self.v, self.k_scale, self.v_scale
+
     @classmethod
     def empty(cls, pages: int, heads: int, dim: int, page: int = 64, device="cuda") -> "KVCache":
         return cls(torch.empty((pages, heads, page, dim), dtype=torch.int8, device=device),
@@ -682,6 +689,9 @@ class KVBatch(_Fixed):
                       cu_q.data_ptr() if cu_q is not None else None, batch, max_pages)
         self._put(page_table=page_table, seq_len=seq_len, cu_q=cu_q, batch=batch, device=seq_len.device,
                   index=seq_len.get_device(), _c=c, _ref=ctypes.byref(c))
+
+    def _parts(self):
+        return self.page_table, self.seq_len, self.cu_q
 
 
 def _check_kv_rows(t, name, cache, heads=None, dtype=None):
@@ -879,6 +889,9 @@ class WeightFP8(_Fixed):
                   scale_type=SCALE_F32 if scale.dtype == torch.float32 else E8M0, device=data.device,
                   index=data.get_device(), at=data.data_ptr(), scale_at=scale.data_ptr())
 
+    def _parts(self):
+        return self.data, self.scale, self.n, self.k
+
     @property
     def shape(self):
         return (*self.lead, self.n, self.k)
@@ -911,6 +924,9 @@ class CodesFP8(_Fixed, _CodesFP8Parts):
             raise ValueError(f"packed {rows} x {k} codes with their scales need a contiguous device tensor of "
                              f"{size + rows * pitch} bytes")
         self._put(buffer=buffer, rows=rows, k=k, size=size, pitch=pitch, index=buffer.get_device())
+
+    def _parts(self):
+        return self.buffer, self.rows, self.k
 
     @property
     def shape(self):
@@ -1120,6 +1136,9 @@ class Routing(_Fixed, _RoutingParts):
         if self._c is None:
             self._put(_c=_RoutingC(*self._at, self.tokens, self.experts, self.k))
         return ctypes.byref(self._c)
+
+    def _parts(self):
+        return self._all()
 
     def _all(self):
         if self._tensors is None:  # parts of route_experts' one buffer, as tensors when they are asked for
