@@ -291,7 +291,7 @@ __global__ __launch_bounds__(256, NB == 4 ? 1 : 2) void k_fp8_tile(Fp8TileArgs a
     constexpr int kLag = 4, kRing = 8;
     v4f part_sum[kRing];  // WIDE: [row % 2][channels' block]
     v8bf wide_b[4][4];
-    // Of binary16 rows S_x is 2^-33 to 2^8.  Its codes are widened by 2^16, which its scale lacks then: so no S_x S_w
+    // Of binary16 rows S_x is 2^-32 to 2^8.  Its codes are widened by 2^16, which its scale lacks then: so no S_x S_w
     // passes 2^128 where the sum is 0.
     constexpr uint32_t kWideBy = 16;
     float both[2];
